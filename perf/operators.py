@@ -314,7 +314,7 @@ def power(e):
 def shared_exponent(x):
     """The exponent e of each block with every finite |x| < 1.75 * 2^e."""
     a = torch.where(torch.isfinite(x), x.abs(), 0.0).amax(1, keepdim=True)
-    return (((a.view(torch.int32) + (1 << 21)) >> 23) - 127).clamp(-110, 120)
+    return (((a.view(torch.int32) + (1 << 21)) >> 23) - 127).clamp(-100, 120)
 
 
 def rounded(a, r, lowest, offset, small):
@@ -505,7 +505,7 @@ def exact_eight(x, r, lowest):
     top = a.amax(1, keepdim=True)
     e = torch.floor(torch.log2(torch.where(top > 0, top, 1.0)))
     e = e + (top >= 1.75 * torch.exp2(e))
-    e = torch.where(top > 0, e, -110.0).clamp(-110, 120)
+    e = torch.where(top > 0, e, -100.0).clamp(-100, 120)
     binade = torch.floor(torch.log2(torch.where(a > 0, a, 2.0 ** -600)))
     step = torch.exp2(torch.maximum(binade, e - lowest) - 3)
     return torch.sign(x) * torch.floor(a / step + r.double() / 65536) * step
