@@ -36,7 +36,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(OUT)
     deps = sources() + [os.path.join(SRC, f) for f in os.listdir(SRC) if f.endswith(".cuh")]
-    deps.append(os.path.join(HERE, "..", "include", "nest.h"))
+    deps += [os.path.join(HERE, "..", "include", f) for f in ("nest.h", "nest_train.h")]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(p) > t for p in deps)
 

@@ -1,0 +1,48 @@
+// Shared by the training-step operators (nest_route.cu, nest_optim.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/nest_train.h"
+#include "nest_internal.cuh"
+
+namespace nest {
+
+constexpr int kSMs = 152;   // of a GB300; grids of at most a few blocks for each
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+inline size_t type_bytes(int32_t t) { return t == NEST_F32 ? 4 : 2; }
+inline bool valid_type(int32_t t) { return t == NEST_F32 || t == NEST_BF16 || t == NEST_F16; }
+inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// fn(T{}) with T the element type t (valid_type holds).
+template <typename F>
+int with_type(int32_t t, F fn) {
+    if (t == NEST_F32) return fn(float{});
+    if (t == NEST_BF16) return fn(__nv_bfloat16{});
+    return fn(__half{});
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace nest

@@ -1,0 +1,440 @@
+"""Python binding of the training-step operators in libnest (include/nest_train.h).
+
+The parts of a training step that decide two inputs of the placement solver:
+
+    r = route(logits, k=2)              # gates, chosen experts, counts, balance loss
+    g = route_backward(logits, r, grad_weights, grad_loss)
+    opt = AdamW(weights, grads, state_bits=8)
+    opt.step(lr, grad_scale=opt.grad_norm(max_norm=1.0)[1])
+
+`gate` is `route` as a differentiable function of the logits.  `capacity_milli` turns expert
+counts into the capacity factor of an all-to-all, `AdamW.opt_factor` is the optimizer bytes per
+bf16 weight byte of the solver's instances.
+
+Argument marshalling and checks only: every result is computed by the library's CUDA kernels on
+the caller's stream, and there is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from typing import NamedTuple, Sequence
+
+import numpy as np
+
+from . import nest
+from .nest import NestError
+
+F32, BF16, F16 = 0, 1, 2
+BLOCK = 256   # NEST_OPT_BLOCK
+
+# Every function declared in include/nest_train.h.
+EXPORTS = ("nest_route_workspace_size", "nest_route", "nest_route_backward", "nest_table_query",
+           "nest_table_pack", "nest_grad_norm_workspace_size", "nest_grad_norm", "nest_adamw",
+           "nest_adamw_values")
+
+
+class RouteDesc(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("experts", C.c_int32), ("k", C.c_int32), ("row_stride", C.c_int64),
+                ("col_stride", C.c_int64), ("dtype", C.c_int32), ("normalize", C.c_int32)]
+
+
+class TableInfo(C.Structure):
+    _fields_ = [("table_bytes", C.c_int64), ("blocks", C.c_int64), ("items", C.c_int64), ("tensors", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class AdamWArgs(C.Structure):
+    _fields_ = [("weight_type", C.c_int32), ("grad_type", C.c_int32), ("state_bits", C.c_int32),
+                ("seed", C.c_uint32), ("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
+                ("eps", C.c_double), ("master", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_exp", C.c_void_p), ("v_exp", C.c_void_p), ("state", C.c_void_p), ("grad_scale", C.c_void_p)]
+
+
+TENSOR_DT = np.dtype([("weight", "<u8"), ("grad", "<u8"), ("numel", "<i8"), ("weight_decay", "<f4"),
+                      ("lr_scale", "<f4")])
+STATE_DT = np.dtype([("beta1_t", "<f8"), ("beta2_t", "<f8"), ("step", "<i8"), ("ticket", "<u4"),
+                     ("reserved", "<u4")])
+
+_lib = None
+
+
+def lib():
+    """libnest.so with the operators' signatures; raises if it has not been built."""
+    global _lib
+    if _lib is None:
+        L = nest.lib()
+        P, V = C.POINTER, C.c_void_p
+        L.nest_route_workspace_size.argtypes = [P(RouteDesc)]
+        L.nest_route_workspace_size.restype = C.c_size_t
+        L.nest_route.argtypes = [P(RouteDesc), V, V, V, V, V, V, V, V, V, C.c_size_t, V]
+        L.nest_route_backward.argtypes = [P(RouteDesc), V, V, V, V, V, V, V, V, V, C.c_int64, V]
+        L.nest_table_query.argtypes = [V, C.c_int32, P(TableInfo)]
+        L.nest_table_pack.argtypes = [V, C.c_int32, P(TableInfo), V]
+        L.nest_grad_norm_workspace_size.argtypes = [P(TableInfo)]
+        L.nest_grad_norm_workspace_size.restype = C.c_size_t
+        L.nest_grad_norm.argtypes = [P(TableInfo), V, C.c_int32, C.c_float, V, V, C.c_size_t, V]
+        L.nest_adamw.argtypes = [P(TableInfo), V, P(AdamWArgs), V]
+        L.nest_adamw_values.argtypes = [P(TableInfo), V, V, V, V, V, V, V]
+        _lib = L
+    return _lib
+
+
+def _check(rc: int, what: str):
+    if rc:
+        raise NestError(rc, what)
+
+
+def _type(t, what: str) -> int:
+    import torch
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} is {t.dtype}: float32, bfloat16 and float16 are supported")
+    return code
+
+
+def _want(t, what: str, dtype, shape, device):
+    """t as a contiguous tensor of this type, shape and device, or an error."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
+    return t
+
+
+class _On:
+    """The device of a call made current, and its stream: the device's current one, or the one
+    given, which is made current too (new tensors belong to it) and recorded as a user of `used`."""
+
+    def __init__(self, device, stream, used=()):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"tensors are on {device}: the operators run on CUDA devices only")
+        self.guards = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None and stream != torch.cuda.current_stream(device):
+            self.guards.append(torch.cuda.stream(stream))
+            for t in used:
+                if t is not None:
+                    t.record_stream(stream)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        import torch
+        for g in self.guards:
+            g.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return C.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+# ---------------------------------------------------------------------------------
+# Routing
+# ---------------------------------------------------------------------------------
+
+class Routing(NamedTuple):
+    """What `route` computes (CUDA tensors)."""
+    ids: object         # int32 [T, k] chosen experts, largest logit first, -1 = none
+    weights: object     # float32 [T, k]
+    counts: object      # int32 [E] how often each expert was chosen
+    tokens: object      # int32 [1] rows that count
+    mean_prob: object   # float32 [E]
+    loss: object        # float32 [] balance loss, 1 for an even router
+
+    @staticmethod
+    def empty(tokens: int, experts: int, k: int, device="cuda") -> "Routing":
+        """Uninitialised result buffers, for `route(..., out=)`."""
+        import torch
+        i, f = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+        return Routing(torch.empty((tokens, k), **i), torch.empty((tokens, k), **f), torch.empty(experts, **i),
+                       torch.empty(1, **i), torch.empty(experts, **f), torch.empty((), **f))
+
+
+def _route_desc(logits, k: int, normalize: bool) -> RouteDesc:
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [tokens, experts], not of shape {tuple(logits.shape)}")
+    T, E = logits.shape
+    return RouteDesc(T, E, k, logits.stride(0), logits.stride(1), _type(logits, "logits"), int(bool(normalize)))
+
+
+def _mask_ptr(mask, logits):
+    import torch
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"mask is {mask.dtype}: bool and uint8 are supported")
+    return _want(mask, "mask", mask.dtype, logits.shape[:1], logits.device).data_ptr()
+
+
+def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None = None, stream=None) -> Routing:
+    """nest_route: softmax gates of the k best experts per token, counts and balance loss.
+
+    logits [T, E] (any strides; float32, bfloat16 or float16); mask [T] (bool or uint8, True = the
+    token counts); normalize: gates of a token sum to 1.  out: buffers to write instead of new ones."""
+    import torch
+    d = _route_desc(logits, k, normalize)
+    L = lib()
+    ws_bytes = L.nest_route_workspace_size(C.byref(d))
+    if not ws_bytes:   # the call says which limit is broken
+        _check(L.nest_route(C.byref(d), None, None, None, None, None, None, None, None, None, 0, None), "nest_route")
+    T, E, dev = logits.shape[0], logits.shape[1], logits.device
+    with _On(dev, stream, (logits, mask) + tuple(out or ())) as s:
+        if out is None:
+            out = Routing.empty(T, E, k, dev)
+        else:
+            _want(out.ids, "out.ids", torch.int32, (T, k), dev)
+            _want(out.weights, "out.weights", torch.float32, (T, k), dev)
+            _want(out.counts, "out.counts", torch.int32, (E,), dev)
+            _want(out.tokens, "out.tokens", torch.int32, (1,), dev)
+            _want(out.mean_prob, "out.mean_prob", torch.float32, (E,), dev)
+            _want(out.loss, "out.loss", torch.float32, (), dev)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        rc = L.nest_route(C.byref(d), logits.data_ptr(), _mask_ptr(mask, logits), out.ids.data_ptr(),
+                          out.weights.data_ptr(), out.counts.data_ptr(), out.tokens.data_ptr(),
+                          out.mean_prob.data_ptr(), out.loss.data_ptr(), ws.data_ptr(), ws_bytes, s)
+    _check(rc, "nest_route")
+    return out
+
+
+def route_backward(logits, routing: Routing, grad_weights=None, grad_loss=None, mask=None, normalize: bool = True,
+                   out=None, stream=None):
+    """nest_route_backward: gradient with respect to the logits, in their type, from the gradients
+    of the weights (float32 [T, k]) and of the loss (float32 scalar tensor); None counts as zero.
+    routing, mask and normalize as in the forward call."""
+    import torch
+    T, E = logits.shape if logits.dim() == 2 else (0, 0)
+    dev = logits.device
+    d = _route_desc(logits, routing.ids.shape[-1], normalize)
+    if T:   # an empty batch reads none of them
+        _want(routing.ids, "routing.ids", torch.int32, (T, d.k), dev)
+        _want(routing.weights, "routing.weights", torch.float32, (T, d.k), dev)
+        _want(routing.counts, "routing.counts", torch.int32, (E,), dev)
+        _want(routing.tokens, "routing.tokens", torch.int32, (1,), dev)
+    if grad_weights is not None:
+        _want(grad_weights, "grad_weights", torch.float32, (T, d.k), dev)
+    if grad_loss is not None:
+        _want(grad_loss, "grad_loss", torch.float32, grad_loss.shape, dev)
+        if grad_loss.numel() != 1:
+            raise ValueError(f"grad_loss must be one number, not of shape {tuple(grad_loss.shape)}")
+    used = (logits, mask, routing.ids, routing.weights, routing.counts, routing.tokens, grad_weights, grad_loss, out)
+    with _On(dev, stream, used) as s:
+        if out is None:
+            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        elif out.dtype != logits.dtype or tuple(out.shape) != (T, E) or out.device != dev or \
+                (E > 1 and out.stride(1) != 1) or (T > 1 and out.stride(0) < E):
+            raise ValueError(f"out must be a {logits.dtype} tensor of shape {(T, E)} on {dev} with rows of its own")
+        rc = lib().nest_route_backward(
+            C.byref(d), logits.data_ptr(), _mask_ptr(mask, logits), routing.ids.data_ptr(),
+            routing.weights.data_ptr(), routing.counts.data_ptr(), routing.tokens.data_ptr(),
+            grad_weights.data_ptr() if grad_weights is not None else None,
+            grad_loss.data_ptr() if grad_loss is not None else None,
+            out.data_ptr(), max(out.stride(0), E), s)
+    _check(rc, "nest_route_backward")
+    return out
+
+
+def _gate_function():
+    import torch
+
+    class Gate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, k, mask, normalize):
+            r = route(logits, k, mask=mask, normalize=normalize)
+            ctx.save_for_backward(logits, mask, *r)
+            ctx.normalize = normalize
+            ctx.mark_non_differentiable(r.ids, r.counts, r.tokens, r.mean_prob)
+            return tuple(r)
+
+        @staticmethod
+        def backward(ctx, _ids, grad_weights, _counts, _tokens, _mean, grad_loss):
+            logits, mask, *r = ctx.saved_tensors
+            return (route_backward(logits, Routing(*r), grad_weights.contiguous(), grad_loss.contiguous(), mask=mask,
+                                   normalize=ctx.normalize), None, None, None)
+
+    return Gate
+
+
+_gate = None
+
+
+def gate(logits, k: int, mask=None, normalize: bool = True) -> Routing:
+    """`route` with gradients: the result's weights and loss are differentiable in the logits (the
+    counts are constants of the gradient; mean_prob carries none)."""
+    global _gate
+    if _gate is None:
+        _gate = _gate_function()
+    return Routing(*_gate.apply(logits, k, mask, normalize))
+
+
+def capacity_milli(counts, tokens: int, k: int) -> int:
+    """Capacity factor in thousandths, rounded up, that a layer's all-to-all needs for these expert
+    counts: the fullest expert's share over the even share, at least 1000 (even).  counts: integers
+    on the host."""
+    c = np.asarray(counts, dtype=np.int64)
+    if not tokens or not k or not c.size:
+        return 1000
+    return max(1000, -(-int(c.max()) * c.size * 1000 // (int(tokens) * k)))
+
+
+# ---------------------------------------------------------------------------------
+# Lists of tensors
+# ---------------------------------------------------------------------------------
+
+class _Table:
+    """The packed table of a list of tensors, on their device."""
+
+    def __init__(self, grads, weights=None, weight_decay=0.0, lr_scale=1.0):
+        import torch
+        if not grads:
+            raise ValueError("an empty list of tensors")
+        n, self.device = len(grads), grads[0].device
+        if self.device.type != "cuda":
+            raise ValueError(f"tensors are on {self.device}: the operators run on CUDA devices only")
+        self.keep = (list(grads), list(weights or ()))
+        rec = np.zeros(n, TENSOR_DT)
+        for what, ts in (("grads", grads), ("weights", weights)):
+            if ts is None:
+                continue
+            if len(ts) != n:
+                raise ValueError(f"{len(ts)} {what} for {n} tensors")
+            for i, t in enumerate(ts):
+                if t.dtype != ts[0].dtype or t.device != self.device or not t.is_contiguous() or \
+                        t.numel() != grads[i].numel():
+                    raise ValueError(f"{what}[{i}] must be a contiguous {ts[0].dtype} tensor of {grads[i].numel()} "
+                                     f"elements on {self.device}")
+                rec["grad" if what == "grads" else "weight"][i] = t.data_ptr()
+        rec["numel"] = [t.numel() for t in grads]
+        rec["weight_decay"], rec["lr_scale"] = weight_decay, lr_scale
+        if weights is not None:
+            at = np.argsort(rec["weight"], kind="stable")
+            at = at[rec["numel"][at] > 0]
+            start = rec["weight"][at].astype(np.int64)
+            if (start[:-1] + rec["numel"][at][:-1] * weights[0].element_size() > start[1:]).any():
+                raise ValueError("weights overlap")
+        self.grad_type = _type(grads[0], "grads")
+        self.info = TableInfo()
+        host = np.ascontiguousarray(rec)
+        _check(lib().nest_table_query(host.ctypes.data, n, C.byref(self.info)), "nest_table_query")
+        packed = np.zeros(self.info.table_bytes, np.uint8)
+        _check(lib().nest_table_pack(host.ctypes.data, n, C.byref(self.info), packed.ctypes.data), "nest_table_pack")
+        self.table = torch.from_numpy(packed).to(self.device)
+        ws = lib().nest_grad_norm_workspace_size(C.byref(self.info))
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
+        self.out = torch.empty(2, dtype=torch.float32, device=self.device)
+
+    def norm(self, max_norm, stream):
+        with _On(self.device, stream) as s:
+            rc = lib().nest_grad_norm(C.byref(self.info), self.table.data_ptr(), self.grad_type, max_norm,
+                                      self.out.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(), s)
+        _check(rc, "nest_grad_norm")
+        return self.out
+
+
+class GradNorm:
+    """nest_grad_norm over a list of contiguous CUDA tensors of one type, bound by reference: the
+    tensors' storage is read by every `run`."""
+
+    def __init__(self, grads: Sequence):
+        self._table = _Table(grads)
+
+    def run(self, max_norm: float = math.inf, stream=None):
+        """float32 [2]: the global norm, and min(1, max_norm / (norm + 1e-6)), NaN when the norm is
+        not finite.  The same buffer every call; calls that overlap on the GPU race on it."""
+        return self._table.norm(max_norm, stream)
+
+
+class AdamW:
+    """nest_adamw over a list of tensors, bound by reference.
+
+    weights, grads: lists of contiguous CUDA tensors, each list of one type (float32, bfloat16 or
+    float16); the step reads the gradients and updates the weights in place.  The object owns the
+    float32 master weights (weights of 16 bits only), the moments m and v (state_bits 32: float32;
+    8: uint8 codes with the scales m_exp and v_exp) and the device's step count.  Buffers hold
+    the tensors in order, each from a multiple of 256 elements on (`starts`).  weight_decay and
+    lr_scale: one number, or one per tensor."""
+
+    def __init__(self, weights: Sequence, grads: Sequence, state_bits: int = 32, betas=(0.9, 0.999),
+                 eps: float = 1e-8, weight_decay=0.01, lr_scale=1.0, seed: int = 0):
+        import torch
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits is {state_bits}: 8 and 32 are supported")
+        self._table = tb = _Table(grads, weights, weight_decay, lr_scale)
+        self.weights, self.grads, self.state_bits, self.betas = list(weights), list(grads), state_bits, tuple(betas)
+        dev, n = tb.device, tb.info.blocks * BLOCK
+        sizes = [-(-t.numel() // BLOCK) * BLOCK for t in weights]
+        self.starts = [0] + np.cumsum(sizes, dtype=np.int64)[:-1].tolist()
+        kind = dict(dtype=torch.float32 if state_bits == 32 else torch.uint8, device=dev)
+        self.m, self.v = torch.zeros(n, **kind), torch.zeros(n, **kind)
+        self.m_exp = self.v_exp = self.master = None
+        if state_bits == 8:
+            self.m_exp, self.v_exp = (torch.full((n // BLOCK,), -100, dtype=torch.int8, device=dev) for _ in "mv")
+        weight_type = _type(weights[0], "weights")
+        if weight_type != F32:
+            self.master = torch.zeros(n, dtype=torch.float32, device=dev)
+            for t, a in zip(weights, self.starts):
+                self.master[a:a + t.numel()] = t.reshape(-1)
+        self._state = torch.zeros(STATE_DT.itemsize, dtype=torch.uint8, device=dev)
+
+        def ptr(t):
+            return t.data_ptr() if t is not None else None
+        self._args = AdamWArgs(weight_type, tb.grad_type, state_bits, seed & 0xFFFFFFFF, 0.0, betas[0], betas[1], eps,
+                               ptr(self.master), ptr(self.m), ptr(self.v), ptr(self.m_exp), ptr(self.v_exp),
+                               self._state.data_ptr(), None)
+        self.set_step(0)
+
+    def set_step(self, step: int):
+        """Set the number of steps taken (synchronises; 0 at the start)."""
+        import torch
+        rec = np.zeros(1, STATE_DT)
+        rec["beta1_t"], rec["beta2_t"], rec["step"] = self.betas[0] ** step, self.betas[1] ** step, step
+        self._state.copy_(torch.from_numpy(rec.view(np.uint8)))
+
+    @property
+    def steps(self) -> int:
+        """Steps taken (reads the device)."""
+        return int(self._state.cpu().numpy().view(STATE_DT)["step"][0])
+
+    @property
+    def opt_factor(self) -> int:
+        """Optimizer-state bytes per bf16 weight byte, rounded down to the solver's whole number: 6
+        for a float32 master and two float32 moments, 3 with 8-bit moments, whose scales are a
+        further 1/256 of the bf16 weight bytes."""
+        per = 2 * self.state_bits // 8 + (4 if self.master is not None else 0)
+        return per // 2
+
+    def grad_norm(self, max_norm: float = math.inf, stream=None):
+        """Norm and clip scale of the gradients, as `GradNorm.run`."""
+        return self._table.norm(max_norm, stream)
+
+    def step(self, lr: float, grad_scale=None, stream=None):
+        """One step.  grad_scale: float32 CUDA scalar that multiplies the gradients (entry 1 of
+        `grad_norm`); when it is not finite the call changes nothing."""
+        import torch
+        a, tb = self._args, self._table
+        if grad_scale is None:
+            a.grad_scale = None
+        else:
+            if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.device != tb.device:
+                raise ValueError(f"grad_scale must be one float32 number on {tb.device}")
+            a.grad_scale = grad_scale.data_ptr()
+        a.lr = lr
+        with _On(tb.device, stream, () if grad_scale is None else (grad_scale,)) as s:
+            rc = lib().nest_adamw(C.byref(tb.info), tb.table.data_ptr(), C.byref(a), s)
+        _check(rc, "nest_adamw")
+
+    def state_values(self, stream=None):
+        """(m, v): the moments, laid out like the object's buffers.  With 8-bit states new bfloat16
+        tensors with the exact values of the codes, else the float32 buffers themselves."""
+        import torch
+        if self.state_bits == 32:
+            return self.m, self.v
+        tb = self._table
+        with _On(tb.device, stream, (self.m, self.v, self.m_exp, self.v_exp)) as s:
+            m, v = (torch.empty(self.m.numel(), dtype=torch.bfloat16, device=tb.device) for _ in "mv")
+            rc = lib().nest_adamw_values(C.byref(tb.info), self.m.data_ptr(), self.v.data_ptr(),
+                                         self.m_exp.data_ptr(), self.v_exp.data_ptr(), m.data_ptr(), v.data_ptr(), s)
+        _check(rc, "nest_adamw_values")
+        return m, v
