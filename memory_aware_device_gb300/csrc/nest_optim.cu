@@ -17,7 +17,6 @@ constexpr int kBlock = NEST_OPT_BLOCK;
 constexpr int kItemBlocks = 16;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kPerLane = kBlock / 32;
 
 struct Entry {            // one tensor
     void *weight;
@@ -38,11 +37,82 @@ __device__ __forceinline__ const Item *items_of(const void *table, int tensors) 
 
 int64_t blocks_in(int64_t numel) { return (numel + kBlock - 1) / kBlock; }
 
+// A lane's share of a block: elements 8 lane .. 8 lane + 7, in one load of 32 bytes (or 16).
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
+    static_assert(sizeof(T) == 2, "16-bit type");
+    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+    const T *h = reinterpret_cast<const T *>(&q);
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = to_f32(h[i]);
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :
+                 : "l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
+    static_assert(sizeof(T) == 2, "16-bit type");
+    uint4 q;
+    T *h = reinterpret_cast<T *>(&q);
+#pragma unroll
+    for (int i = 0; i < 8; i++) h[i] = from_f32<T>(x[i]);
+    *reinterpret_cast<uint4 *>(p) = q;
+}
+
+template <typename T>
+__device__ __forceinline__ bool wide(const T *p) {   // every block of the tensor can be loaded by load8
+    return (reinterpret_cast<uintptr_t>(p) & (8 * sizeof(T) - 1)) == 0;
+}
+
+// The lane's share of the block that starts at p[0], of which `n` elements (1 to 256) exist; the
+// others are 0.  A tensor that does not start at a multiple of 8 elements, and a tensor's last
+// block, go through the warp's shared memory: 32 neighbours at a time between it and the tensor.
+template <typename T>
+__device__ __forceinline__ void load_block(const T *p, int n, bool vector, int lane, float *room, float (&x)[8]) {
+    if (vector && n >= kBlock) {
+        load8(p + 8 * lane, x);
+        return;
+    }
+    T part[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) part[i] = lane + 32 * i < n ? p[lane + 32 * i] : from_f32<T>(0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; i++) room[lane + 32 * i] = to_f32(part[i]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = room[8 * lane + i];
+    __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ void store_block(T *p, int n, bool vector, int lane, float *room, const float (&x)[8]) {
+    if (vector && n >= kBlock) {
+        store8(p + 8 * lane, x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) room[8 * lane + i] = x[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        if (lane + 32 * i < n) p[lane + 32 * i] = from_f32<T>(room[lane + 32 * i]);
+    __syncwarp();
+}
+
 // ---- gradient norm ----------------------------------------------------------------
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const void *table, int tensors, int items, double *part) {
     __shared__ double sh[kWarps];
+    __shared__ __align__(16) float room[kWarps][kBlock];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -51,17 +121,19 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const void *table, int t
     double sum = 0.0;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
         const Item item = list[it];
-        const Entry e = entries[item.tensor];
-        const T *g = static_cast<const T *>(e.grad);
+        const T *g = static_cast<const T *>(entries[item.tensor].grad);
+        const int64_t numel = entries[item.tensor].numel;
+        const bool vector = wide(g);
         float s = 0.0f;
-        for (int b = item.block + warp; b < item.block + kItemBlocks; b += kWarps)
-            for (int i = 0; i < kPerLane; i++) {
-                const int64_t j = int64_t(b) * kBlock + lane + 32 * i;
-                if (j < e.numel) {
-                    const float x = to_f32(g[j]);
-                    s = fmaf(x, x, s);
-                }
-            }
+#pragma unroll
+        for (int b = 0; b < kItemBlocks; b += kWarps) {
+            const int64_t at = int64_t(item.block + b + warp) * kBlock, left = numel - at;
+            if (left <= 0) break;
+            float x[8];
+            load_block(g + at, int(left < kBlock ? left : kBlock), vector, lane, room[warp], x);
+#pragma unroll
+            for (int i = 0; i < 8; i++) s = fmaf(x[i], x[i], s);
+        }
         sum += s;
     }
     sum = warp_sum(sum);
@@ -74,13 +146,19 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const void *table, int t
     }
 }
 
-__global__ void __launch_bounds__(32) norm_finish_kernel(const double *part, int blocks, float max_norm, float *out) {
+__global__ void __launch_bounds__(kThreads) norm_finish_kernel(const double *part, int blocks, float max_norm,
+                                                               float *out) {
+    __shared__ double sh[kWarps];
     pdl_wait();
     pdl_trigger();
     double s = 0.0;
-    for (int b = threadIdx.x; b < blocks; b += 32) s += part[b];
+    for (int b = threadIdx.x; b < blocks; b += kThreads) s += part[b];
     s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+    __syncthreads();
     if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int w = 0; w < kWarps; w++) s += sh[w];
         const float norm = float(sqrt(s));
         out[0] = norm;
         out[1] = isfinite(norm) ? fminf(1.0f, max_norm / (norm + 1e-6f)) : NAN;
@@ -112,35 +190,69 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
 
 // Code of y >= 0 with 3 mantissa bits: 16 bits of noise r are added under the last bit
 // kept and the rest is cut off.  Exponent field f of a normal code stands for the 32-bit
-// exponent field offset + f; under the smallest normal value the code counts steps of 1 / small.
+// exponent field OFFSET + f; under the smallest normal value the code counts steps of
+// 1 / small, whose fraction is cut to 16 bits by adding 128 (one unit in the last place of a
+// number there is 2^-16) and summed with the noise as an integer.
 template <int OFFSET>
 __device__ __forceinline__ uint32_t code_of(float y, uint32_t r, float small) {
-    const uint32_t normal = ((__float_as_uint(y) + (r << 4)) >> 20) - (OFFSET << 3);
-    const uint32_t fixed = uint32_t(fmaf(y, small, float(r) * 0x1p-16f));
+    const uint32_t normal = (__float_as_uint(y) + (r << 4) - (uint32_t(OFFSET) << 23)) >> 20;
+    const uint32_t fixed = (__float_as_uint(__fmaf_rz(y, small, 128.0f)) + r - 0x43000000u) >> 16;
     return __float_as_uint(y) < (uint32_t(OFFSET + 1) << 23) ? fixed : normal;
 }
 
-__device__ __forceinline__ uint8_t encode_m(float m, int s, uint32_t r) {
-    const uint32_t sign = (__float_as_uint(m) >> 24) & 0x80u;
-    uint32_t c = min(code_of<120>(fabsf(m) * power2(8 - s), r, 512.0f), 0x7Eu);
-    if (!isfinite(m)) c = 0x7F;
-    return uint8_t(c | sign);
+// Codes of a lane's eight moments.  rare: the block holds one that is not finite, or whose scale
+// is clipped, and codes are checked against the largest.
+__device__ __forceinline__ uint2 encode_m(const float (&m)[8], int s, const uint32_t (&noise)[8], bool rare) {
+    const float f = power2(8 - s);
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        c[i] = code_of<120>(fabsf(m[i]) * f, noise[i] >> 16, 512.0f);
+        if (rare) c[i] = isfinite(m[i]) ? min(c[i], 0x7Eu) : 0x7Fu;
+        c[i] |= (__float_as_uint(m[i]) >> 24) & 0x80u;
+    }
+    return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
 }
 
-__device__ __forceinline__ uint8_t encode_v(float v, int s, uint32_t r) {
-    const uint32_t c = min(code_of<95>(v * power2(-1 - s), r, 0x1p34f), 0xFEu);
-    return uint8_t(isfinite(v) ? c : 0xFFu);
+__device__ __forceinline__ uint2 encode_v(const float (&v)[8], int s, const uint32_t (&noise)[8], bool rare) {
+    const float f = power2(-1 - s);
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        c[i] = code_of<95>(v[i] * f, noise[i] & 0xFFFFu, 0x1p34f);
+        if (rare) c[i] = isfinite(v[i]) ? min(c[i], 0xFEu) : 0xFFu;
+    }
+    return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
 }
 
-__device__ __forceinline__ float decode_m(uint32_t c, int s) {
-    // the code's 7 lower bits as a 32-bit float with the exponent 120 too small
-    const float y = __uint_as_float((c & 0x7Fu) << 20) * 0x1p120f * power2(s - 8);
-    return (c & 0x7Fu) == 0x7Fu ? NAN : (c & 0x80u) ? -y : y;
+// Two codes with 4 exponent bits as two floats: the hardware's e4m3 conversion (0x7F is NaN there too).
+__device__ __forceinline__ float2 pair_of(uint16_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-__device__ __forceinline__ float decode_v(uint32_t c, int s) {
-    const float y = __uint_as_float(c << 20) * 0x1p95f * power2(s + 1);
-    return c == 0xFFu ? NAN : y;
+__device__ __forceinline__ void decode_m(uint2 c, int s, float (&m)[8]) {
+    const float f = power2(s - 8);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 y = pair_of(uint16_t((i < 2 ? c.x : c.y) >> (16 * (i & 1))));
+        m[2 * i] = y.x * f;
+        m[2 * i + 1] = y.y * f;
+    }
+}
+
+// A code's bits as a 32-bit float are its value with the exponent 95 too small, subnormal codes included.
+__device__ __forceinline__ void decode_v(uint2 c, int s, float (&v)[8]) {
+    const float f = power2(s + 1);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        v[i] = __uint_as_float(((i < 4 ? c.x : c.y) >> (8 * (i & 3)) & 0xFFu) << 20) * 0x1p95f * f;
+    if (__vcmpeq4(c.x, 0xFFFFFFFFu) | __vcmpeq4(c.y, 0xFFFFFFFFu)) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (((i < 4 ? c.x : c.y) >> (8 * (i & 3)) & 0xFFu) == 0xFFu) v[i] = NAN;
+    }
 }
 
 // ---- AdamW --------------------------------------------------------------------------
@@ -158,9 +270,39 @@ struct StepArgs {
     const float *grad_scale;
 };
 
+__device__ __forceinline__ float root_of(float x) {   // relative error 2^-23
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The lane's share of a block of the list's own buffers; past the tensor's end nothing is written.
+__device__ __forceinline__ void store_own(float *p, int n, int lane, const float (&x)[8]) {
+    if (8 * lane + 8 <= n) {
+        store8(p + 8 * lane, x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        if (8 * lane + i < n) p[8 * lane + i] = x[i];
+}
+__device__ __forceinline__ void store_own(uint8_t *p, int n, int lane, uint2 c) {
+    if (8 * lane + 8 <= n) {
+        *reinterpret_cast<uint2 *>(p + 8 * lane) = c;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        if (8 * lane + i < n) p[8 * lane + i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+}
+
+// Magnitudes (as bits) from which a block's codes take the checked path: 1.75 * 2^120, infinity, NaN.
+constexpr uint32_t kRare = (uint32_t(120 + 127) << 23) | 0x600000u;
+
 template <typename W, typename G, bool EIGHT>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
     constexpr bool kOwnMaster = sizeof(W) == 4;
+    __shared__ __align__(16) float room[kWarps][kBlock];
     pdl_wait();
     pdl_trigger();
     const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
@@ -175,71 +317,82 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
     for (int it = blockIdx.x; it < a.items; it += gridDim.x) {
         const Item item = list[it];
         const Entry e = entries[item.tensor];
+        W *weight = static_cast<W *>(e.weight);
+        const G *grad = static_cast<const G *>(e.grad);
+        const bool wide_w = wide(weight), wide_g = wide(grad);
         const float lr = a.lr * e.lr_scale, decay = e.weight_decay;
         for (int b = item.block + warp; b < item.block + kItemBlocks; b += kWarps) {
-            const int64_t j0 = int64_t(b) * kBlock;
-            if (j0 >= e.numel) break;
-            const int64_t block = e.first + b;
-            int sm = 0, sv = 0;
+            const int64_t j0 = int64_t(b) * kBlock, left = e.numel - j0;
+            if (left <= 0) break;
+            const int n = int(left < kBlock ? left : kBlock);
+            const int64_t block = e.first + b, at = block * kBlock;
+            float g[8], m[8], v[8], p[8];
+            load_block(grad + j0, n, wide_g, lane, room[warp], g);
+            if constexpr (kOwnMaster)
+                load_block(weight + j0, n, wide_w, lane, room[warp], p);
+            else
+                load8(a.master + at + 8 * lane, p);   // the list's own buffers hold whole blocks
             if constexpr (EIGHT) {
-                sm = a.m_exp[block];
-                sv = a.v_exp[block];
+                const uint2 cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.m) + at + 8 * lane);
+                const uint2 cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.v) + at + 8 * lane);
+                decode_m(cm, a.m_exp[block], m);
+                decode_v(cv, a.v_exp[block], v);
+            } else {
+                load8(static_cast<const float *>(a.m) + at + 8 * lane, m);
+                load8(static_cast<const float *>(a.v) + at + 8 * lane, v);
             }
-            float m[kPerLane], v[kPerLane];
             uint32_t top_m = 0, top_v = 0;
 #pragma unroll
-            for (int i = 0; i < kPerLane; i++) {
-                const int pos = lane + 32 * i;
-                const int64_t at = block * kBlock + pos;
-                m[i] = v[i] = 0.0f;
-                if (j0 + pos < e.numel) {
-                    const float g = to_f32(static_cast<const G *>(e.grad)[j0 + pos]) * scale;
-                    if constexpr (EIGHT) {
-                        m[i] = decode_m(static_cast<const uint8_t *>(a.m)[at], sm);
-                        v[i] = decode_v(static_cast<const uint8_t *>(a.v)[at], sv);
-                    } else {
-                        m[i] = static_cast<const float *>(a.m)[at];
-                        v[i] = static_cast<const float *>(a.v)[at];
-                    }
-                    // each product rounded by itself, so that a moment is the same number
-                    // wherever these formulas are evaluated, and its 8-bit code with it
-                    m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(g, a.rest1));
-                    v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(g, g), a.rest2));
-                    W *w = static_cast<W *>(e.weight) + j0 + pos;
-                    float p = kOwnMaster ? to_f32(*w) : a.master[at];
-                    p -= lr * (m[i] * inv1 / (sqrtf(v[i]) * root2 + a.eps) + decay * p);
-                    if (!kOwnMaster) a.master[at] = p;
-                    *w = from_f32<W>(p);
-                    if constexpr (EIGHT) {
-                        top_m = max(top_m, finite_bits(m[i]));
-                        top_v = max(top_v, finite_bits(v[i]));
-                    } else {
-                        static_cast<float *>(a.m)[at] = m[i];
-                        static_cast<float *>(a.v)[at] = v[i];
-                    }
+            for (int i = 0; i < 8; i++) {
+                const float x = g[i] * scale;
+                // each product rounded by itself, so that a moment is the same number wherever
+                // these formulas are evaluated, and its 8-bit code with it
+                m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(x, a.rest1));
+                v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(x, x), a.rest2));
+                p[i] -= lr * (__fdividef(m[i] * inv1, fmaf(root_of(v[i]), root2, a.eps)) + decay * p[i]);
+                if (EIGHT && 8 * lane + i < n) {
+                    top_m = max(top_m, __float_as_uint(m[i]) & 0x7fffffffu);
+                    top_v = max(top_v, __float_as_uint(v[i]) & 0x7fffffffu);
                 }
             }
+            store_block(weight + j0, n, wide_w, lane, room[warp], p);
+            if constexpr (!kOwnMaster) store_own(a.master + at, n, lane, p);
             if constexpr (EIGHT) {
-                sm = shared_exponent(__reduce_max_sync(0xffffffffu, top_m));
-                sv = shared_exponent(__reduce_max_sync(0xffffffffu, top_v));
-                const uint32_t noise = mixed(start + uint32_t(block) * 0x9E3779B1u);
+                top_m = __reduce_max_sync(0xffffffffu, top_m);
+                top_v = __reduce_max_sync(0xffffffffu, top_v);
+                const bool rare = max(top_m, top_v) >= kRare;
+                if (rare) {   // the largest finite magnitudes
+                    top_m = top_v = 0;
 #pragma unroll
-                for (int i = 0; i < kPerLane; i++) {
-                    const int pos = lane + 32 * i;
-                    uint32_t x = noise + uint32_t(pos) * 0x9E3779B1u;
+                    for (int i = 0; i < 8; i++)
+                        if (8 * lane + i < n) {
+                            top_m = max(top_m, finite_bits(m[i]));
+                            top_v = max(top_v, finite_bits(v[i]));
+                        }
+                    top_m = __reduce_max_sync(0xffffffffu, top_m);
+                    top_v = __reduce_max_sync(0xffffffffu, top_v);
+                }
+                const int sm = shared_exponent(top_m), sv = shared_exponent(top_v);
+                uint32_t noise[8];
+                const uint32_t word = mixed(start + uint32_t(block) * 0x9E3779B1u);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    uint32_t x = word + uint32_t(8 * lane + i) * 0x9E3779B1u;
                     x ^= x >> 15;
                     x *= 0x6A09E667u;
-                    x ^= x >> 16;
-                    if (j0 + pos < e.numel) {
-                        const int64_t at = block * kBlock + pos;
-                        static_cast<uint8_t *>(a.m)[at] = encode_m(m[i], sm, x >> 16);
-                        static_cast<uint8_t *>(a.v)[at] = encode_v(v[i], sv, x & 0xFFFFu);
-                    }
+                    noise[i] = x ^ (x >> 16);
                 }
+                store_own(static_cast<uint8_t *>(a.m) + at, n, lane,
+                          rare ? encode_m(m, sm, noise, true) : encode_m(m, sm, noise, false));
+                store_own(static_cast<uint8_t *>(a.v) + at, n, lane,
+                          rare ? encode_v(v, sv, noise, true) : encode_v(v, sv, noise, false));
                 if (lane == 0) {
                     a.m_exp[block] = int8_t(sm);
                     a.v_exp[block] = int8_t(sv);
                 }
+            } else {
+                store_own(static_cast<float *>(a.m) + at, n, lane, m);
+                store_own(static_cast<float *>(a.v) + at, n, lane, v);
             }
         }
     }
@@ -261,10 +414,15 @@ __global__ void __launch_bounds__(kThreads) values_kernel(int64_t blocks, const 
                                                           __nv_bfloat16 *m_out, __nv_bfloat16 *v_out) {
     pdl_wait();
     pdl_trigger();
-    for (int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x; at < blocks * kBlock;
-         at += int64_t(gridDim.x) * kThreads) {
-        m_out[at] = __float2bfloat16_rn(decode_m(m[at], m_exp[at / kBlock]));
-        v_out[at] = __float2bfloat16_rn(decode_v(v[at], v_exp[at / kBlock]));
+    const int lane = threadIdx.x & 31;
+    for (int64_t b = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5; b < blocks; b += int64_t(gridDim.x) * kWarps) {
+        const int64_t at = b * kBlock + 8 * lane;
+        const uint2 cm = *reinterpret_cast<const uint2 *>(m + at), cv = *reinterpret_cast<const uint2 *>(v + at);
+        float x[8];
+        decode_m(cm, m_exp[b], x);
+        store8(m_out + at, x);
+        decode_v(cv, v_exp[b], x);
+        store8(v_out + at, x);
     }
 }
 
@@ -345,7 +503,7 @@ int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_
                              int(info->tensors), int(info->items), part);
     });
     if (rc) return rc;
-    return launch_kernel(norm_finish_kernel, dim3(1), dim3(32), 0, stream, 1, "norm finish launch",
+    return launch_kernel(norm_finish_kernel, dim3(1), dim3(kThreads), 0, stream, 1, "norm finish launch",
                          static_cast<const double *>(part), blocks, max_norm, out);
 }
 
@@ -387,7 +545,8 @@ int nest_adamw_values(const nest_table_info *info, const void *m, const void *v,
     if (!m || !v || !m_exp || !v_exp || !m_out || !v_out || !aligned_to(m, 256) || !aligned_to(v, 256) ||
         !aligned_to(m_out, 256) || !aligned_to(v_out, 256))
         return NEST_E_INVALID;
-    const dim3 grid(unsigned(info->blocks < kSMs * 16 ? info->blocks : kSMs * 16));
+    const int64_t grid_blocks = (info->blocks + kWarps - 1) / kWarps;
+    const dim3 grid(unsigned(grid_blocks < kSMs * 8 ? grid_blocks : kSMs * 8));
     return launch_kernel(values_kernel, grid, dim3(kThreads), 0, stream, 1, "adamw values launch", info->blocks,
                          static_cast<const uint8_t *>(m), static_cast<const uint8_t *>(v), m_exp, v_exp,
                          static_cast<__nv_bfloat16 *>(m_out), static_cast<__nv_bfloat16 *>(v_out));
