@@ -1,0 +1,15 @@
+// Routing kernels for 16-bit logits (nest_route.cuh), a translation unit of its own so that
+// the types compile in parallel.
+#include "nest_route.cuh"
+
+namespace nest {
+
+int launch_route_f16(const RouteArgs &a, int blocks, void *stream) {
+    return launch_route_type<__half>(a, blocks, stream);
+}
+
+int launch_route_backward_f16(const RouteArgs &a, void *stream) {
+    return launch_route_backward_type<__half>(a, stream);
+}
+
+}  // namespace nest
