@@ -124,11 +124,10 @@ __device__ __forceinline__ void store_piece(T *p, const T *from) {
     }
 }
 
-// Row t as the lane holds it; minus infinity past the last expert.
+// A row as the lane holds it; minus infinity past the last expert.
 template <typename T, int V, bool VEC>
-__device__ __forceinline__ void fetch_row(const RouteArgs &a, int64_t t, int lane, T (&x)[V]) {
+__device__ __forceinline__ void fetch_row(const RouteArgs &a, const T *row, int lane, T (&x)[V]) {
     using L = Place<V, VEC>;
-    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
 #pragma unroll
     for (int i = 0; i < V; i += L::C) {
         const int e = L::of(i, lane);
@@ -144,7 +143,20 @@ __device__ __forceinline__ void fetch_row(const RouteArgs &a, int64_t t, int lan
     }
 }
 
-// Whether a fetched row is live; x, its largest value `top`, e = exp(x - top) and their sum.
+// exp(x - top) over the row's own unit: one multiply-add and an exponential of base 2.  The
+// rounding of top * log2(e) is the same factor in every gate of the row and leaves with the
+// division by their sum.  A largest value near the type's end would overflow it: then the
+// difference is taken first.
+struct RowExp {
+    float top, shift;
+    bool far;
+    __device__ __forceinline__ explicit RowExp(float t) : top(t), shift(t * kLog2e), far(fabsf(t) > 1e38f) {}
+    __device__ __forceinline__ float operator()(float x) const {
+        return exp2_of(far ? (x - top) * kLog2e : fmaf(x, kLog2e, -shift));
+    }
+};
+
+// Whether a fetched row is live; x, its largest value, e = exp(x - top) and their sum.
 template <typename T, int V>
 __device__ __forceinline__ bool gates_of(const T (&raw)[V], float (&x)[V], float (&e)[V], float &top, float &sum) {
     top = -INFINITY;
@@ -160,14 +172,28 @@ __device__ __forceinline__ bool gates_of(const T (&raw)[V], float (&x)[V], float
         for (int i = 0; i < V; i++) nan |= isnan(x[i]);
         if (!__any_sync(0xffffffffu, nan)) return false;
     }
+    const RowExp ex(top);
+    if (ex.far) {
+#pragma unroll
+        for (int i = 0; i < V; i++) e[i] = exp2_of((x[i] - top) * kLog2e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) e[i] = exp2_of(fmaf(x[i], kLog2e, -ex.shift));
+    }
     sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        e[i] = exp2_of((x[i] - top) * kLog2e);
-        sum += e[i];
-    }
+    for (int i = 0; i < V; i++) sum += e[i];
     sum = warp_sum(sum);
     return true;
+}
+
+// The sum over the warp of what only the first 8 lanes (FEW) or any lanes have; the others get it
+// only in the second case, or as 0.
+template <bool FEW>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = FEW ? 4 : 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 // Sorts w[0 .. V) downwards (V a power of two): Batcher's merging of odd and even parts.
@@ -190,7 +216,7 @@ __device__ __forceinline__ void sort_down(uint32_t (&w)[V]) {
 
 // The choice on whole logits, which are read again: lane j gets the j-th chosen expert or -1.
 template <typename T, int V>
-__device__ __noinline__ int choose_exactly(const T *row, int64_t col_stride, int experts, int k) {
+__device__ __forceinline__ int choose_exactly(const T *row, int64_t col_stride, int experts, int k) {
     const int lane = threadIdx.x & 31;
     uint32_t w[V], taken = 0;
 #pragma unroll
@@ -200,6 +226,7 @@ __device__ __noinline__ int choose_exactly(const T *row, int64_t col_stride, int
         w[i] = x > -INFINITY ? order_word(x) : 0u;   // 0 for NaN too
     }
     int id = -1;
+#pragma unroll 1
     for (int j = 0; j < k; j++) {
         uint32_t best = 0;
         int at = INT32_MAX;
@@ -218,14 +245,14 @@ __device__ __noinline__ int choose_exactly(const T *row, int64_t col_stride, int
     return id;
 }
 
-// Lane j gets the j-th chosen expert of row t or -1.  LEN: how much of a lane's list is needed, at
-// least min(V, k + 1).  nan: some gate of the row is NaN.
-template <typename T, int V, bool VEC, int LEN>
-__device__ __forceinline__ int choose(const RouteArgs &a, int64_t t, const float (&x)[V], int lane, bool nan) {
-    const int k = a.k;
+// Lane j gets the j-th chosen expert of the row or -1.  FEW: k is at most 8.  nan: some gate of
+// the row is NaN.
+template <typename T, int V, bool VEC, bool FEW>
+__device__ __forceinline__ int choose(const RouteArgs &a, const T *row, const float (&x)[V], int lane, bool nan) {
     using L = Place<V, VEC>;
     constexpr uint32_t kIndex = 32 * V - 1;   // the bits that hold the index
-    constexpr bool kWhole = sizeof(T) == 2;
+    constexpr int kRest = sizeof(T) == 2 ? 0 : 1;   // whether the largest word left is looked at too
+    const int k = a.k;
     bool again = nan;
     uint32_t mine = 0;
     if (!again) {
@@ -233,25 +260,40 @@ __device__ __forceinline__ int choose(const RouteArgs &a, int64_t t, const float
 #pragma unroll
         for (int i = 0; i < V; i++) w[i] = (order_word(x[i]) & ~kIndex) | (kIndex - L::of(i, lane));
         sort_down<V>(w);
-        uint32_t last = 0;
-#pragma unroll 1
-        for (int j = 0; j < k; j++) {
-            last = __reduce_max_sync(0xffffffffu, w[0]);
-            if (lane == j) mine = last;
-            if (w[0] == last) {
+        if constexpr (FEW) {
 #pragma unroll
-                for (int i = 0; i + 1 < LEN; i++) w[i] = w[i + 1];
-                w[LEN - 1] = 0;
+            for (int j = 0; j < 8; j++) {
+                if (j >= k) break;
+                const uint32_t last = __reduce_max_sync(0xffffffffu, w[0]);
+                if (lane == j) mine = last;
+                if (w[0] == last) {   // of a list only what the rounds left can reach is moved
+                    constexpr int kNone = 0;
+                    const int rounds = 8 + kRest - 1 - j;
+#pragma unroll
+                    for (int i = 0; i < V; i++)
+                        if (i < rounds) w[i] = i + 1 < V ? w[i + 1 < V ? i + 1 : i] : kNone;
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < k; j++) {
+                const uint32_t last = __reduce_max_sync(0xffffffffu, w[0]);
+                if (lane == j) mine = last;
+                if (w[0] == last) {
+#pragma unroll
+                    for (int i = 0; i + 1 < V; i++) w[i] = w[i + 1];
+                    w[V - 1] = 0;
+                }
             }
         }
-        if (!kWhole) {
+        if (kRest) {
             const uint32_t left = __reduce_max_sync(0xffffffffu, w[0]);
             uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
             if (lane == k - 1) next = left;
             again = __any_sync(0xffffffffu, lane < k && next > kClosed && ((mine ^ next) & ~kIndex) == 0);
         }
     }
-    if (again) return choose_exactly<T, V>(static_cast<const T *>(a.logits) + t * a.row_stride, a.col_stride, a.experts, k);
+    if (again) return choose_exactly<T, V>(row, a.col_stride, a.experts, k);
     return mine > kClosed ? int(kIndex - (mine & kIndex)) : -1;
 }
 
@@ -320,7 +362,7 @@ __device__ __forceinline__ void finish(const RouteArgs &a, int rows, P row_p, N 
     cluster.sync();   // the others' shared memory is read until here
 }
 
-template <typename T, int V, bool VEC, int LEN>
+template <typename T, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
     constexpr int kWarps = RouteShape<V>::kWarps, kThreads = RouteShape<V>::kThreads;
     using L = Place<V, VEC>;
@@ -330,23 +372,29 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int stride = int(gridDim.x) * kWarps, tokens = int(a.tokens);
+    int t = int(blockIdx.x) * kWarps + warp;
+    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
+    const int64_t row_step = stride * a.row_stride;
+    int at = t * a.k + lane;             // T k is below 2^31
+    const int at_step = stride * a.k;
+    T raw[V];
+    bool on = t < tokens && !(a.mask && !a.mask[t]);
+    if (on) fetch_row<T, V, VEC>(a, row, lane, raw);
     for (int e = threadIdx.x; e <= a.experts; e += kThreads) sh_count[e] = 0;
     __syncthreads();
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; i++) acc[i] = 0.0f;
     int live = 0;
-    const int64_t stride = int64_t(gridDim.x) * kWarps;
-    int64_t t = int64_t(blockIdx.x) * kWarps + warp;
-    T raw[V];
-    bool on = t < a.tokens && !(a.mask && !a.mask[t]);
-    if (on) fetch_row<T, V, VEC>(a, t, lane, raw);
-    for (; t < a.tokens; t += stride) {
+#pragma unroll 1
+    for (; t < tokens; t += stride, at += at_step) {
         float x[V], e[V], top, sum;
         const bool is_live = on && gates_of<T, V>(raw, x, e, top, sum);
-        const int64_t ahead = t + stride;
-        on = ahead < a.tokens && !(a.mask && !a.mask[ahead]);
-        if (on) fetch_row<T, V, VEC>(a, ahead, lane, raw);
+        const T *here = row;
+        row += row_step;
+        on = t < tokens - stride && !(a.mask && !a.mask[t + stride]);
+        if (on) fetch_row<T, V, VEC>(a, row, lane, raw);
         int id = -1;
         float w = 0.0f;
         if (is_live) {
@@ -354,19 +402,18 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
             const float inv = __fdividef(1.0f, sum);
 #pragma unroll
             for (int i = 0; i < V; i++) acc[i] = fmaf(e[i], inv, acc[i]);
-            id = choose<T, V, VEC, LEN>(a, t, x, lane, isnan(sum));
+            id = choose<T, V, VEC, FEW>(a, here, x, lane, isnan(sum));
             if (id >= 0) {
-                const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
-                w = exp2_of((to_f32(row[id * a.col_stride]) - top) * kLog2e);
+                w = RowExp(top)(to_f32(here[id * a.col_stride]));
                 atomicAdd(&sh_count[id], 1);
             }
-            // NaN rows: every gate is NaN, those of finite logits below plus infinity too
-            w = a.normalize && !isnan(sum) ? w / warp_sum(w) : w * inv;
+            // in a row with NaN every gate is NaN, also those that are 0 here
+            w *= a.normalize && !isnan(sum) ? __fdividef(1.0f, group_sum<FEW>(w)) : inv;
             if (id < 0) w = 0.0f;
         }
         if (lane < a.k) {
-            a.ids[t * a.k + lane] = id;
-            a.weights[t * a.k + lane] = w;
+            a.ids[at] = id;
+            a.weights[at] = w;
         }
     }
 #pragma unroll
@@ -430,7 +477,7 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
     float w = 0.0f, u = 0.0f;
     auto fetch = [&](int64_t row) {
         if (row >= a.tokens || (a.mask && !a.mask[row])) return false;
-        fetch_row<T, V, VEC>(a, row, lane, raw);
+        fetch_row<T, V, VEC>(a, static_cast<const T *>(a.logits) + row * a.row_stride, lane, raw);
         id = -1;
         w = u = 0.0f;
         if (a.grad_weights && lane < a.k) {
@@ -512,11 +559,10 @@ int launch_route_type(const RouteArgs &a, int blocks, void *stream) {
     return with_values(a.experts, [&](auto v) {
         constexpr int V = decltype(v)::v;
         using S = RouteShape<V>;
-        constexpr int kShort = V < 9 ? V : 9;   // lists of 9 serve k up to 8
         const size_t smem = size_t(4) * (S::kWarps * a.experts + a.experts + 1);
-        const bool vec = vector_rows<T, V>(a), few = a.k < 9;
-        auto kernel = vec ? (few ? route_kernel<T, V, (V > 1), kShort> : route_kernel<T, V, (V > 1), V>)
-                          : (few ? route_kernel<T, V, false, kShort> : route_kernel<T, V, false, V>);
+        const bool vec = vector_rows<T, V>(a), few = a.k <= 8;
+        auto kernel = vec ? (few ? route_kernel<T, V, (V > 1), true> : route_kernel<T, V, (V > 1), false>)
+                          : (few ? route_kernel<T, V, false, true> : route_kernel<T, V, false, false>);
         return launch_kernel(kernel, dim3(blocks), dim3(S::kThreads), smem, stream, a.joined ? blocks : 1,
                              "route launch", a);
     });
