@@ -29,20 +29,23 @@ int check(const nest_route_desc *d) {
     return NEST_OK;
 }
 
-// Blocks of the forward kernel, and whether they are one cluster.
+// Blocks of the forward kernel, and whether they are one cluster: up to kJoined passes of it over
+// the rows are quicker than a second launch.
+constexpr int kJoined = 4;
 struct Grid {
     int blocks;
     bool joined;
 };
 Grid grid_of(const nest_route_desc *d) {
     Grid g;
-    with_values(d->experts, [&](auto v) {
-        using S = RouteShape<decltype(v)::v>;
-        const int64_t b = (d->tokens + S::kWarps - 1) / S::kWarps, most = kSMs * S::kPerSm;
-        g.blocks = int(b < 1 ? 1 : b < most ? b : most);
+    with_row(d->experts, [&](auto lanes, auto values) {
+        using S = RouteShape<decltype(values)::v>;
+        constexpr int kRows = S::kWarps * 32 / decltype(lanes)::v;
+        const int64_t b = (d->tokens + kRows - 1) / kRows, most = kSMs * S::kPerSm;
+        g.joined = b <= kJoined * kCluster;
+        g.blocks = int(b < 1 ? 1 : g.joined && b > kCluster ? kCluster : b < most ? b : most);
         return 0;
     });
-    g.joined = g.blocks <= kCluster;
     return g;
 }
 

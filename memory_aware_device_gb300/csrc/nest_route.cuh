@@ -1,18 +1,20 @@
 // Kernels of the routing operators (definitions in nest_train.h), one instantiation per
 // element type in nest_route_f32.cu, nest_route_bf16.cu and nest_route_f16.cu.
 //
-// A warp takes a row at a time and holds it in registers, so the logits are read once, in
-// pieces of up to 32 bytes per lane where alignment allows (VEC); the next row's are under
-// way while one is worked on.
+// Forward, a warp takes 32 / LANES rows at a time, each held in the registers of LANES lanes
+// with up to 32 values per lane, so that the logits are read once and what is done per row
+// (reductions, rounds, results) is shared by several rows; backward, a row at a time.  Logits are
+// read in pieces of up to 32 bytes per lane where alignment allows (VEC).
 //
 // Choice of the k largest.  A logit becomes a 32-bit word whose order is that of the logits,
 // with its lowest bits replaced by the complement of the expert's index: all words of a row
 // differ, and among logits that agree in the bits kept the lower index is the larger word.
-// Each lane sorts its words once; then k rounds take the maximum over the lanes' largest words
-// with one warp-wide reduction instruction each, and the lane that had it moves its list up.
-// 16-bit logits lose nothing to the index.  With 32-bit logits up to 10 bits are lost: one
-// more round gives the largest word left, and if two of these neighbours agree in the bits
-// kept, or a gate is NaN, the row's choice is made again on whole logits.
+// Each lane sorts its words once and keeps as many as can be chosen; then k rounds take the
+// maximum over the row's lanes, and the lane that had it moves its list up.  16-bit logits
+// lose nothing to the index.  With 32-bit logits up to 10 bits are lost, and the word comes
+// from the exponent (x - top) log2(e), negative for every x, which may round two logits to
+// one: one more round gives the largest word left, and if two of these neighbours agree in
+// the bits kept, the row's choice is made again on whole logits.  So it is where a gate is NaN.
 //
 // Sums.  Every warp adds up the gates of its rows per expert in registers, the block adds its
 // warps in order, and the blocks' rows are added in order in 64 bits, so no result depends on
@@ -47,10 +49,16 @@ struct RouteArgs {
     bool vector_grad;
 };
 
-// Rows of up to 32 V experts.  Values per lane, block size and blocks per SM that the kernels
-// are compiled for: the registers of a row, of the next one and of the sums.
+// Block size and blocks per SM that the kernels are compiled for, by the values per lane: the
+// registers of the values, of their words and of the sums.
 template <int V>
 struct RouteShape {
+    static constexpr int kWarps = 16;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kPerSm = V <= 8 ? 2 : 1;
+};
+template <int V>
+struct BackwardShape {
     static constexpr int kWarps = V >= 32 ? 8 : 16;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kPerSm = V <= 8 ? 2 : 1;
@@ -90,10 +98,10 @@ template <> struct Piece<8> { using type = uint2; };
 template <> struct Piece<16> { using type = uint4; };
 
 // Which expert a lane's i-th value is: pieces of C neighbours, one lane's after another's.
-template <int V, bool VEC>
+template <int V, bool VEC, int LANES = 32>
 struct Place {
     static constexpr int C = VEC ? (V < 8 ? V : 8) : 1;
-    static __device__ __forceinline__ int of(int i, int lane) { return (i / C) * (32 * C) + lane * C + i % C; }
+    static __device__ __forceinline__ int of(int i, int lane) { return (i / C) * (LANES * C) + lane * C + i % C; }
 };
 
 template <typename T, int N>
@@ -125,9 +133,9 @@ __device__ __forceinline__ void store_piece(T *p, const T *from) {
 }
 
 // A row as the lane holds it; minus infinity past the last expert.
-template <typename T, int V, bool VEC>
+template <typename T, int V, bool VEC, int LANES = 32>
 __device__ __forceinline__ void fetch_row(const RouteArgs &a, const T *row, int lane, T (&x)[V]) {
-    using L = Place<V, VEC>;
+    using L = Place<V, VEC, LANES>;
 #pragma unroll
     for (int i = 0; i < V; i += L::C) {
         const int e = L::of(i, lane);
@@ -143,17 +151,18 @@ __device__ __forceinline__ void fetch_row(const RouteArgs &a, const T *row, int 
     }
 }
 
-// exp(x - top) over the row's own unit: one multiply-add and an exponential of base 2.  The
-// rounding of top * log2(e) is the same factor in every gate of the row and leaves with the
-// division by their sum.  A largest value near the type's end would overflow it: then the
-// difference is taken first.
+// exp(x - top) as base 2 to the power r, r = (x - top) log2(e) by one multiply-add.  The
+// rounding of top log2(e), and the little that `shift` is more so that r is below 0 for every
+// x <= top, are the same factor in every gate of the row and leave with the division by their
+// sum.  A largest value near the type's end would overflow the product: far, the difference
+// is taken first.
 struct RowExp {
     float top, shift;
     bool far;
-    __device__ __forceinline__ explicit RowExp(float t) : top(t), shift(t * kLog2e), far(fabsf(t) > 1e38f) {}
-    __device__ __forceinline__ float operator()(float x) const {
-        return exp2_of(far ? (x - top) * kLog2e : fmaf(x, kLog2e, -shift));
-    }
+    __device__ __forceinline__ explicit RowExp(float t)
+        : top(t), shift(fmaf(t, kLog2e, fmaf(fabsf(t), 0x1p-20f, 0x1p-20f))), far(fabsf(t) > 1e38f) {}
+    __device__ __forceinline__ float near(float x) const { return fmaf(x, kLog2e, -shift); }
+    __device__ __forceinline__ float of(float x) const { return far ? (x - top) * kLog2e : near(x); }
 };
 
 // Whether a fetched row is live; x, its largest value, e = exp(x - top) and their sum.
@@ -175,10 +184,10 @@ __device__ __forceinline__ bool gates_of(const T (&raw)[V], float (&x)[V], float
     const RowExp ex(top);
     if (ex.far) {
 #pragma unroll
-        for (int i = 0; i < V; i++) e[i] = exp2_of((x[i] - top) * kLog2e);
+        for (int i = 0; i < V; i++) e[i] = exp2_of(ex.of(x[i]));
     } else {
 #pragma unroll
-        for (int i = 0; i < V; i++) e[i] = exp2_of(fmaf(x[i], kLog2e, -ex.shift));
+        for (int i = 0; i < V; i++) e[i] = exp2_of(ex.near(x[i]));
     }
     sum = 0.0f;
 #pragma unroll
@@ -187,114 +196,188 @@ __device__ __forceinline__ bool gates_of(const T (&raw)[V], float (&x)[V], float
     return true;
 }
 
-// The sum over the warp of what only the first 8 lanes (FEW) or any lanes have; the others get it
-// only in the second case, or as 0.
-template <bool FEW>
-__device__ __forceinline__ float group_sum(float v) {
+// Over the LANES lanes of a row.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int o = FEW ? 4 : 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+template <int LANES>
+__device__ __forceinline__ float row_max(float v) {   // NaN counts as nothing
+    if constexpr (LANES == 32) return warp_max(v);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <int LANES, typename U>
+__device__ __forceinline__ U row_largest(U v) {
+    if constexpr (LANES == 32 && sizeof(U) == 4) return __reduce_max_sync(0xffffffffu, v);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+// Whether any lane of the row says so.
+template <int LANES>
+__device__ __forceinline__ bool row_any(bool b) {
+    const uint32_t all = __ballot_sync(0xffffffffu, b);
+    if constexpr (LANES == 32) return all != 0;
+    return (all >> (threadIdx.x & 31 & ~(LANES - 1)) & ((1u << (LANES & 31)) - 1)) != 0;
+}
 
-// Sorts w[0 .. V) downwards (V a power of two): Batcher's merging of odd and even parts.
-template <int V>
+// Sorts w[A .. A + N) downwards (N a power of two): Batcher's merging of odd and even parts.
+template <int A, int N, int V>
 __device__ __forceinline__ void sort_down(uint32_t (&w)[V]) {
 #pragma unroll
-    for (int p = 1; p < V; p *= 2)
+    for (int p = 1; p < N; p *= 2)
 #pragma unroll
         for (int q = p; q > 0; q /= 2)
 #pragma unroll
-            for (int j = q % p; j < V - q; j += 2 * q)
+            for (int j = q % p; j < N - q; j += 2 * q)
 #pragma unroll
                 for (int i = 0; i < q; i++)
-                    if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const uint32_t hi = max(w[i + j], w[i + j + q]), lo = min(w[i + j], w[i + j + q]);
-                        w[i + j] = hi;
-                        w[i + j + q] = lo;
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const int u = A + i + j, l = u + q;
+                        const uint32_t hi = max(w[u], w[l]), lo = min(w[u], w[l]);
+                        w[u] = hi;
+                        w[l] = lo;
                     }
 }
 
-// The choice on whole logits, which are read again: lane j gets the j-th chosen expert or -1.
-template <typename T, int V>
-__device__ __forceinline__ int choose_exactly(const T *row, int64_t col_stride, int experts, int k) {
-    const int lane = threadIdx.x & 31;
+// Leaves the 8 largest of w, downwards, in w[0 .. 8): sorted eights, merged in pairs.  Of two
+// sorted eights the larger of each element and the other's mirror image are the 8 largest, in
+// an order that three rounds of exchanges sort.
+template <int V>
+__device__ __forceinline__ void largest_eight(uint32_t (&w)[V]) {
+    static_assert(V % 8 == 0, "whole eights");
+    sort_down<0, 8>(w);
+    if constexpr (V >= 16) sort_down<8, 8>(w);
+    if constexpr (V >= 32) {
+        sort_down<16, 8>(w);
+        sort_down<24, 8>(w);
+    }
+#pragma unroll
+    for (int step = 8; step < V; step *= 2)
+#pragma unroll
+        for (int at = 0; at + step < V; at += 2 * step) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                // the other's mirror image is read before either is changed: it is not written
+                w[at + i] = max(w[at + i], w[at + step + 7 - i]);
+            }
+#pragma unroll
+            for (int q = 4; q; q /= 2)
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (!(i & q)) {
+                        const uint32_t hi = max(w[at + i], w[at + i + q]), lo = min(w[at + i], w[at + i + q]);
+                        w[at + i] = hi;
+                        w[at + i + q] = lo;
+                    }
+        }
+}
+
+// The choice on whole logits, which are read again, for the rows whose lanes have `wanted` set
+// (all lanes of the warp take part): lane g of a row's LANES gets in slot s the chosen expert
+// number s LANES + g, or -1.
+template <typename T, int V, int LANES, int SLOTS>
+__device__ __forceinline__ void choose_exactly(const RouteArgs &a, const T *row, bool wanted, int (&id)[SLOTS]) {
+    const int g = threadIdx.x & (LANES - 1);
     uint32_t w[V], taken = 0;
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        const int e = lane + 32 * i;
-        const float x = e < experts ? to_f32(row[e * col_stride]) : -INFINITY;
+        const int e = g + LANES * i;
+        const float x = wanted && e < a.experts ? to_f32(row[e * a.col_stride]) : -INFINITY;
         w[i] = x > -INFINITY ? order_word(x) : 0u;   // 0 for NaN too
     }
-    int id = -1;
-#pragma unroll 1
-    for (int j = 0; j < k; j++) {
-        uint32_t best = 0;
-        int at = INT32_MAX;
+    if (wanted)
 #pragma unroll
-        for (int i = 0; i < V; i++)
-            if (w[i] > best && !(taken >> i & 1)) {
-                best = w[i];
-                at = lane + 32 * i;
-            }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (!top) break;
-        const int e = __reduce_min_sync(0xffffffffu, best == top ? at : INT32_MAX);
-        if ((e & 31) == lane) taken |= 1u << (e >> 5);
-        if (lane == j) id = e;
+        for (int s = 0; s < SLOTS; s++) id[s] = -1;
+#pragma unroll 1
+    for (int j = 0; j < a.k; j++) {
+        unsigned long long best = 0;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            const unsigned long long c =
+                (static_cast<unsigned long long>(w[i]) << 32) | uint32_t(~(g + LANES * i));
+            if (w[i] && !(taken >> i & 1) && c > best) best = c;
+        }
+        best = row_largest<LANES>(best);
+        const int e = int(~uint32_t(best));
+        if (best && e % LANES == g) taken |= 1u << (e / LANES);
+#pragma unroll
+        for (int s = 0; s < SLOTS; s++)
+            if (wanted && best && s * LANES + g == j) id[s] = e;
     }
-    return id;
 }
 
-// Lane j gets the j-th chosen expert of the row or -1.  FEW: k is at most 8.  nan: some gate of
-// the row is NaN.
-template <typename T, int V, bool VEC, bool FEW>
-__device__ __forceinline__ int choose(const RouteArgs &a, const T *row, const float (&x)[V], int lane, bool nan) {
-    using L = Place<V, VEC>;
-    constexpr uint32_t kIndex = 32 * V - 1;   // the bits that hold the index
-    constexpr int kRest = sizeof(T) == 2 ? 0 : 1;   // whether the largest word left is looked at too
-    const int k = a.k;
-    bool again = nan;
-    uint32_t mine = 0;
-    if (!again) {
-        uint32_t w[V];
+// Lane g of a row's LANES gets in slot s the row's chosen expert number s LANES + g, or -1.  w:
+// the words of the lane's values.  FEW: k is at most 8, and one slot is enough.  again: the row's
+// words cannot be used; idle: nothing is chosen in the row.
+template <typename T, int V, int LANES, bool FEW, int SLOTS>
+__device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_t (&w)[V], bool again, bool idle,
+                                       int (&id)[SLOTS]) {
+    constexpr uint32_t kIndex = LANES * V - 1;   // the bits that hold the index
+    constexpr bool kWhole = sizeof(T) == 2;      // no bit of a logit is lost
+    constexpr int kList = FEW && V > 8 ? 8 : V;
+    const int k = a.k, g = threadIdx.x & (LANES - 1);
+    uint32_t mine[SLOTS], last = 0;
 #pragma unroll
-        for (int i = 0; i < V; i++) w[i] = (order_word(x[i]) & ~kIndex) | (kIndex - L::of(i, lane));
-        sort_down<V>(w);
-        if constexpr (FEW) {
+    for (int s = 0; s < SLOTS; s++) mine[s] = 0;
+    if constexpr (kList < V)
+        largest_eight<V>(w);
+    else
+        sort_down<0, V>(w);
+    if constexpr (FEW) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                if (j >= k) break;
-                const uint32_t last = __reduce_max_sync(0xffffffffu, w[0]);
-                if (lane == j) mine = last;
-                if (w[0] == last) {   // of a list only what the rounds left can reach is moved
-                    constexpr int kNone = 0;
-                    const int rounds = 8 + kRest - 1 - j;
+        for (int j = 0; j < 8; j++) {
+            if (j >= k) break;
+            last = row_largest<LANES>(w[0]);
+            if (g == j) mine[0] = last;
+            if (w[0] == last) {   // of a list only what the rounds left can reach is moved
 #pragma unroll
-                    for (int i = 0; i < V; i++)
-                        if (i < rounds) w[i] = i + 1 < V ? w[i + 1 < V ? i + 1 : i] : kNone;
-                }
+                for (int i = 0; i < kList; i++)
+                    if (i < 8 - j) w[i] = i + 1 < kList ? w[i + 1 < kList ? i + 1 : i] : 0u;
             }
-        } else {
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < SLOTS; s++)
 #pragma unroll 1
-            for (int j = 0; j < k; j++) {
-                const uint32_t last = __reduce_max_sync(0xffffffffu, w[0]);
-                if (lane == j) mine = last;
+            for (int j = 0; j < LANES && s * LANES + j < k; j++) {
+                last = row_largest<LANES>(w[0]);
+                if (g == j) mine[s] = last;
                 if (w[0] == last) {
 #pragma unroll
                     for (int i = 0; i + 1 < V; i++) w[i] = w[i + 1];
                     w[V - 1] = 0;
                 }
             }
-        }
-        if (kRest) {
-            const uint32_t left = __reduce_max_sync(0xffffffffu, w[0]);
-            uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
-            if (lane == k - 1) next = left;
-            again = __any_sync(0xffffffffu, lane < k && next > kClosed && ((mine ^ next) & ~kIndex) == 0);
-        }
     }
-    if (again) return choose_exactly<T, V>(row, a.col_stride, a.experts, k);
-    return mine > kClosed ? int(kIndex - (mine & kIndex)) : -1;
+    if (!kWhole) {
+        // a list of 8 that is used up may have had more
+        if (kList < V) again |= row_any<LANES>(w[0] == 0u);
+        uint32_t next = row_largest<LANES>(w[0]);
+        bool close = ((last ^ next) & ~kIndex) == 0;
+#pragma unroll
+        for (int s = SLOTS - 1; s >= 0; s--) {   // each chosen word against the one after it
+            uint32_t up = __shfl_down_sync(0xffffffffu, mine[s], 1, LANES);
+            if (s + 1 < SLOTS) {
+                const uint32_t over = __shfl_sync(0xffffffffu, mine[s + 1 < SLOTS ? s + 1 : s], 0, LANES);
+                if (g == LANES - 1) up = over;
+            } else if (g == LANES - 1) {
+                up = ~mine[s];
+            }
+            close |= s * LANES + g < k - 1 && ((mine[s] ^ up) & ~kIndex) == 0;
+            // the words of closed experts and of logits that overflow the exponent are alike
+            close |= s * LANES + g < k && mine[s] <= kClosed;
+        }
+        again |= row_any<LANES>(close);
+    }
+#pragma unroll
+    for (int s = 0; s < SLOTS; s++) id[s] = mine[s] > kClosed ? int(kIndex - (mine[s] & kIndex)) : -1;
+    if (__any_sync(0xffffffffu, again && !idle))
+        choose_exactly<T, V, LANES, SLOTS>(a, row, again && !idle, id);
 }
 
 // Experts first .. first + 31 (lane) summed over `rows` rows of sums and counts by the block's
@@ -362,63 +445,110 @@ __device__ __forceinline__ void finish(const RouteArgs &a, int rows, P row_p, N 
     cluster.sync();   // the others' shared memory is read until here
 }
 
-template <typename T, int V, bool VEC, bool FEW>
+template <typename T, int LANES, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
     constexpr int kWarps = RouteShape<V>::kWarps, kThreads = RouteShape<V>::kThreads;
-    using L = Place<V, VEC>;
+    constexpr int kRows = 32 / LANES, kSlots = FEW ? 1 : 32 / LANES;
+    constexpr uint32_t kIndex = LANES * V - 1;
+    using L = Place<V, VEC, LANES>;
     extern __shared__ unsigned char sh[];
     float *sh_sum = reinterpret_cast<float *>(sh);                            // [kWarps][experts]
     int32_t *sh_count = reinterpret_cast<int32_t *>(sh_sum + kWarps * a.experts);   // [experts], then live rows
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int stride = int(gridDim.x) * kWarps, tokens = int(a.tokens);
-    int t = int(blockIdx.x) * kWarps + warp;
-    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
-    const int64_t row_step = stride * a.row_stride;
-    int at = t * a.k + lane;             // T k is below 2^31
-    const int at_step = stride * a.k;
-    T raw[V];
-    bool on = t < tokens && !(a.mask && !a.mask[t]);
-    if (on) fetch_row<T, V, VEC>(a, row, lane, raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane & (LANES - 1);
+    const int64_t stride = int64_t(gridDim.x) * kWarps * kRows;
     for (int e = threadIdx.x; e <= a.experts; e += kThreads) sh_count[e] = 0;
     __syncthreads();
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; i++) acc[i] = 0.0f;
     int live = 0;
-#pragma unroll 1
-    for (; t < tokens; t += stride, at += at_step) {
-        float x[V], e[V], top, sum;
-        const bool is_live = on && gates_of<T, V>(raw, x, e, top, sum);
-        const T *here = row;
-        row += row_step;
-        on = t < tokens - stride && !(a.mask && !a.mask[t + stride]);
-        if (on) fetch_row<T, V, VEC>(a, row, lane, raw);
-        int id = -1;
-        float w = 0.0f;
-        if (is_live) {
-            live++;
-            const float inv = __fdividef(1.0f, sum);
+    for (int64_t first = (int64_t(blockIdx.x) * kWarps + warp) * kRows; first < a.tokens; first += stride) {
+        const int64_t t = first + lane / LANES;
+        const bool in = t < a.tokens, on = in && !(a.mask && !a.mask[t]);
+        const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
+        T raw[V];
 #pragma unroll
-            for (int i = 0; i < V; i++) acc[i] = fmaf(e[i], inv, acc[i]);
-            id = choose<T, V, VEC, FEW>(a, here, x, lane, isnan(sum));
-            if (id >= 0) {
-                w = RowExp(top)(to_f32(here[id * a.col_stride]));
-                atomicAdd(&sh_count[id], 1);
-            }
-            // in a row with NaN every gate is NaN, also those that are 0 here
-            w *= a.normalize && !isnan(sum) ? __fdividef(1.0f, group_sum<FEW>(w)) : inv;
-            if (id < 0) w = 0.0f;
+        for (int i = 0; i < V; i++) raw[i] = from_f32<T>(-INFINITY);
+        if (on) fetch_row<T, V, VEC, LANES>(a, row, g, raw);
+        float x[V], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            x[i] = to_f32(raw[i]);
+            top = fmaxf(top, x[i]);
         }
-        if (lane < a.k) {
-            a.ids[at] = id;
-            a.weights[at] = w;
+        top = row_max<LANES>(top);
+        bool is_live = top > -INFINITY;
+        if (__any_sync(0xffffffffu, on && !is_live)) {   // closed, unless NaN is in it
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < V; i++) nan |= isnan(x[i]);
+            is_live |= row_any<LANES>(nan);
+        }
+        if (!(top > -INFINITY)) top = 0.0f;
+        const RowExp ex(top);
+        uint32_t w[V];
+        float sum = 0.0f;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < V; i++) w[i] = (order_word(x[i]) & ~kIndex) | (kIndex - L::of(i, g));
+        }
+        if (__any_sync(0xffffffffu, ex.far)) {
+#pragma unroll
+            for (int i = 0; i < V; i++) x[i] = ex.of(x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) x[i] = ex.near(x[i]);
+        }
+        if constexpr (sizeof(T) == 4) {   // r is below 0: its bits inverted are in order
+#pragma unroll
+            for (int i = 0; i < V; i++) w[i] = (~__float_as_uint(x[i]) & ~kIndex) | (kIndex - L::of(i, g));
+        }
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            x[i] = exp2_of(x[i]);
+            sum += x[i];
+        }
+        sum = row_sum<LANES>(sum);
+        const float inv = is_live ? __fdividef(1.0f, sum) : 0.0f;
+        live += is_live;
+#pragma unroll
+        for (int i = 0; i < V; i++) acc[i] = fmaf(x[i], inv, acc[i]);
+
+        int id[kSlots];
+        choose<T, V, LANES, FEW, kSlots>(a, row, w, isnan(sum) || (sizeof(T) == 4 && ex.far), !is_live, id);
+        float gate[kSlots], total = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSlots; s++) {
+            if (!is_live) id[s] = -1;
+            gate[s] = 0.0f;
+            if (id[s] >= 0) {
+                gate[s] = exp2_of(ex.of(to_f32(row[id[s] * a.col_stride])));
+                atomicAdd(&sh_count[id[s]], 1);
+            }
+            total += gate[s];
+        }
+        // in a row with NaN every gate is NaN, also those that are 0 here
+        const float over = a.normalize ? row_sum<LANES>(total) : sum;
+        const float by = __fdividef(1.0f, isnan(sum) ? sum : over);
+#pragma unroll
+        for (int s = 0; s < kSlots; s++) {
+            const int j = s * LANES + g;
+            if (in && j < a.k) {
+                a.ids[t * a.k + j] = id[s];
+                a.weights[t * a.k + j] = id[s] >= 0 ? gate[s] * by : 0.0f;
+            }
         }
     }
+    // the warp's rows of lanes, then its lanes, then the block's warps
 #pragma unroll
-    for (int i = 0; i < V; i++)
-        if (L::of(i, lane) < a.experts) sh_sum[warp * a.experts + L::of(i, lane)] = acc[i];
+    for (int i = 0; i < V; i++) {
+#pragma unroll
+        for (int o = LANES; o < 32; o *= 2) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        if (lane < LANES && L::of(i, g) < a.experts) sh_sum[warp * a.experts + L::of(i, g)] = acc[i];
+    }
+    live = __reduce_add_sync(0xffffffffu, g ? 0 : live);
     if (lane == 0 && live) atomicAdd(&sh_count[a.experts], live);
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += kThreads) {
@@ -451,8 +581,8 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
 // drops out of the gradient, and without it the subtraction of the mean loses no digits.
 // The k terms reach their experts' lanes through the warp's row of shared memory.
 template <typename T, int V, bool VEC>
-__global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_backward_kernel(RouteArgs a) {
-    constexpr int kWarps = RouteShape<V>::kWarps;
+__global__ void __launch_bounds__(BackwardShape<V>::kThreads, BackwardShape<V>::kPerSm) route_backward_kernel(RouteArgs a) {
+    constexpr int kWarps = BackwardShape<V>::kWarps;
     using L = Place<V, VEC>;
     extern __shared__ unsigned char sh[];
     pdl_wait();
@@ -532,16 +662,29 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
     }
 }
 
-// fn(integral constant V): the values per lane of a row of `experts`.
-template <int V> struct Values { static constexpr int v = V; };
+template <int N> struct Number { static constexpr int v = N; };
+
+// fn(lanes, values): how a row of `experts` is held.  Eight lanes hold up to 32 values each;
+// longer rows take more lanes.
+template <typename F>
+int with_row(int experts, F fn) {
+    if (experts <= 32) return fn(Number<8>{}, Number<4>{});
+    if (experts <= 64) return fn(Number<8>{}, Number<8>{});
+    if (experts <= 128) return fn(Number<8>{}, Number<16>{});
+    if (experts <= 256) return fn(Number<8>{}, Number<32>{});
+    if (experts <= 512) return fn(Number<16>{}, Number<32>{});
+    return fn(Number<32>{}, Number<32>{});
+}
+
+// fn(values): a row of `experts` in a whole warp.
 template <typename F>
 int with_values(int experts, F fn) {
-    if (experts <= 32) return fn(Values<1>{});
-    if (experts <= 64) return fn(Values<2>{});
-    if (experts <= 128) return fn(Values<4>{});
-    if (experts <= 256) return fn(Values<8>{});
-    if (experts <= 512) return fn(Values<16>{});
-    return fn(Values<32>{});
+    if (experts <= 32) return fn(Number<1>{});
+    if (experts <= 64) return fn(Number<2>{});
+    if (experts <= 128) return fn(Number<4>{});
+    if (experts <= 256) return fn(Number<8>{});
+    if (experts <= 512) return fn(Number<16>{});
+    return fn(Number<32>{});
 }
 
 template <typename T, int V>
@@ -556,13 +699,18 @@ bool vector_rows(const RouteArgs &a) {
 // Launches of one element type (each in its own translation unit).
 template <typename T>
 int launch_route_type(const RouteArgs &a, int blocks, void *stream) {
-    return with_values(a.experts, [&](auto v) {
-        constexpr int V = decltype(v)::v;
+    return with_row(a.experts, [&](auto lanes, auto values) {
+        constexpr int L = decltype(lanes)::v, V = decltype(values)::v;
         using S = RouteShape<V>;
         const size_t smem = size_t(4) * (S::kWarps * a.experts + a.experts + 1);
         const bool vec = vector_rows<T, V>(a), few = a.k <= 8;
-        auto kernel = vec ? (few ? route_kernel<T, V, (V > 1), true> : route_kernel<T, V, (V > 1), false>)
-                          : (few ? route_kernel<T, V, false, true> : route_kernel<T, V, false, false>);
+        auto kernel = vec ? (few ? route_kernel<T, L, V, true, true> : route_kernel<T, L, V, true, false>)
+                          : (few ? route_kernel<T, L, V, false, true> : route_kernel<T, L, V, false, false>);
+        if (smem > 40000) {
+            const int rc = cuda_status(
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)), "route attribute");
+            if (rc) return rc;
+        }
         return launch_kernel(kernel, dim3(blocks), dim3(S::kThreads), smem, stream, a.joined ? blocks : 1,
                              "route launch", a);
     });
@@ -572,7 +720,7 @@ template <typename T>
 int launch_route_backward_type(RouteArgs a, void *stream) {
     return with_values(a.experts, [&](auto v) {
         constexpr int V = decltype(v)::v;
-        using S = RouteShape<V>;
+        using S = BackwardShape<V>;
         constexpr int C = Place<V, true>::C;
         a.vector_grad = a.grad_stride % C == 0 && aligned_to(a.grad, C * sizeof(T));
         const size_t smem = size_t(4) * S::kWarps * 32 * V;
