@@ -7,16 +7,12 @@ namespace nest {
 namespace {
 
 __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(RouteArgs a, int blocks) {
-    __shared__ int32_t sh_n[kFinishThreads / 32];
+    cg::this_cluster().sync();   // every block has started; while the rows are still being written
     pdl_wait();
     pdl_trigger();
     int32_t n = 0;
-    for (int b = threadIdx.x; b < blocks; b += kFinishThreads) n += a.part_n[b];
+    for (int b = threadIdx.x & 31; b < blocks; b += 32) n += a.part_n[b];
     n = __reduce_add_sync(0xffffffffu, n);
-    if ((threadIdx.x & 31) == 0) sh_n[threadIdx.x >> 5] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < kFinishThreads / 32; w++) n += sh_n[w];
     finish<kFinishThreads / 32>(a, blocks, [&](int r, int e) { return a.part_p[int64_t(r) * a.experts + e]; },
            [&](int r, int e) { return a.part_c[int64_t(r) * a.experts + e]; }, n);
 }

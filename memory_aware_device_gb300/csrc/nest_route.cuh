@@ -16,9 +16,9 @@
 // one: one more round gives the largest word left, and if two of these neighbours agree in
 // the bits kept, the row's choice is made again on whole logits.  So it is where a gate is NaN.
 //
-// Sums.  Every warp adds up the gates of its rows per expert in registers, the block adds its
-// warps in order, and the blocks' rows are added in order in 64 bits, so no result depends on
-// the order in which blocks run.  Few rows: the whole grid is one cluster, whose blocks read one
+// Sums.  Every lane adds up the gates of its experts in registers, the block adds its warps in
+// order, and the blocks' rows are added in a fixed order, so no result depends on the order in
+// which blocks run.  Few rows: the whole grid is one cluster, whose blocks read one
 // another's sums from shared memory, and the call is one launch.  Otherwise each block writes
 // its row of sums to the workspace and a second kernel adds them.
 #pragma once
@@ -380,69 +380,56 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
         choose_exactly<T, V, LANES, SLOTS>(a, row, again && !idle, id);
 }
 
-// Experts first .. first + 31 (lane) summed over `rows` rows of sums and counts by the block's
-// warps; warp 0 gets the result in p and c.
-template <int WARPS, typename P, typename N>
-__device__ __forceinline__ void add_rows(int rows, P part_p, N part_c, double (*sh_p)[32], int32_t (*sh_c)[32],
-                                         double &p, int32_t &c) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    p = 0.0;
-    c = 0;
-    for (int r = warp; r < rows; r += WARPS) {
-        p += part_p(r);
-        c += part_c(r);
-    }
-    sh_p[warp][lane] = p;
-    sh_c[warp][lane] = c;
-    __syncthreads();
-    if (warp == 0) {
-        p = 0.0;
-        c = 0;
-        for (int w = 0; w < WARPS; w++) {
-            p += sh_p[w][lane];
-            c += sh_c[w][lane];
-        }
-    }
-    __syncthreads();
-}
-
-// The results from `rows` rows, by the blocks of a cluster: each takes groups of 32 experts.
-// row_p(r, e), row_c(r, e): sums and counts; n: live rows.
+// The results from `rows` rows of sums and counts, row_p(r, e) and row_c(r, e), and n live rows,
+// by the blocks of a cluster that have all started: each takes groups of 32 experts.  A warp
+// adds every WARPS-th row, then a warp adds an expert's WARPS parts as a tree.
 template <int WARPS, typename P, typename N>
 __device__ __forceinline__ void finish(const RouteArgs &a, int rows, P row_p, N row_c, int n) {
-    __shared__ double sh_p[WARPS][32];
-    __shared__ int32_t sh_c[WARPS][32];
-    __shared__ double sh_dot;
+    __shared__ float sh_p[WARPS][33], sh_dot[WARPS], sh_all[kCluster];
+    __shared__ int32_t sh_c[WARPS][33];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = int(cluster.block_rank()), ranks = int(cluster.num_blocks());
-    const int lane = threadIdx.x & 31;
-    double dot = 0.0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float over = n ? 1.0f / float(n) : 0.0f;
+    float dot = 0.0f;
     for (int first = 32 * rank; first < a.experts; first += 32 * ranks) {
-        const int e = first + lane;
-        const bool in = e < a.experts;
-        double p;
-        int32_t c;
-        add_rows<WARPS>(rows, [&](int r) { return in ? row_p(r, e) : 0.0f; }, [&](int r) { return in ? row_c(r, e) : 0; },
-                 sh_p, sh_c, p, c);
-        if (threadIdx.x < 32 && in) {
-            const double mean = n ? p / n : 0.0;
-            a.counts[e] = c;
-            a.mean_prob[e] = float(mean);
-            dot += mean * c;
+        float p = 0.0f;
+        int32_t c = 0;
+        if (first + lane < a.experts) {
+#pragma unroll 4
+            for (int r = warp; r < rows; r += WARPS) {
+                p += row_p(r, first + lane);
+                c += row_c(r, first + lane);
+            }
+        }
+        sh_p[warp][lane] = p;
+        sh_c[warp][lane] = c;
+        __syncthreads();
+        for (int e = warp; e < 32 && first + e < a.experts; e += WARPS) {
+            p = warp_sum(lane < WARPS ? sh_p[lane < WARPS ? lane : 0][e] : 0.0f) * over;
+            c = __reduce_add_sync(0xffffffffu, lane < WARPS ? sh_c[lane < WARPS ? lane : 0][e] : 0);
+            if (lane == 0) {
+                a.counts[first + e] = c;
+                a.mean_prob[first + e] = p;
+            }
+            dot = fmaf(p, float(c), dot);
+        }
+        __syncthreads();
+    }
+    if (lane == 0) sh_dot[warp] = dot;
+    __syncthreads();
+    if (warp == 0) {
+        dot = warp_sum(lane < WARPS ? sh_dot[lane < WARPS ? lane : 0] : 0.0f);
+        if (lane == 0) *cluster.map_shared_rank(sh_all + rank, 0) = dot;
+    }
+    cluster.sync();   // also keeps every block's sums until all have read them
+    if (rank == 0 && warp == 0) {
+        dot = warp_sum(lane < ranks ? sh_all[lane < ranks ? lane : 0] : 0.0f);
+        if (lane == 0) {
+            *a.live = n;
+            *a.loss = n ? dot * float(a.experts) / (float(a.k) * float(n)) : 0.0f;
         }
     }
-    if (threadIdx.x < 32) {
-        dot = warp_sum(dot);
-        if (lane == 0) sh_dot = dot;
-    }
-    cluster.sync();
-    if (rank == 0 && threadIdx.x == 0) {
-        dot = 0.0;
-        for (int r = 0; r < ranks; r++) dot += *cluster.map_shared_rank(&sh_dot, r);
-        *a.live = n;
-        *a.loss = n ? float(dot * a.experts / (double(a.k) * n)) : 0.0f;
-    }
-    cluster.sync();   // the others' shared memory is read until here
 }
 
 template <typename T, int LANES, int V, bool VEC, bool FEW>
@@ -469,9 +456,12 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
         const bool in = t < a.tokens, on = in && !(a.mask && !a.mask[t]);
         const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
         T raw[V];
+        if (on) {
+            fetch_row<T, V, VEC, LANES>(a, row, g, raw);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; i++) raw[i] = from_f32<T>(-INFINITY);
-        if (on) fetch_row<T, V, VEC, LANES>(a, row, g, raw);
+            for (int i = 0; i < V; i++) raw[i] = from_f32<T>(-INFINITY);
+        }
         float x[V], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; i++) {
@@ -568,8 +558,9 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
     }
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    int n = 0;
-    for (int r = 0; r < int(gridDim.x); r++) n += *cluster.map_shared_rank(sh_count + a.experts, r);
+    const bool there = lane < int(gridDim.x);
+    const int n = __reduce_add_sync(0xffffffffu,
+                                    there ? *cluster.map_shared_rank(sh_count + a.experts, there ? lane : 0) : 0);
     finish<kWarps>(a, int(gridDim.x), [&](int r, int e) { return cluster.map_shared_rank(sh_sum, r)[e]; },
            [&](int r, int e) { return cluster.map_shared_rank(sh_count, r)[e]; }, n);
 }
