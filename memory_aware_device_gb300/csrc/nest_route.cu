@@ -6,15 +6,61 @@ namespace nest {
 
 namespace {
 
-__global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(RouteArgs a, int blocks) {
-    cg::this_cluster().sync();   // every block has started; while the rows are still being written
+constexpr int kFinishWarps = 32;
+
+// The results from the blocks' rows of sums and counts, by the blocks of a cluster: each takes
+// groups of 32 experts.  A warp adds every 32nd row, then a warp adds an expert's 32 parts as
+// a tree.
+__global__ void __launch_bounds__(32 * kFinishWarps) route_finish_kernel(RouteArgs a, int rows) {
+    __shared__ float sh_p[kFinishWarps][33], sh_dot[kFinishWarps], sh_all[kCluster];
+    __shared__ int32_t sh_c[kFinishWarps][33];
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();   // every block has started; while the rows are still being written
     pdl_wait();
     pdl_trigger();
-    int32_t n = 0;
-    for (int b = threadIdx.x & 31; b < blocks; b += 32) n += a.part_n[b];
-    n = __reduce_add_sync(0xffffffffu, n);
-    finish<kFinishThreads / 32>(a, blocks, [&](int r, int e) { return a.part_p[int64_t(r) * a.experts + e]; },
-           [&](int r, int e) { return a.part_c[int64_t(r) * a.experts + e]; }, n);
+    const int rank = int(blockIdx.x), ranks = int(gridDim.x);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n = 0;
+    for (int r = lane; r < rows; r += 32) n += a.part_n[r];
+    float dot = 0.0f;
+    for (int first = 32 * rank; first < a.experts; first += 32 * ranks) {
+        float p = 0.0f;
+        int32_t c = 0;
+        if (first + lane < a.experts) {
+#pragma unroll 4
+            for (int r = warp; r < rows; r += kFinishWarps) {
+                p += a.part_p[int64_t(r) * a.experts + first + lane];
+                c += a.part_c[int64_t(r) * a.experts + first + lane];
+            }
+        }
+        sh_p[warp][lane] = p;
+        sh_c[warp][lane] = c;
+        __syncthreads();
+        p = warp_sum(sh_p[lane][warp]);
+        c = __reduce_add_sync(0xffffffffu, sh_c[lane][warp]);
+        if (first == 32 * rank) n = __reduce_add_sync(0xffffffffu, n);
+        p *= n ? 1.0f / float(n) : 0.0f;
+        if (lane == 0 && first + warp < a.experts) {
+            a.counts[first + warp] = c;
+            a.mean_prob[first + warp] = p;
+        }
+        dot = fmaf(p, float(c), dot);   // 0 past the last expert
+        __syncthreads();
+    }
+    if (lane == 0) sh_dot[warp] = dot;
+    __syncthreads();
+    if (warp == 0) {
+        dot = warp_sum(sh_dot[lane]);
+        if (lane == 0) *cluster.map_shared_rank(sh_all + rank, 0) = dot;
+    }
+    cluster.sync();
+    if (rank == 0 && warp == 0) {
+        dot = warp_sum(lane < ranks ? sh_all[lane < ranks ? lane : 0] : 0.0f);
+        if (lane == 0) {
+            *a.live = n;
+            *a.loss = loss_of(a, dot, n);
+        }
+    }
 }
 
 int check(const nest_route_desc *d) {
@@ -25,21 +71,24 @@ int check(const nest_route_desc *d) {
     return NEST_OK;
 }
 
-// Blocks of the forward kernel, and whether they are one cluster: up to kJoined passes of it over
-// the rows are quicker than a second launch.
+// The forward kernel's blocks and threads, and whether the blocks are one cluster: up to
+// kJoined passes of it over the rows are quicker than a second launch.  A single block is no
+// larger than its rows need.
 constexpr int kJoined = 4;
 struct Grid {
-    int blocks;
+    int blocks, threads;
     bool joined;
 };
 Grid grid_of(const nest_route_desc *d) {
     Grid g;
     with_row(d->experts, [&](auto lanes, auto values) {
         using S = RouteShape<decltype(values)::v>;
-        constexpr int kRows = S::kWarps * 32 / decltype(lanes)::v;
+        constexpr int kPerWarp = 32 / decltype(lanes)::v, kRows = S::kWarps * kPerWarp;
         const int64_t b = (d->tokens + kRows - 1) / kRows, most = kSMs * S::kPerSm;
+        const int64_t warps = (d->tokens + kPerWarp - 1) / kPerWarp;
         g.joined = b <= kJoined * kCluster;
         g.blocks = int(b < 1 ? 1 : g.joined && b > kCluster ? kCluster : b < most ? b : most);
+        g.threads = 32 * int(warps < 1 ? 1 : warps < S::kWarps ? warps : S::kWarps);
         return 0;
     });
     return g;
@@ -91,12 +140,12 @@ int nest_route(const nest_route_desc *d, const void *logits, const uint8_t *mask
     a.mean_prob = mean_prob;
     a.loss = loss;
     a.joined = g.joined;
-    const int rc = d->dtype == NEST_F32    ? launch_route_f32(a, g.blocks, stream)
-                   : d->dtype == NEST_BF16 ? launch_route_bf16(a, g.blocks, stream)
-                                           : launch_route_f16(a, g.blocks, stream);
+    const int rc = d->dtype == NEST_F32    ? launch_route_f32(a, g.blocks, g.threads, stream)
+                   : d->dtype == NEST_BF16 ? launch_route_bf16(a, g.blocks, g.threads, stream)
+                                           : launch_route_f16(a, g.blocks, g.threads, stream);
     if (rc || g.joined) return rc;
     const int groups = (d->experts + 31) / 32, cluster = groups < kCluster ? groups : kCluster;
-    return launch_kernel(route_finish_kernel, dim3(cluster), dim3(kFinishThreads), 0, stream, cluster,
+    return launch_kernel(route_finish_kernel, dim3(cluster), dim3(32 * kFinishWarps), 0, stream, cluster,
                          "route finish launch", a, g.blocks);
 }
 

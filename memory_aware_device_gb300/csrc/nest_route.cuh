@@ -49,13 +49,14 @@ struct RouteArgs {
     bool vector_grad;
 };
 
-// Block size and blocks per SM that the kernels are compiled for, by the values per lane: the
-// registers of the values, of their words and of the sums.
+// Largest block and blocks per SM that the kernels are compiled for, by the values per lane: the
+// registers of the values, of their words and of the sums.  The forward kernel takes any whole
+// number of warps up to that.
 template <int V>
 struct RouteShape {
-    static constexpr int kWarps = 16;
+    static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 12 : 16;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kPerSm = V <= 8 ? 2 : 1;
+    static constexpr int kPerSm = V == 16 ? 2 : 1;
 };
 template <int V>
 struct BackwardShape {
@@ -68,7 +69,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kFinishThreads = 1024;
 constexpr int kCluster = 8;
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -205,17 +205,23 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 template <int LANES>
 __device__ __forceinline__ float row_max(float v) {   // NaN counts as nothing
-    if constexpr (LANES == 32) return warp_max(v);
+    if constexpr (LANES == 32) {
+        return warp_max(v);
+    } else {
 #pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+        for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    }
 }
 template <int LANES, typename U>
 __device__ __forceinline__ U row_largest(U v) {
-    if constexpr (LANES == 32 && sizeof(U) == 4) return __reduce_max_sync(0xffffffffu, v);
+    if constexpr (LANES == 32 && sizeof(U) == 4) {
+        return __reduce_max_sync(0xffffffffu, v);
+    } else {
 #pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+        for (int o = LANES / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    }
 }
 // Whether any lane of the row says so.
 template <int LANES>
@@ -380,78 +386,32 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
         choose_exactly<T, V, LANES, SLOTS>(a, row, again && !idle, id);
 }
 
-// The results from `rows` rows of sums and counts, row_p(r, e) and row_c(r, e), and n live rows,
-// by the blocks of a cluster that have all started: each takes groups of 32 experts.  A warp
-// adds every WARPS-th row, then a warp adds an expert's WARPS parts as a tree.
-template <int WARPS, typename P, typename N>
-__device__ __forceinline__ void finish(const RouteArgs &a, int rows, P row_p, N row_c, int n) {
-    __shared__ float sh_p[WARPS][33], sh_dot[WARPS], sh_all[kCluster];
-    __shared__ int32_t sh_c[WARPS][33];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = int(cluster.block_rank()), ranks = int(cluster.num_blocks());
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float over = n ? 1.0f / float(n) : 0.0f;
-    float dot = 0.0f;
-    for (int first = 32 * rank; first < a.experts; first += 32 * ranks) {
-        float p = 0.0f;
-        int32_t c = 0;
-        if (first + lane < a.experts) {
-#pragma unroll 4
-            for (int r = warp; r < rows; r += WARPS) {
-                p += row_p(r, first + lane);
-                c += row_c(r, first + lane);
-            }
-        }
-        sh_p[warp][lane] = p;
-        sh_c[warp][lane] = c;
-        __syncthreads();
-        for (int e = warp; e < 32 && first + e < a.experts; e += WARPS) {
-            p = warp_sum(lane < WARPS ? sh_p[lane < WARPS ? lane : 0][e] : 0.0f) * over;
-            c = __reduce_add_sync(0xffffffffu, lane < WARPS ? sh_c[lane < WARPS ? lane : 0][e] : 0);
-            if (lane == 0) {
-                a.counts[first + e] = c;
-                a.mean_prob[first + e] = p;
-            }
-            dot = fmaf(p, float(c), dot);
-        }
-        __syncthreads();
-    }
-    if (lane == 0) sh_dot[warp] = dot;
-    __syncthreads();
-    if (warp == 0) {
-        dot = warp_sum(lane < WARPS ? sh_dot[lane < WARPS ? lane : 0] : 0.0f);
-        if (lane == 0) *cluster.map_shared_rank(sh_all + rank, 0) = dot;
-    }
-    cluster.sync();   // also keeps every block's sums until all have read them
-    if (rank == 0 && warp == 0) {
-        dot = warp_sum(lane < ranks ? sh_all[lane < ranks ? lane : 0] : 0.0f);
-        if (lane == 0) {
-            *a.live = n;
-            *a.loss = n ? dot * float(a.experts) / (float(a.k) * float(n)) : 0.0f;
-        }
-    }
+// From the sum over experts of count * mean.
+__device__ __forceinline__ float loss_of(const RouteArgs &a, float dot, int n) {
+    return n ? dot * float(a.experts) / (float(a.k) * float(n)) : 0.0f;
 }
 
 template <typename T, int LANES, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
-    constexpr int kWarps = RouteShape<V>::kWarps, kThreads = RouteShape<V>::kThreads;
     constexpr int kRows = 32 / LANES, kSlots = FEW ? 1 : 32 / LANES;
     constexpr uint32_t kIndex = LANES * V - 1;
     using L = Place<V, VEC, LANES>;
     extern __shared__ unsigned char sh[];
-    float *sh_sum = reinterpret_cast<float *>(sh);                            // [kWarps][experts]
-    int32_t *sh_count = reinterpret_cast<int32_t *>(sh_sum + kWarps * a.experts);   // [experts], then live rows
+    __shared__ float sh_dot[32], sh_all[kCluster];
+    const int threads = blockDim.x, warps = threads >> 5;
+    float *sh_sum = reinterpret_cast<float *>(sh);                            // [warps][experts]
+    int32_t *sh_count = reinterpret_cast<int32_t *>(sh_sum + warps * a.experts);   // [experts], then live rows
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane & (LANES - 1);
-    const int64_t stride = int64_t(gridDim.x) * kWarps * kRows;
-    for (int e = threadIdx.x; e <= a.experts; e += kThreads) sh_count[e] = 0;
+    const int64_t stride = int64_t(gridDim.x) * warps * kRows;
+    for (int e = threadIdx.x; e <= a.experts; e += threads) sh_count[e] = 0;
     __syncthreads();
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; i++) acc[i] = 0.0f;
     int live = 0;
-    for (int64_t first = (int64_t(blockIdx.x) * kWarps + warp) * kRows; first < a.tokens; first += stride) {
+    for (int64_t first = (int64_t(blockIdx.x) * warps + warp) * kRows; first < a.tokens; first += stride) {
         const int64_t t = first + lane / LANES;
         const bool in = t < a.tokens, on = in && !(a.mask && !a.mask[t]);
         const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
@@ -541,10 +501,10 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
     live = __reduce_add_sync(0xffffffffu, g ? 0 : live);
     if (lane == 0 && live) atomicAdd(&sh_count[a.experts], live);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+    for (int e = threadIdx.x; e < a.experts; e += threads) {
         float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; w++) s += sh_sum[w * a.experts + e];
+#pragma unroll 4
+        for (int w = 0; w < warps; w++) s += sh_sum[w * a.experts + e];
         if (a.joined) {
             sh_sum[e] = s;   // only this thread reads this column
         } else {
@@ -556,13 +516,43 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
         if (threadIdx.x == 0) a.part_n[blockIdx.x] = sh_count[a.experts];
         return;
     }
+    // the cluster's blocks share the experts, and the first one the loss
     cg::cluster_group cluster = cg::this_cluster();
+    const int rank = int(blockIdx.x), ranks = int(gridDim.x);
     cluster.sync();
-    const bool there = lane < int(gridDim.x);
-    const int n = __reduce_add_sync(0xffffffffu,
-                                    there ? *cluster.map_shared_rank(sh_count + a.experts, there ? lane : 0) : 0);
-    finish<kWarps>(a, int(gridDim.x), [&](int r, int e) { return cluster.map_shared_rank(sh_sum, r)[e]; },
-           [&](int r, int e) { return cluster.map_shared_rank(sh_count, r)[e]; }, n);
+    const int n = __reduce_add_sync(
+        0xffffffffu, lane < ranks ? *cluster.map_shared_rank(sh_count + a.experts, lane < ranks ? lane : 0) : 0);
+    const float over = n ? 1.0f / float(n) : 0.0f;
+    float dot = 0.0f;
+    for (int e = rank * threads + int(threadIdx.x); e < a.experts; e += ranks * threads) {
+        float p = 0.0f;
+        int32_t c = 0;
+#pragma unroll
+        for (int r = 0; r < kCluster; r++)
+            if (r < ranks) {
+                p += cluster.map_shared_rank(sh_sum, r)[e];
+                c += cluster.map_shared_rank(sh_count, r)[e];
+            }
+        p *= over;
+        a.counts[e] = c;
+        a.mean_prob[e] = p;
+        dot = fmaf(p, float(c), dot);
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) sh_dot[warp] = dot;
+    __syncthreads();
+    if (warp == 0) {
+        dot = warp_sum(lane < warps ? sh_dot[lane] : 0.0f);
+        if (lane == 0) *cluster.map_shared_rank(sh_all + rank, 0) = dot;
+    }
+    cluster.sync();   // also keeps every block's sums until all have read them
+    if (rank == 0 && warp == 0) {
+        dot = warp_sum(lane < ranks ? sh_all[lane < ranks ? lane : 0] : 0.0f);
+        if (lane == 0) {
+            *a.live = n;
+            *a.loss = loss_of(a, dot, n);
+        }
+    }
 }
 
 // The gradient.  With the weights w that the forward pass wrote, what reaches a chosen logit
@@ -689,11 +679,10 @@ bool vector_rows(const RouteArgs &a) {
 
 // Launches of one element type (each in its own translation unit).
 template <typename T>
-int launch_route_type(const RouteArgs &a, int blocks, void *stream) {
+int launch_route_type(const RouteArgs &a, int blocks, int threads, void *stream) {
     return with_row(a.experts, [&](auto lanes, auto values) {
         constexpr int L = decltype(lanes)::v, V = decltype(values)::v;
-        using S = RouteShape<V>;
-        const size_t smem = size_t(4) * (S::kWarps * a.experts + a.experts + 1);
+        const size_t smem = size_t(4) * (threads / 32 * a.experts + a.experts + 1);
         const bool vec = vector_rows<T, V>(a), few = a.k <= 8;
         auto kernel = vec ? (few ? route_kernel<T, L, V, true, true> : route_kernel<T, L, V, true, false>)
                           : (few ? route_kernel<T, L, V, false, true> : route_kernel<T, L, V, false, false>);
@@ -702,8 +691,7 @@ int launch_route_type(const RouteArgs &a, int blocks, void *stream) {
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)), "route attribute");
             if (rc) return rc;
         }
-        return launch_kernel(kernel, dim3(blocks), dim3(S::kThreads), smem, stream, a.joined ? blocks : 1,
-                             "route launch", a);
+        return launch_kernel(kernel, dim3(blocks), dim3(threads), smem, stream, a.joined ? blocks : 1, "route launch", a);
     });
 }
 
@@ -722,9 +710,9 @@ int launch_route_backward_type(RouteArgs a, void *stream) {
     });
 }
 
-int launch_route_f32(const RouteArgs &a, int blocks, void *stream);
-int launch_route_bf16(const RouteArgs &a, int blocks, void *stream);
-int launch_route_f16(const RouteArgs &a, int blocks, void *stream);
+int launch_route_f32(const RouteArgs &a, int blocks, int threads, void *stream);
+int launch_route_bf16(const RouteArgs &a, int blocks, int threads, void *stream);
+int launch_route_f16(const RouteArgs &a, int blocks, int threads, void *stream);
 int launch_route_backward_f32(const RouteArgs &a, void *stream);
 int launch_route_backward_bf16(const RouteArgs &a, void *stream);
 int launch_route_backward_f16(const RouteArgs &a, void *stream);

@@ -4,8 +4,8 @@
 
 namespace nest {
 
-int launch_route_bf16(const RouteArgs &a, int blocks, void *stream) {
-    return launch_route_type<__nv_bfloat16>(a, blocks, stream);
+int launch_route_bf16(const RouteArgs &a, int blocks, int threads, void *stream) {
+    return launch_route_type<__nv_bfloat16>(a, blocks, threads, stream);
 }
 
 int launch_route_backward_bf16(const RouteArgs &a, void *stream) {

@@ -4,8 +4,8 @@
 
 namespace nest {
 
-int launch_route_f32(const RouteArgs &a, int blocks, void *stream) {
-    return launch_route_type<float>(a, blocks, stream);
+int launch_route_f32(const RouteArgs &a, int blocks, int threads, void *stream) {
+    return launch_route_type<float>(a, blocks, threads, stream);
 }
 
 int launch_route_backward_f32(const RouteArgs &a, void *stream) {

@@ -85,9 +85,24 @@ def _check(rc: int, what: str):
         raise NestError(rc, what)
 
 
-def _type(t, what: str) -> int:
+_torch = _codes = _raw_stream = None
+
+
+def _load_torch():
+    """torch, imported at the first call, with what every call looks up."""
+    global _torch, _codes, _raw_stream
     import torch
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    _codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _type(t, what: str) -> int:
+    if _torch is None:
+        _load_torch()
+    code = _codes.get(t.dtype)
     if code is None:
         raise TypeError(f"{what} is {t.dtype}: float32, bfloat16 and float16 are supported")
     return code
@@ -95,40 +110,59 @@ def _type(t, what: str) -> int:
 
 def _want(t, what: str, dtype, shape, device):
     """t as a contiguous tensor of this type, shape and device, or an error."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
     return t
 
 
 class _On:
-    """The device of a call made current, and its stream: the device's current one, or the one
-    given, which is made current too (new tensors belong to it) and recorded as a user of `used`."""
+    """Makes a call's device current, and the stream given (new tensors belong to it), which is
+    recorded as a user of `used`; entered, the stream's handle."""
 
     def __init__(self, device, stream, used=()):
         import torch
-        if device.type != "cuda":
-            raise ValueError(f"tensors are on {device}: the operators run on CUDA devices only")
         self.guards = []
-        if device.index is not None and device.index != torch.cuda.current_device():
+        if device.index != torch.cuda.current_device():
             self.guards.append(torch.cuda.device(device))
-        if stream is not None and stream != torch.cuda.current_stream(device):
+        if stream is not None:
             self.guards.append(torch.cuda.stream(stream))
-            for t in used:
-                if t is not None:
-                    t.record_stream(stream)
-        self.device, self.stream = device, stream
+            if stream != torch.cuda.current_stream(device):
+                for t in used:
+                    if t is not None:
+                        t.record_stream(stream)
+        self.index = device.index
 
     def __enter__(self):
-        import torch
         for g in self.guards:
             g.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return C.c_void_p(s.cuda_stream)
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
+
+
+class _Here:
+    """The current device and stream as they are."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        return _raw_stream(self.index)
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _on(device, stream, used=()):
+    torch = _torch or _load_torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}: the operators run on CUDA devices only")
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(device.index)
+    return _On(device, stream, used)
 
 
 # ---------------------------------------------------------------------------------
@@ -146,25 +180,54 @@ class Routing(NamedTuple):
 
     @staticmethod
     def empty(tokens: int, experts: int, k: int, device="cuda") -> "Routing":
-        """Uninitialised result buffers, for `route(..., out=)`."""
+        """Uninitialised result buffers, and the workspace of calls into them, for `route(..., out=)`."""
         import torch
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         i, f = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
-        return Routing(torch.empty((tokens, k), **i), torch.empty((tokens, k), **f), torch.empty(experts, **i),
+        out = _Buffers(torch.empty((tokens, k), **i), torch.empty((tokens, k), **f), torch.empty(experts, **i),
                        torch.empty(1, **i), torch.empty(experts, **f), torch.empty((), **f))
+        out.call = _RouteCall(tokens, experts, k, device, out)
+        return out
+
+
+class _Buffers(Routing):
+    """Buffers of `Routing.empty`, with the arguments of calls that write them."""
+    call = None
+
+
+def _route_workspace(ref) -> int:
+    size = lib().nest_route_workspace_size(ref)
+    if not size:   # the call says which limit is broken
+        _check(lib().nest_route(ref, None, None, None, None, None, None, None, None, None, 0, None), "nest_route")
+    return size
+
+
+class _RouteCall:
+    """The arguments of nest_route that stay the same for given sizes and result buffers."""
+
+    def __init__(self, tokens, experts, k, device, out):
+        import torch
+        self.key = (tokens, experts, k, device)
+        self.desc = RouteDesc(tokens, experts, k, 0, 0, F32, 0)
+        self.ref = C.byref(self.desc)
+        size = _route_workspace(self.ref)
+        self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        self.out = tuple(t.data_ptr() for t in out) + (self.workspace.data_ptr(), size)
 
 
 def _route_desc(logits, k: int, normalize: bool) -> RouteDesc:
     if logits.dim() != 2:
         raise ValueError(f"logits must be [tokens, experts], not of shape {tuple(logits.shape)}")
     T, E = logits.shape
-    return RouteDesc(T, E, k, logits.stride(0), logits.stride(1), _type(logits, "logits"), int(bool(normalize)))
+    return RouteDesc(T, E, k, logits.stride(0), logits.stride(1), _type(logits, "logits"), 1 if normalize else 0)
 
 
 def _mask_ptr(mask, logits):
-    import torch
     if mask is None:
         return None
-    if mask.dtype not in (torch.bool, torch.uint8):
+    if mask.dtype not in (_torch.bool, _torch.uint8):
         raise TypeError(f"mask is {mask.dtype}: bool and uint8 are supported")
     return _want(mask, "mask", mask.dtype, logits.shape[:1], logits.device).data_ptr()
 
@@ -173,28 +236,38 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
     """nest_route: softmax gates of the k best experts per token, counts and balance loss.
 
     logits [T, E] (any strides; float32, bfloat16 or float16); mask [T] (bool or uint8, True = the
-    token counts); normalize: gates of a token sum to 1.  out: buffers to write instead of new ones."""
-    import torch
-    d = _route_desc(logits, k, normalize)
-    L = lib()
-    ws_bytes = L.nest_route_workspace_size(C.byref(d))
-    if not ws_bytes:   # the call says which limit is broken
-        _check(L.nest_route(C.byref(d), None, None, None, None, None, None, None, None, None, 0, None), "nest_route")
-    T, E, dev = logits.shape[0], logits.shape[1], logits.device
-    with _On(dev, stream, (logits, mask) + tuple(out or ())) as s:
+    token counts); normalize: gates of a token sum to 1.  out: buffers to write instead of new ones
+    (quickest those of `Routing.empty`); calls that overlap on the GPU need buffers of their own."""
+    dtype = _type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [tokens, experts], not of shape {tuple(logits.shape)}")
+    T, E = logits.shape
+    dev = logits.device
+    call = getattr(out, "call", None)
+    if call is None or call.key != (T, E, k, dev):
+        call = None
+        _route_workspace(C.byref(RouteDesc(T, E, k, 0, 0, dtype, 0)))
+    with _on(dev, stream, (logits, mask) + tuple(out or ())) as s:
         if out is None:
             out = Routing.empty(T, E, k, dev)
-        else:
+            call = out.call
+        elif call is None:
+            torch = _torch
             _want(out.ids, "out.ids", torch.int32, (T, k), dev)
             _want(out.weights, "out.weights", torch.float32, (T, k), dev)
             _want(out.counts, "out.counts", torch.int32, (E,), dev)
             _want(out.tokens, "out.tokens", torch.int32, (1,), dev)
             _want(out.mean_prob, "out.mean_prob", torch.float32, (E,), dev)
             _want(out.loss, "out.loss", torch.float32, (), dev)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        rc = L.nest_route(C.byref(d), logits.data_ptr(), _mask_ptr(mask, logits), out.ids.data_ptr(),
-                          out.weights.data_ptr(), out.counts.data_ptr(), out.tokens.data_ptr(),
-                          out.mean_prob.data_ptr(), out.loss.data_ptr(), ws.data_ptr(), ws_bytes, s)
+            call = _RouteCall(T, E, k, dev, out)
+        elif stream is not None:
+            call.workspace.record_stream(stream)
+        d = call.desc
+        d.row_stride, d.col_stride = logits.stride()
+        d.dtype = dtype
+        d.normalize = 1 if normalize else 0
+        rc = _lib.nest_route(call.ref, logits.data_ptr(), None if mask is None else _mask_ptr(mask, logits),
+                             *call.out, s)
     _check(rc, "nest_route")
     return out
 
@@ -204,34 +277,32 @@ def route_backward(logits, routing: Routing, grad_weights=None, grad_loss=None, 
     """nest_route_backward: gradient with respect to the logits, in their type, from the gradients
     of the weights (float32 [T, k]) and of the loss (float32 scalar tensor); None counts as zero.
     routing, mask and normalize as in the forward call."""
-    import torch
-    T, E = logits.shape if logits.dim() == 2 else (0, 0)
-    dev = logits.device
     d = _route_desc(logits, routing.ids.shape[-1], normalize)
+    torch, dev = _torch, logits.device
+    T, E, k = d.tokens, d.experts, d.k
+    ids, weights, counts, tokens = routing[:4]
     if T:   # an empty batch reads none of them
-        _want(routing.ids, "routing.ids", torch.int32, (T, d.k), dev)
-        _want(routing.weights, "routing.weights", torch.float32, (T, d.k), dev)
-        _want(routing.counts, "routing.counts", torch.int32, (E,), dev)
-        _want(routing.tokens, "routing.tokens", torch.int32, (1,), dev)
+        _want(ids, "routing.ids", torch.int32, (T, k), dev)
+        _want(weights, "routing.weights", torch.float32, (T, k), dev)
+        _want(counts, "routing.counts", torch.int32, (E,), dev)
+        _want(tokens, "routing.tokens", torch.int32, (1,), dev)
     if grad_weights is not None:
-        _want(grad_weights, "grad_weights", torch.float32, (T, d.k), dev)
+        _want(grad_weights, "grad_weights", torch.float32, (T, k), dev)
     if grad_loss is not None:
         _want(grad_loss, "grad_loss", torch.float32, grad_loss.shape, dev)
         if grad_loss.numel() != 1:
             raise ValueError(f"grad_loss must be one number, not of shape {tuple(grad_loss.shape)}")
-    used = (logits, mask, routing.ids, routing.weights, routing.counts, routing.tokens, grad_weights, grad_loss, out)
-    with _On(dev, stream, used) as s:
+    used = (logits, mask, ids, weights, counts, tokens, grad_weights, grad_loss, out)
+    with _on(dev, stream, used) as s:
         if out is None:
             out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        elif out.dtype != logits.dtype or tuple(out.shape) != (T, E) or out.device != dev or \
+        elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev or \
                 (E > 1 and out.stride(1) != 1) or (T > 1 and out.stride(0) < E):
             raise ValueError(f"out must be a {logits.dtype} tensor of shape {(T, E)} on {dev} with rows of its own")
         rc = lib().nest_route_backward(
-            C.byref(d), logits.data_ptr(), _mask_ptr(mask, logits), routing.ids.data_ptr(),
-            routing.weights.data_ptr(), routing.counts.data_ptr(), routing.tokens.data_ptr(),
-            grad_weights.data_ptr() if grad_weights is not None else None,
-            grad_loss.data_ptr() if grad_loss is not None else None,
-            out.data_ptr(), max(out.stride(0), E), s)
+            C.byref(d), logits.data_ptr(), _mask_ptr(mask, logits), ids.data_ptr(), weights.data_ptr(),
+            counts.data_ptr(), tokens.data_ptr(), None if grad_weights is None else grad_weights.data_ptr(),
+            None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), max(out.stride(0), E), s)
     _check(rc, "nest_route_backward")
     return out
 
@@ -324,11 +395,12 @@ class _Table:
         ws = lib().nest_grad_norm_workspace_size(C.byref(self.info))
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
         self.out = torch.empty(2, dtype=torch.float32, device=self.device)
+        self.head = (C.byref(self.info), self.table.data_ptr())
+        self.tail = (self.out.data_ptr(), self.workspace.data_ptr(), ws)
 
     def norm(self, max_norm, stream):
-        with _On(self.device, stream) as s:
-            rc = lib().nest_grad_norm(C.byref(self.info), self.table.data_ptr(), self.grad_type, max_norm,
-                                      self.out.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(), s)
+        with _on(self.device, stream) as s:
+            rc = _lib.nest_grad_norm(*self.head, self.grad_type, max_norm, *self.tail, s)
         _check(rc, "nest_grad_norm")
         return self.out
 
@@ -383,6 +455,7 @@ class AdamW:
         self._args = AdamWArgs(weight_type, tb.grad_type, state_bits, seed & 0xFFFFFFFF, 0.0, betas[0], betas[1], eps,
                                ptr(self.master), ptr(self.m), ptr(self.v), ptr(self.m_exp), ptr(self.v_exp),
                                self._state.data_ptr(), None)
+        self._ref = C.byref(self._args)
         self.set_step(0)
 
     def set_step(self, step: int):
@@ -412,17 +485,16 @@ class AdamW:
     def step(self, lr: float, grad_scale=None, stream=None):
         """One step.  grad_scale: float32 CUDA scalar that multiplies the gradients (entry 1 of
         `grad_norm`); when it is not finite the call changes nothing."""
-        import torch
         a, tb = self._args, self._table
         if grad_scale is None:
             a.grad_scale = None
         else:
-            if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.device != tb.device:
+            if _codes.get(grad_scale.dtype) != F32 or grad_scale.numel() != 1 or grad_scale.device != tb.device:
                 raise ValueError(f"grad_scale must be one float32 number on {tb.device}")
             a.grad_scale = grad_scale.data_ptr()
         a.lr = lr
-        with _On(tb.device, stream, () if grad_scale is None else (grad_scale,)) as s:
-            rc = lib().nest_adamw(C.byref(tb.info), tb.table.data_ptr(), C.byref(a), s)
+        with _on(tb.device, stream, () if grad_scale is None else (grad_scale,)) as s:
+            rc = _lib.nest_adamw(*tb.head, self._ref, s)
         _check(rc, "nest_adamw")
 
     def state_values(self, stream=None):
@@ -432,9 +504,9 @@ class AdamW:
         if self.state_bits == 32:
             return self.m, self.v
         tb = self._table
-        with _On(tb.device, stream, (self.m, self.v, self.m_exp, self.v_exp)) as s:
+        with _on(tb.device, stream, (self.m, self.v, self.m_exp, self.v_exp)) as s:
             m, v = (torch.empty(self.m.numel(), dtype=torch.bfloat16, device=tb.device) for _ in "mv")
-            rc = lib().nest_adamw_values(C.byref(tb.info), self.m.data_ptr(), self.v.data_ptr(),
+            rc = _lib.nest_adamw_values(tb.head[0], self.m.data_ptr(), self.v.data_ptr(),
                                          self.m_exp.data_ptr(), self.v_exp.data_ptr(), m.data_ptr(), v.data_ptr(), s)
         _check(rc, "nest_adamw_values")
         return m, v
