@@ -121,8 +121,8 @@ int nest_table_pack(const nest_tensor *tensors, int32_t n, const nest_table_info
 /* ---- gradient norm -----------------------------------------------------------------
  *   out[0] = sqrt(sum over all tensors of grad^2)
  *   out[1] = min(1, max_norm / (out[0] + 1e-6)), NaN when out[0] is not finite
- * Squares are summed in 32 bits within a thread's share of an item and in 64 bits above
- * that; gradients beyond 1.8e19 overflow to an infinite norm.
+ * Squares are summed in 32 bits, with the rounding errors of the long sums added up beside
+ * them; gradients beyond 1.8e19 overflow to an infinite norm.
  *   out   DEVICE float [2];  max_norm > 0 (may be infinite: out[1] = 1)              */
 size_t nest_grad_norm_workspace_size(const nest_table_info *info);
 int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_type, float max_norm,

@@ -109,16 +109,37 @@ __device__ __forceinline__ void store_block(T *p, int n, bool vector, int lane, 
 
 // ---- gradient norm ----------------------------------------------------------------
 
+// A sum in 32 bits with the rounding error of every addition added up beside it (Knuth's
+// exact sum of two numbers): 64-bit additions are 64 times slower here, and one for every
+// item and thread took a quarter of the kernel's time.
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = hi + x, b = s - hi;
+        lo += (hi - (s - b)) + (x - b);
+        hi = s;
+    }
+    __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+};
+
+// The block's sum of its threads' values, in thread 0.
+__device__ __forceinline__ float block_sum(float v, float *sh) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum(threadIdx.x < kWarps ? sh[threadIdx.x] : 0.0f);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const void *table, int tensors, int items, double *part) {
-    __shared__ double sh[kWarps];
+__global__ void __launch_bounds__(kThreads) norm_kernel(const void *table, int tensors, int items, float *part) {
+    __shared__ float sh[kWarps];
     __shared__ __align__(16) float room[kWarps][kBlock];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Entry *entries = static_cast<const Entry *>(table);
     const Item *list = items_of(table, tensors);
-    double sum = 0.0;
+    Sum sum;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
         const Item item = list[it];
         const T *g = static_cast<const T *>(entries[item.tensor].grad);
@@ -134,32 +155,23 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const void *table, int t
 #pragma unroll
             for (int i = 0; i < 8; i++) s = fmaf(x[i], x[i], s);
         }
-        sum += s;
+        sum.add(s);
     }
-    sum = warp_sum(sum);
-    if (lane == 0) sh[warp] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int w = 0; w < kWarps; w++) s += sh[w];
-        part[blockIdx.x] = s;
-    }
+    const float s = block_sum(sum.value(), sh);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(kThreads) norm_finish_kernel(const double *part, int blocks, float max_norm,
+__global__ void __launch_bounds__(kThreads) norm_finish_kernel(const float *part, int blocks, float max_norm,
                                                                float *out) {
-    __shared__ double sh[kWarps];
+    __shared__ float sh[kWarps];
     pdl_wait();
     pdl_trigger();
-    double s = 0.0;
-    for (int b = threadIdx.x; b < blocks; b += kThreads) s += part[b];
-    s = warp_sum(s);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
-    __syncthreads();
+    Sum sum;
+#pragma unroll 8
+    for (int b = threadIdx.x; b < blocks; b += kThreads) sum.add(part[b]);
+    const float s = block_sum(sum.value(), sh);
     if (threadIdx.x == 0) {
-        s = 0.0;
-        for (int w = 0; w < kWarps; w++) s += sh[w];
-        const float norm = float(sqrt(s));
+        const float norm = sqrtf(s);
         out[0] = norm;
         out[1] = isfinite(norm) ? fminf(1.0f, max_norm / (norm + 1e-6f)) : NAN;
     }
@@ -200,29 +212,31 @@ __device__ __forceinline__ uint32_t code_of(float y, uint32_t r, float small) {
     return __float_as_uint(y) < (uint32_t(OFFSET + 1) << 23) ? fixed : normal;
 }
 
-// Codes of a lane's eight moments.  rare: the block holds one that is not finite, or whose scale
-// is clipped, and codes are checked against the largest.
-__device__ __forceinline__ uint2 encode_m(const float (&m)[8], int s, const uint32_t (&noise)[8], bool rare) {
-    const float f = power2(8 - s);
-    uint32_t c[8];
+// Codes of a lane's eight pairs of moments; word: the block's noise.  rare: the block holds one
+// that is not finite, or whose scale is clipped, and codes are checked against the largest.
+template <bool RARE>
+__device__ __forceinline__ void encode(const float (&m)[8], const float (&v)[8], int sm, int sv, uint32_t word,
+                                       int lane, uint2 &cm, uint2 &cv) {
+    const float fm = power2(8 - sm), fv = power2(-1 - sv);
+    uint32_t pm[2] = {0, 0}, pv[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        c[i] = code_of<120>(fabsf(m[i]) * f, noise[i] >> 16, 512.0f);
-        if (rare) c[i] = isfinite(m[i]) ? min(c[i], 0x7Eu) : 0x7Fu;
-        c[i] |= (__float_as_uint(m[i]) >> 24) & 0x80u;
+        uint32_t x = word + uint32_t(8 * lane + i) * 0x9E3779B1u;
+        x ^= x >> 15;
+        x *= 0x6A09E667u;
+        x ^= x >> 16;
+        uint32_t a = code_of<120>(fabsf(m[i]) * fm, x >> 16, 512.0f);
+        uint32_t b = code_of<95>(v[i] * fv, x & 0xFFFFu, 0x1p34f);
+        if (RARE) {
+            a = isfinite(m[i]) ? min(a, 0x7Eu) : 0x7Fu;
+            b = isfinite(v[i]) ? min(b, 0xFEu) : 0xFFu;
+        }
+        a |= (__float_as_uint(m[i]) >> 24) & 0x80u;
+        pm[i / 4] |= a << (8 * (i % 4));
+        pv[i / 4] |= b << (8 * (i % 4));
     }
-    return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
-}
-
-__device__ __forceinline__ uint2 encode_v(const float (&v)[8], int s, const uint32_t (&noise)[8], bool rare) {
-    const float f = power2(-1 - s);
-    uint32_t c[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        c[i] = code_of<95>(v[i] * f, noise[i] & 0xFFFFu, 0x1p34f);
-        if (rare) c[i] = isfinite(v[i]) ? min(c[i], 0xFEu) : 0xFFu;
-    }
-    return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+    cm = make_uint2(pm[0], pm[1]);
+    cv = make_uint2(pv[0], pv[1]);
 }
 
 // Two codes with 4 exponent bits as two floats: the hardware's e4m3 conversion (0x7F is NaN there too).
@@ -300,23 +314,44 @@ __device__ __forceinline__ void store_own(uint8_t *p, int n, int lane, uint2 c) 
 constexpr uint32_t kRare = (uint32_t(120 + 127) << 23) | 0x600000u;
 
 template <typename W, typename G, bool EIGHT>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(StepArgs a) {
     constexpr bool kOwnMaster = sizeof(W) == 4;
     __shared__ __align__(16) float room[kWarps][kBlock];
+    __shared__ struct {
+        float scale, inv1, root2;
+        uint32_t start;
+    } shared;
     pdl_wait();
     pdl_trigger();
-    const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
-    if (!isfinite(scale)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const double b1t = a.state->beta1_t * a.beta1d, b2t = a.state->beta2_t * a.beta2d;
-    const int64_t step = a.state->step + 1;
-    const float inv1 = 1.0f / float(1.0 - b1t), root2 = rsqrtf(float(1.0 - b2t));
-    const uint32_t start = mixed(a.seed ^ mixed(uint32_t(step)));
     const Entry *entries = static_cast<const Entry *>(a.table);
     const Item *list = items_of(a.table, a.tensors);
-    for (int it = blockIdx.x; it < a.items; it += gridDim.x) {
-        const Item item = list[it];
+    int it = blockIdx.x;
+    Item item = {0, 0};
+    if (it < a.items) item = list[it];
+    if (threadIdx.x == 0) {   // what all share, by one thread: 64-bit arithmetic is slow
+        const nest_adamw_state st = *a.state;
+        shared.scale = a.grad_scale ? *a.grad_scale : 1.0f;
+        shared.inv1 = 1.0f / float(1.0 - st.beta1_t * a.beta1d);
+        shared.root2 = rsqrtf(float(1.0 - st.beta2_t * a.beta2d));
+        shared.start = mixed(a.seed ^ mixed(uint32_t(st.step + 1)));
+    }
+    __syncthreads();
+    const float scale = shared.scale, inv1 = shared.inv1, root2 = shared.root2;
+    const uint32_t start = shared.start;
+    if (!isfinite(scale)) return;
+    // says that this block has read the step's state; the last block to say so advances it at
+    // its end, when the answer has long arrived
+    uint32_t before = 0;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        before = atomicAdd(&a.state->ticket, 1u);
+    }
+    while (it < a.items) {
         const Entry e = entries[item.tensor];
+        it += gridDim.x;
+        Item next = {0, 0};
+        if (it < a.items) next = list[it];
         W *weight = static_cast<W *>(e.weight);
         const G *grad = static_cast<const G *>(e.grad);
         const bool wide_w = wide(weight), wide_g = wide(grad);
@@ -373,19 +408,14 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
                     top_v = __reduce_max_sync(0xffffffffu, top_v);
                 }
                 const int sm = shared_exponent(top_m), sv = shared_exponent(top_v);
-                uint32_t noise[8];
                 const uint32_t word = mixed(start + uint32_t(block) * 0x9E3779B1u);
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    uint32_t x = word + uint32_t(8 * lane + i) * 0x9E3779B1u;
-                    x ^= x >> 15;
-                    x *= 0x6A09E667u;
-                    noise[i] = x ^ (x >> 16);
-                }
-                store_own(static_cast<uint8_t *>(a.m) + at, n, lane,
-                          rare ? encode_m(m, sm, noise, true) : encode_m(m, sm, noise, false));
-                store_own(static_cast<uint8_t *>(a.v) + at, n, lane,
-                          rare ? encode_v(v, sv, noise, true) : encode_v(v, sv, noise, false));
+                uint2 cm, cv;
+                if (rare)
+                    encode<true>(m, v, sm, sv, word, lane, cm, cv);
+                else
+                    encode<false>(m, v, sm, sv, word, lane, cm, cv);
+                store_own(static_cast<uint8_t *>(a.m) + at, n, lane, cm);
+                store_own(static_cast<uint8_t *>(a.v) + at, n, lane, cv);
                 if (lane == 0) {
                     a.m_exp[block] = int8_t(sm);
                     a.v_exp[block] = int8_t(sv);
@@ -395,17 +425,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
                 store_own(static_cast<float *>(a.v) + at, n, lane, v);
             }
         }
+        item = next;
     }
-    // the last block to get here has seen every block read the step's state
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        if (atomicAdd(&a.state->ticket, 1u) == gridDim.x - 1) {
-            a.state->beta1_t = b1t;
-            a.state->beta2_t = b2t;
-            a.state->step = step;
-            a.state->ticket = 0;
-        }
+    if (threadIdx.x == 0 && before == gridDim.x - 1) {
+        a.state->beta1_t *= a.beta1d;
+        a.state->beta2_t *= a.beta2d;
+        a.state->step++;
+        a.state->ticket = 0;
     }
 }
 
@@ -486,7 +512,7 @@ int nest_table_pack(const nest_tensor *t, int32_t n, const nest_table_info *info
 
 size_t nest_grad_norm_workspace_size(const nest_table_info *info) {
     if (check_info(info)) return 0;
-    return (size_t(blocks_for(info->items)) * 8 + 255) & ~size_t(255);
+    return (size_t(blocks_for(info->items)) * 4 + 255) & ~size_t(255);
 }
 
 int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_type, float max_norm, float *out,
@@ -497,14 +523,14 @@ int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_
     if (!workspace || ws_bytes < nest_grad_norm_workspace_size(info) || !aligned_to(workspace, 256))
         return NEST_E_WORKSPACE;
     const int blocks = blocks_for(info->items);
-    double *part = static_cast<double *>(workspace);
+    float *part = static_cast<float *>(workspace);
     const int rc = with_type(grad_type, [&](auto t) {
         return launch_kernel(norm_kernel<decltype(t)>, dim3(blocks), dim3(kThreads), 0, stream, 1, "norm launch", table,
                              int(info->tensors), int(info->items), part);
     });
     if (rc) return rc;
     return launch_kernel(norm_finish_kernel, dim3(1), dim3(kThreads), 0, stream, 1, "norm finish launch",
-                         static_cast<const double *>(part), blocks, max_norm, out);
+                         static_cast<const float *>(part), blocks, max_norm, out);
 }
 
 int nest_adamw(const nest_table_info *info, const void *table, const nest_adamw_args *p, void *stream) {

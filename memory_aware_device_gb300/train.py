@@ -214,7 +214,7 @@ class _RouteCall:
         self.ref = C.byref(self.desc)
         size = _route_workspace(self.ref)
         self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
-        self.out = tuple(t.data_ptr() for t in out) + (self.workspace.data_ptr(), size)
+        self.tail = (self.workspace.data_ptr(), size)
 
 
 def _route_desc(logits, k: int, normalize: bool) -> RouteDesc:
@@ -267,7 +267,7 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
         d.dtype = dtype
         d.normalize = 1 if normalize else 0
         rc = _lib.nest_route(call.ref, logits.data_ptr(), None if mask is None else _mask_ptr(mask, logits),
-                             *call.out, s)
+                             *[t.data_ptr() for t in out], *call.tail, s)
     _check(rc, "nest_route")
     return out
 
