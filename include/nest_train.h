@@ -105,9 +105,9 @@ typedef struct {
 typedef struct {
     int64_t table_bytes; /* of the packed table */
     int64_t blocks;      /* NEST_OPT_BLOCK-element blocks of the list, < 2^31 */
-    int64_t items;       /* units of work */
+    int64_t items;       /* runs of blocks of one tensor that one worker takes */
     int32_t tensors;
-    int32_t reserved;
+    int32_t workers;     /* even shares of the blocks that the kernels are launched over */
 } nest_table_info;
 
 /* Sizes of the packed table of n >= 0 tensors (HOST array). */

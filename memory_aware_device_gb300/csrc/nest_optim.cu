@@ -1,9 +1,10 @@
 // The optimizer's operators over lists of tensors: gradient norm and AdamW step, with
 // moments in 32 or in 8 bits (definitions in nest_train.h).
 //
-// The packed table holds the tensors' entries and a list of items (tensor, first block);
-// an item is up to kItemBlocks blocks of 256 elements of one tensor and is the unit that
-// a thread block takes; a warp takes whole blocks of 256.
+// The list's blocks of 256 elements are divided evenly between workers, which thread blocks
+// take; a worker's blocks are a few segments, each of one tensor, and its warps take every
+// kWarps-th of them, a warp a whole block.  The packed table holds the tensors' entries, the
+// segments in order and where each worker's begin.
 #include <cmath>
 #include <cstring>
 
@@ -14,9 +15,9 @@ namespace nest {
 namespace {
 
 constexpr int kBlock = NEST_OPT_BLOCK;
-constexpr int kItemBlocks = 16;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kWorkers = kSMs * 8;   // at most
 
 struct Entry {            // one tensor
     void *weight;
@@ -26,18 +27,66 @@ struct Entry {            // one tensor
     float weight_decay, lr_scale;
     int64_t pad;
 };
-struct Item {
-    int32_t tensor, block;   // block: within the tensor
+struct Segment {
+    int32_t tensor, block, count;   // blocks [block, block + count) of the tensor
+    int32_t before;                 // the worker's blocks in earlier segments
 };
-static_assert(sizeof(Entry) == 48 && sizeof(Item) == 8, "table layout");
+static_assert(sizeof(Entry) == 48 && sizeof(Segment) == 16, "table layout");
 
-__device__ __forceinline__ const Item *items_of(const void *table, int tensors) {
-    return reinterpret_cast<const Item *>(static_cast<const Entry *>(table) + tensors);
+struct Table {
+    const Entry *entries;
+    const Segment *segments;
+    const int32_t *starts;   // [workers + 1]
+};
+Table table_of(const void *table, const nest_table_info *info) {
+    const Entry *e = static_cast<const Entry *>(table);
+    const Segment *s = reinterpret_cast<const Segment *>(e + info->tensors);
+    return {e, s, reinterpret_cast<const int32_t *>(s + info->items)};
 }
+int64_t table_bytes(int64_t tensors, int64_t segments, int64_t workers) {
+    return int64_t(sizeof(Entry)) * tensors + int64_t(sizeof(Segment)) * segments + 4 * (workers + 1);
+}
+
+// A worker's segments, 32 at a time, one per lane.
+struct Segments {
+    int from, to;
+    Segment lane_s;
+    __device__ __forceinline__ void fetch(const Table &t) {
+        const int at = from + (threadIdx.x & 31);
+        lane_s = at < to ? t.segments[at] : Segment{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ Segments(const Table &t, int worker, int workers) {
+        from = worker < workers ? t.starts[worker] : 0;
+        to = worker < workers ? t.starts[worker + 1] : 0;
+        fetch(t);
+    }
+    // fn(entry, first, count) for each segment in which the warp has blocks: the first one in the
+    // tensor, and how many, kWarps apart.
+    template <typename F>
+    __device__ __forceinline__ void each(const Table &t, F fn) {
+        const int warp = threadIdx.x >> 5;
+        while (from < to) {
+            const Segment all = lane_s;
+            from += 32;
+            if (from < to) fetch(t);
+            const int own = (warp - all.before) & (kWarps - 1);   // the warp's first block in the segment
+            uint32_t with = __ballot_sync(0xffffffffu, own < all.count);
+            while (with) {
+                const int j = __ffs(with) - 1;
+                with &= with - 1;
+                const int skip = __shfl_sync(0xffffffffu, own, j), block = __shfl_sync(0xffffffffu, all.block, j);
+                const int count = __shfl_sync(0xffffffffu, all.count, j);
+                fn(t.entries[__shfl_sync(0xffffffffu, all.tensor, j)], block + skip,
+                   (count - skip + kWarps - 1) / kWarps);
+            }
+        }
+    }
+};
 
 int64_t blocks_in(int64_t numel) { return (numel + kBlock - 1) / kBlock; }
 
-// A lane's share of a block: elements 8 lane .. 8 lane + 7, in one load of 32 bytes (or 16).
+// A lane's share of a block: elements 8 lane .. 8 lane + 7, in one access of 32 bytes (or 16).
+// Values stay as they were read until all of a block's loads are under way.
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
     asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
@@ -45,12 +94,9 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
                  : "memory");
 }
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
+__device__ __forceinline__ void load8(const T *p, T (&x)[8]) {
     static_assert(sizeof(T) == 2, "16-bit type");
-    const uint4 q = *reinterpret_cast<const uint4 *>(p);
-    const T *h = reinterpret_cast<const T *>(&q);
-#pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = to_f32(h[i]);
+    *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(p);
 }
 __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
@@ -61,11 +107,10 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
     static_assert(sizeof(T) == 2, "16-bit type");
-    uint4 q;
-    T *h = reinterpret_cast<T *>(&q);
+    alignas(16) T h[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) h[i] = from_f32<T>(x[i]);
-    *reinterpret_cast<uint4 *>(p) = q;
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
 }
 
 template <typename T>
@@ -77,19 +122,20 @@ __device__ __forceinline__ bool wide(const T *p) {   // every block of the tenso
 // others are 0.  A tensor that does not start at a multiple of 8 elements, and a tensor's last
 // block, go through the warp's shared memory: 32 neighbours at a time between it and the tensor.
 template <typename T>
-__device__ __forceinline__ void load_block(const T *p, int n, bool vector, int lane, float *room, float (&x)[8]) {
+__device__ __forceinline__ void load_block(const T *p, int n, bool vector, int lane, float *room, T (&x)[8]) {
     if (vector && n >= kBlock) {
         load8(p + 8 * lane, x);
         return;
     }
+    T *own = reinterpret_cast<T *>(room);
     T part[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) part[i] = lane + 32 * i < n ? p[lane + 32 * i] : from_f32<T>(0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; i++) room[lane + 32 * i] = to_f32(part[i]);
+    for (int i = 0; i < 8; i++) own[lane + 32 * i] = part[i];
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = room[8 * lane + i];
+    for (int i = 0; i < 8; i++) x[i] = own[8 * lane + i];
     __syncwarp();
 }
 template <typename T>
@@ -98,12 +144,13 @@ __device__ __forceinline__ void store_block(T *p, int n, bool vector, int lane, 
         store8(p + 8 * lane, x);
         return;
     }
+    T *own = reinterpret_cast<T *>(room);
 #pragma unroll
-    for (int i = 0; i < 8; i++) room[8 * lane + i] = x[i];
+    for (int i = 0; i < 8; i++) own[8 * lane + i] = from_f32<T>(x[i]);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 8; i++)
-        if (lane + 32 * i < n) p[lane + 32 * i] = from_f32<T>(room[lane + 32 * i]);
+        if (lane + 32 * i < n) p[lane + 32 * i] = own[lane + 32 * i];
     __syncwarp();
 }
 
@@ -131,32 +178,42 @@ __device__ __forceinline__ float block_sum(float v, float *sh) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const void *table, int tensors, int items, float *part) {
+__global__ void __launch_bounds__(kThreads, 8) norm_kernel(Table table, int workers, float *part) {
     __shared__ float sh[kWarps];
     __shared__ __align__(16) float room[kWarps][kBlock];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Entry *entries = static_cast<const Entry *>(table);
-    const Item *list = items_of(table, tensors);
     Sum sum;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const Item item = list[it];
-        const T *g = static_cast<const T *>(entries[item.tensor].grad);
-        const int64_t numel = entries[item.tensor].numel;
+    Segments(table, blockIdx.x, workers).each(table, [&](const Entry &e, int block, int count) {
+        const T *g = static_cast<const T *>(e.grad) + int64_t(block) * kBlock;
+        int64_t left = e.numel - int64_t(block) * kBlock;
         const bool vector = wide(g);
-        float s = 0.0f;
+        while (count > 0) {
+            float s = 0.0f;
+            if (vector && count > 1 && left >= (kWarps + 1) * kBlock) {   // two blocks' loads at once
+                alignas(16) T x[8], y[8];
+                load8(g + 8 * lane, x);
+                load8(g + kWarps * kBlock + 8 * lane, y);
 #pragma unroll
-        for (int b = 0; b < kItemBlocks; b += kWarps) {
-            const int64_t at = int64_t(item.block + b + warp) * kBlock, left = numel - at;
-            if (left <= 0) break;
-            float x[8];
-            load_block(g + at, int(left < kBlock ? left : kBlock), vector, lane, room[warp], x);
+                for (int i = 0; i < 8; i++) s = fmaf(to_f32(x[i]), to_f32(x[i]), s);
 #pragma unroll
-            for (int i = 0; i < 8; i++) s = fmaf(x[i], x[i], s);
+                for (int i = 0; i < 8; i++) s = fmaf(to_f32(y[i]), to_f32(y[i]), s);
+                count--;
+                g += kWarps * kBlock;
+                left -= kWarps * kBlock;
+            } else {
+                alignas(16) T x[8];
+                load_block(g, int(left < kBlock ? left : kBlock), vector, lane, room[warp], x);
+#pragma unroll
+                for (int i = 0; i < 8; i++) s = fmaf(to_f32(x[i]), to_f32(x[i]), s);
+            }
+            sum.add(s);
+            count--;
+            g += kWarps * kBlock;
+            left -= kWarps * kBlock;
         }
-        sum.add(s);
-    }
+    });
     const float s = block_sum(sum.value(), sh);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
@@ -200,38 +257,35 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
     return a < 0x7f800000u ? a : 0u;
 }
 
-// Code of y >= 0 with 3 mantissa bits: 16 bits of noise r are added under the last bit
-// kept and the rest is cut off.  Exponent field f of a normal code stands for the 32-bit
-// exponent field OFFSET + f; under the smallest normal value the code counts steps of
-// 1 / small, whose fraction is cut to 16 bits by adding 128 (one unit in the last place of a
-// number there is 2^-16) and summed with the noise as an integer.
-template <int OFFSET>
-__device__ __forceinline__ uint32_t code_of(float y, uint32_t r, float small) {
-    const uint32_t normal = (__float_as_uint(y) + (r << 4) - (uint32_t(OFFSET) << 23)) >> 20;
-    const uint32_t fixed = (__float_as_uint(__fmaf_rz(y, small, 128.0f)) + r - 0x43000000u) >> 16;
-    return __float_as_uint(y) < (uint32_t(OFFSET + 1) << 23) ? fixed : normal;
-}
-
-// Codes of a lane's eight pairs of moments; word: the block's noise.  rare: the block holds one
-// that is not finite, or whose scale is clipped, and codes are checked against the largest.
+// Codes of a lane's eight pairs of moments; word: the block's noise.  A moment is scaled so that
+// the smallest normal code becomes the smallest normal 32-bit number: then exponent field and
+// upper three mantissa bits of either kind, normal or not, are the code, and adding 16 bits of
+// noise under them and cutting off the rest rounds it.  RARE: the block holds a moment that is
+// not finite, or a scale that is clipped or does not fit one factor.
 template <bool RARE>
 __device__ __forceinline__ void encode(const float (&m)[8], const float (&v)[8], int sm, int sv, uint32_t word,
                                        int lane, uint2 &cm, uint2 &cv) {
-    const float fm = power2(8 - sm), fv = power2(-1 - sv);
+    const float fm = power2(RARE ? 8 - sm : -112 - sm), fv = power2(RARE ? -1 - sv : -96 - sv);
     uint32_t pm[2] = {0, 0}, pv[2] = {0, 0};
+    word += 8 * lane * 0x9E3779B1u;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        uint32_t x = word + uint32_t(8 * lane + i) * 0x9E3779B1u;
+        uint32_t x = word + i * 0x9E3779B1u;
         x ^= x >> 15;
         x *= 0x6A09E667u;
         x ^= x >> 16;
-        uint32_t a = code_of<120>(fabsf(m[i]) * fm, x >> 16, 512.0f);
-        uint32_t b = code_of<95>(v[i] * fv, x & 0xFFFFu, 0x1p34f);
+        float ym = fabsf(m[i]) * fm, yv = v[i] * fv;
+        if (RARE) {
+            ym *= 0x1p-120f;
+            yv *= 0x1p-95f;
+        }
+        uint32_t a = (__float_as_uint(ym) + (x >> 12 & 0xFFFF0u)) >> 20;
+        uint32_t b = (__float_as_uint(yv) + (x << 4 & 0xFFFF0u)) >> 20;
         if (RARE) {
             a = isfinite(m[i]) ? min(a, 0x7Eu) : 0x7Fu;
             b = isfinite(v[i]) ? min(b, 0xFEu) : 0xFFu;
         }
-        a |= (__float_as_uint(m[i]) >> 24) & 0x80u;
+        a |= __float_as_uint(m[i]) >> 24 & 0x80u;
         pm[i / 4] |= a << (8 * (i % 4));
         pv[i / 4] |= b << (8 * (i % 4));
     }
@@ -258,10 +312,13 @@ __device__ __forceinline__ void decode_m(uint2 c, int s, float (&m)[8]) {
 
 // A code's bits as a 32-bit float are its value with the exponent 95 too small, subnormal codes included.
 __device__ __forceinline__ void decode_v(uint2 c, int s, float (&v)[8]) {
-    const float f = power2(s + 1);
+    const float f = power2(min(s + 96, 127));
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-        v[i] = __uint_as_float(((i < 4 ? c.x : c.y) >> (8 * (i & 3)) & 0xFFu) << 20) * 0x1p95f * f;
+    for (int i = 0; i < 8; i++) v[i] = __uint_as_float(((i < 4 ? c.x : c.y) >> (8 * (i & 3)) & 0xFFu) << 20) * f;
+    if (s > 31) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] *= power2(s - 31);
+    }
     if (__vcmpeq4(c.x, 0xFFFFFFFFu) | __vcmpeq4(c.y, 0xFFFFFFFFu)) {
 #pragma unroll
         for (int i = 0; i < 8; i++)
@@ -271,9 +328,11 @@ __device__ __forceinline__ void decode_v(uint2 c, int s, float (&v)[8]) {
 
 // ---- AdamW --------------------------------------------------------------------------
 
+constexpr int kStepsPerSm = 3;   // thread blocks: up to 80 registers a thread
+
 struct StepArgs {
-    const void *table;
-    int tensors, items;
+    Table table;
+    int workers;
     float lr, beta1, beta2, rest1, rest2, eps;
     double beta1d, beta2d;
     uint32_t seed;
@@ -287,6 +346,16 @@ struct StepArgs {
 __device__ __forceinline__ float root_of(float x) {   // relative error 2^-23
     float r;
     asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float inverse_of(float x) {   // relative error 2^-23; 0 above 2^126
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float larger(float a, float b) {   // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
@@ -310,34 +379,74 @@ __device__ __forceinline__ void store_own(uint8_t *p, int n, int lane, uint2 c) 
         if (8 * lane + i < n) p[8 * lane + i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
 }
 
-// Magnitudes (as bits) from which a block's codes take the checked path: 1.75 * 2^120, infinity, NaN.
-constexpr uint32_t kRare = (uint32_t(120 + 127) << 23) | 0x600000u;
+// Copies from global to shared memory that the thread waits for later.
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void *to, const void *from) {
+    const uint32_t dst = uint32_t(__cvta_generic_to_shared(to));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_mark() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
+
+// What a warp needs of a block whose moments are in 8 bits, each lane its own share in planes
+// of 16 or 8 bytes per lane.  The codes' decoding and encoding leave too few warps on an SM to
+// cover the memory's latency with one block each, so blocks are copied ahead.
+constexpr int kAhead = 3;
+template <typename G>
+struct Stage {
+    uint4 grad[sizeof(G) / 2][32];
+    uint4 master[2][32];
+    uint2 m[32], v[32];
+
+    __device__ __forceinline__ void copy(const G *g, const float *p, const uint8_t *cm, const uint8_t *cv, int lane) {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(G) / 2); i++) copy_ahead<16>(&grad[i][lane], g + 8 * lane + i * (16 / sizeof(G)));
+#pragma unroll
+        for (int i = 0; i < 2; i++) copy_ahead<16>(&master[i][lane], p + 8 * lane + 4 * i);
+        copy_ahead<8>(&m[lane], cm + 8 * lane);
+        copy_ahead<8>(&v[lane], cv + 8 * lane);
+    }
+    __device__ __forceinline__ void read(G (&g)[8], float (&p)[8], uint2 &cm, uint2 &cv, int lane) const {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(G) / 2); i++) reinterpret_cast<uint4 *>(g)[i] = grad[i][lane];
+#pragma unroll
+        for (int i = 0; i < 2; i++) reinterpret_cast<uint4 *>(p)[i] = master[i][lane];
+        cm = m[lane];
+        cv = v[lane];
+    }
+};
+// Magnitudes of m and v (as bits) from which a block's codes take the checked path: 1.75 * 2^14
+// and 1.75 * 2^30, above which the scale is no single factor; infinity; NaN.
+constexpr uint32_t kRareM = (uint32_t(14 + 127) << 23) | 0x600000u, kRareV = (uint32_t(30 + 127) << 23) | 0x600000u;
 
 template <typename W, typename G, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(StepArgs a) {
+__global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a) {
     constexpr bool kOwnMaster = sizeof(W) == 4;
     __shared__ __align__(16) float room[kWarps][kBlock];
+    extern __shared__ __align__(16) unsigned char sh[];
     __shared__ struct {
-        float scale, inv1, root2;
+        float scale, root, eps;
         uint32_t start;
     } shared;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Entry *entries = static_cast<const Entry *>(a.table);
-    const Item *list = items_of(a.table, a.tensors);
-    int it = blockIdx.x;
-    Item item = {0, 0};
-    if (it < a.items) item = list[it];
+    Segments segments(a.table, blockIdx.x, a.workers);   // under way with the step's state
     if (threadIdx.x == 0) {   // what all share, by one thread: 64-bit arithmetic is slow
         const nest_adamw_state st = *a.state;
         shared.scale = a.grad_scale ? *a.grad_scale : 1.0f;
-        shared.inv1 = 1.0f / float(1.0 - st.beta1_t * a.beta1d);
-        shared.root2 = rsqrtf(float(1.0 - st.beta2_t * a.beta2d));
+        // m / c1 / (sqrt(v / c2) + eps) = m / (sqrt(v) c1 / sqrt(c2) + c1 eps)
+        const float c1 = float(1.0 - st.beta1_t * a.beta1d);
+        shared.root = c1 * rsqrtf(float(1.0 - st.beta2_t * a.beta2d));
+        shared.eps = c1 * a.eps;
         shared.start = mixed(a.seed ^ mixed(uint32_t(st.step + 1)));
     }
     __syncthreads();
-    const float scale = shared.scale, inv1 = shared.inv1, root2 = shared.root2;
+    const float scale = shared.scale, root = shared.root, eps = shared.eps;
     const uint32_t start = shared.start;
     if (!isfinite(scale)) return;
     // says that this block has read the step's state; the last block to say so advances it at
@@ -347,69 +456,113 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(StepArgs a) {
         __threadfence();
         before = atomicAdd(&a.state->ticket, 1u);
     }
-    while (it < a.items) {
-        const Entry e = entries[item.tensor];
-        it += gridDim.x;
-        Item next = {0, 0};
-        if (it < a.items) next = list[it];
+    segments.each(a.table, [&](const Entry &e, int b, int count) {
         W *weight = static_cast<W *>(e.weight);
         const G *grad = static_cast<const G *>(e.grad);
         const bool wide_w = wide(weight), wide_g = wide(grad);
         const float lr = a.lr * e.lr_scale, decay = e.weight_decay;
-        for (int b = item.block + warp; b < item.block + kItemBlocks; b += kWarps) {
-            const int64_t j0 = int64_t(b) * kBlock, left = e.numel - j0;
-            if (left <= 0) break;
-            const int n = int(left < kBlock ? left : kBlock);
-            const int64_t block = e.first + b, at = block * kBlock;
-            float g[8], m[8], v[8], p[8];
-            load_block(grad + j0, n, wide_g, lane, room[warp], g);
-            if constexpr (kOwnMaster)
-                load_block(weight + j0, n, wide_w, lane, room[warp], p);
-            else
-                load8(a.master + at + 8 * lane, p);   // the list's own buffers hold whole blocks
-            if constexpr (EIGHT) {
-                const uint2 cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.m) + at + 8 * lane);
-                const uint2 cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.v) + at + 8 * lane);
-                decode_m(cm, a.m_exp[block], m);
-                decode_v(cv, a.v_exp[block], v);
-            } else {
-                load8(static_cast<const float *>(a.m) + at + 8 * lane, m);
-                load8(static_cast<const float *>(a.v) + at + 8 * lane, v);
+        using S = Stage<G>;
+        S *const stages = reinterpret_cast<S *>(sh) + warp * (kAhead + 1);
+        // the warp's whole blocks here, where their parts are aligned, are copied ahead
+        const int64_t past = e.numel / kBlock - b;
+        const int whole = EIGHT && wide_g && (!kOwnMaster || wide_w) && past > 0
+                              ? int(past < int64_t(count) * kWarps ? (past + kWarps - 1) / kWarps : count) : 0;
+        auto ahead = [&](int i) {
+            if (i < whole) {
+                const int64_t j = int64_t(b + i * kWarps) * kBlock, own = e.first * kBlock + j;
+                const float *p;
+                if constexpr (kOwnMaster)
+                    p = weight + j;
+                else
+                    p = a.master + own;
+                stages[i % (kAhead + 1)].copy(grad + j, p, static_cast<const uint8_t *>(a.m) + own,
+                                              static_cast<const uint8_t *>(a.v) + own, lane);
             }
-            uint32_t top_m = 0, top_v = 0;
+            copies_mark();
+        };
+        if constexpr (EIGHT) {
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) ahead(i);
+        }
+        int lane_sm = 0, lane_sv = 0;   // scales of the warp's next 32 blocks, one per lane
+        for (int k = 0; k < count; k++) {
+            const int64_t bk = b + k * kWarps, j0 = bk * kBlock, left = e.numel - j0;
+            const int n = int(left < kBlock ? left : kBlock);
+            const int64_t block = e.first + bk, at = block * kBlock;
+            alignas(16) G g[8];
+            alignas(16) float p[8];
+            float m[8], v[8];
+            uint2 cm, cv;
+            int sm, sv;
+            if constexpr (EIGHT) {
+                if (k % 32 == 0 && k + lane < count) {
+                    lane_sm = a.m_exp[block + lane * kWarps];
+                    lane_sv = a.v_exp[block + lane * kWarps];
+                }
+                ahead(k + kAhead);
+                sm = __shfl_sync(0xffffffffu, lane_sm, k % 32);
+                sv = __shfl_sync(0xffffffffu, lane_sv, k % 32);
+            }
+            if (EIGHT && k < whole) {
+                copies_wait<kAhead>();
+                stages[k % (kAhead + 1)].read(g, p, cm, cv, lane);
+            } else {
+                load_block(grad + j0, n, wide_g, lane, room[warp], g);
+                if constexpr (EIGHT) {
+                    cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.m) + at + 8 * lane);
+                    cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.v) + at + 8 * lane);
+                } else {
+                    load8(static_cast<const float *>(a.m) + at + 8 * lane, m);
+                    load8(static_cast<const float *>(a.v) + at + 8 * lane, v);
+                }
+                if constexpr (kOwnMaster)
+                    load_block(weight + j0, n, wide_w, lane, room[warp], p);
+                else
+                    load8(a.master + at + 8 * lane, p);   // the list's own buffers hold whole blocks
+            }
+            if constexpr (EIGHT) {
+                decode_m(cm, sm, m);
+                decode_v(cv, sv, v);
+            }
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float x = g[i] * scale;
+                const float x = to_f32(g[i]) * scale;
                 // each product rounded by itself, so that a moment is the same number wherever
                 // these formulas are evaluated, and its 8-bit code with it
                 m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(x, a.rest1));
                 v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(x, x), a.rest2));
-                p[i] -= lr * (__fdividef(m[i] * inv1, fmaf(root_of(v[i]), root2, a.eps)) + decay * p[i]);
-                if (EIGHT && 8 * lane + i < n) {
-                    top_m = max(top_m, __float_as_uint(m[i]) & 0x7fffffffu);
-                    top_v = max(top_v, __float_as_uint(v[i]) & 0x7fffffffu);
-                }
+                p[i] -= lr * fmaf(decay, p[i], m[i] * inverse_of(fmaf(root_of(v[i]), root, eps)));
             }
             store_block(weight + j0, n, wide_w, lane, room[warp], p);
             if constexpr (!kOwnMaster) store_own(a.master + at, n, lane, p);
             if constexpr (EIGHT) {
-                top_m = __reduce_max_sync(0xffffffffu, top_m);
-                top_v = __reduce_max_sync(0xffffffffu, top_v);
-                const bool rare = max(top_m, top_v) >= kRare;
-                if (rare) {   // the largest finite magnitudes
-                    top_m = top_v = 0;
+                float top_m = 0.0f, top_v = 0.0f;
+                if (n < kBlock) {   // what lies past the end has no say in the scale
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        if (8 * lane + i < n) {
-                            top_m = max(top_m, finite_bits(m[i]));
-                            top_v = max(top_v, finite_bits(v[i]));
-                        }
-                    top_m = __reduce_max_sync(0xffffffffu, top_m);
-                    top_v = __reduce_max_sync(0xffffffffu, top_v);
+                        if (8 * lane + i >= n) m[i] = v[i] = 0.0f;
                 }
-                const int sm = shared_exponent(top_m), sv = shared_exponent(top_v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    top_m = larger(top_m, fabsf(m[i]));
+                    top_v = larger(top_v, v[i]);
+                }
+                uint32_t bits_m = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
+                uint32_t bits_v = __reduce_max_sync(0xffffffffu, __float_as_uint(top_v));
+                const bool rare = bits_m >= kRareM || bits_v >= kRareV;
+                if (rare) {   // the largest finite magnitudes
+                    bits_m = bits_v = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        bits_m = max(bits_m, finite_bits(m[i]));
+                        bits_v = max(bits_v, finite_bits(v[i]));
+                    }
+                    bits_m = __reduce_max_sync(0xffffffffu, bits_m);
+                    bits_v = __reduce_max_sync(0xffffffffu, bits_v);
+                }
+                sm = shared_exponent(bits_m);
+                sv = shared_exponent(bits_v);
                 const uint32_t word = mixed(start + uint32_t(block) * 0x9E3779B1u);
-                uint2 cm, cv;
                 if (rare)
                     encode<true>(m, v, sm, sv, word, lane, cm, cv);
                 else
@@ -425,8 +578,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(StepArgs a) {
                 store_own(static_cast<float *>(a.v) + at, n, lane, v);
             }
         }
-        item = next;
-    }
+    });
     if (threadIdx.x == 0 && before == gridDim.x - 1) {
         a.state->beta1_t *= a.beta1d;
         a.state->beta2_t *= a.beta2d;
@@ -440,28 +592,67 @@ __global__ void __launch_bounds__(kThreads) values_kernel(int64_t blocks, const 
                                                           __nv_bfloat16 *m_out, __nv_bfloat16 *v_out) {
     pdl_wait();
     pdl_trigger();
+    // a warp takes two blocks at a time, half the grid apart in the list
     const int lane = threadIdx.x & 31;
-    for (int64_t b = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5; b < blocks; b += int64_t(gridDim.x) * kWarps) {
-        const int64_t at = b * kBlock + 8 * lane;
-        const uint2 cm = *reinterpret_cast<const uint2 *>(m + at), cv = *reinterpret_cast<const uint2 *>(v + at);
-        float x[8];
-        decode_m(cm, m_exp[b], x);
-        store8(m_out + at, x);
-        decode_v(cv, v_exp[b], x);
-        store8(v_out + at, x);
+    const int64_t warps = int64_t(gridDim.x) * kWarps;
+    for (int64_t b = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5; b < blocks; b += 2 * warps) {
+        uint2 cm[2], cv[2];
+        int sm[2], sv[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int64_t at = b + h * warps;
+            if (at >= blocks) break;
+            cm[h] = *reinterpret_cast<const uint2 *>(m + at * kBlock + 8 * lane);
+            cv[h] = *reinterpret_cast<const uint2 *>(v + at * kBlock + 8 * lane);
+            sm[h] = m_exp[at];
+            sv[h] = v_exp[at];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int64_t at = b + h * warps;
+            if (at >= blocks) break;
+            float x[8];
+            decode_m(cm[h], sm[h], x);
+            store8(m_out + at * kBlock + 8 * lane, x);
+            decode_v(cv[h], sv[h], x);
+            store8(v_out + at * kBlock + 8 * lane, x);
+        }
     }
 }
 
 // ---- host -----------------------------------------------------------------------------
 
+int64_t workers_for(int64_t blocks) {
+    const int64_t w = (blocks + kWarps - 1) / kWarps;
+    return w < kWorkers ? w : kWorkers;
+}
+
 int check_info(const nest_table_info *info) {
     if (!info || info->tensors < 0 || info->blocks < 0 || info->items < 0 || info->items > info->blocks ||
-        info->table_bytes < int64_t(sizeof(Entry)) * info->tensors + int64_t(sizeof(Item)) * info->items)
+        info->workers != workers_for(info->blocks) ||
+        info->table_bytes < table_bytes(info->tensors, info->items, info->workers))
         return NEST_E_INVALID;
     return info->blocks > INT32_MAX ? NEST_E_LIMITS : NEST_OK;
 }
 
-int blocks_for(int64_t items) { return int(items < 1 ? 1 : items < kSMs * 8 ? items : kSMs * 8); }
+// fn(tensor, block, count, before, worker) for every segment in order: worker w has the list's
+// blocks [w blocks / workers, (w + 1) blocks / workers).
+template <typename F>
+void each_segment(const nest_tensor *t, int32_t n, int64_t blocks, F fn) {
+    const int64_t workers = workers_for(blocks);
+    int64_t done = 0, worker = 0;
+    for (int32_t i = 0; i < n; i++) {
+        const int64_t size = blocks_in(t[i].numel);
+        for (int64_t b = 0; b < size;) {
+            int64_t end = (worker + 1) * blocks / workers;
+            while (end <= done) end = (++worker + 1) * blocks / workers;
+            const int64_t count = size - b < end - done ? size - b : end - done;
+            fn(i, int32_t(b), int32_t(count), int32_t(done - worker * blocks / workers), worker);
+            b += count;
+            done += count;
+        }
+    }
+}
 
 }  // namespace
 
@@ -478,14 +669,14 @@ int nest_table_query(const nest_tensor *t, int32_t n, nest_table_info *out) {
         if (t[i].numel < 0 || (t[i].numel && !t[i].grad)) return NEST_E_INVALID;
         if (t[i].numel > int64_t(INT32_MAX) * kBlock) return NEST_E_LIMITS;
         blocks += blocks_in(t[i].numel);
-        items += (blocks_in(t[i].numel) + kItemBlocks - 1) / kItemBlocks;
         if (blocks > INT32_MAX) return NEST_E_LIMITS;
     }
-    out->table_bytes = int64_t(sizeof(Entry)) * n + int64_t(sizeof(Item)) * items;
+    each_segment(t, n, blocks, [&](int32_t, int32_t, int32_t, int32_t, int64_t) { items++; });
     out->blocks = blocks;
     out->items = items;
     out->tensors = n;
-    out->reserved = 0;
+    out->workers = int32_t(workers_for(blocks));
+    out->table_bytes = table_bytes(n, items, out->workers);
     return NEST_OK;
 }
 
@@ -493,26 +684,32 @@ int nest_table_pack(const nest_tensor *t, int32_t n, const nest_table_info *info
     nest_table_info need;
     if (const int rc = nest_table_query(t, n, &need)) return rc;
     if (!info || need.tensors != info->tensors || need.items != info->items || need.blocks != info->blocks ||
-        need.table_bytes != info->table_bytes || (need.table_bytes && !table))
+        need.workers != info->workers || need.table_bytes != info->table_bytes || !table)
         return NEST_E_INVALID;
-    unsigned char *entries = static_cast<unsigned char *>(table), *items = entries + sizeof(Entry) * n;
+    unsigned char *at = static_cast<unsigned char *>(table);   // of any alignment
     int64_t first = 0;
-    for (int32_t i = 0; i < n; i++) {
+    for (int32_t i = 0; i < n; i++, at += sizeof(Entry)) {
         const Entry e = {t[i].weight, t[i].grad, t[i].numel, first, t[i].weight_decay, t[i].lr_scale, 0};
-        std::memcpy(entries + sizeof(Entry) * i, &e, sizeof e);
-        const int64_t blocks = blocks_in(t[i].numel);
-        for (int64_t b = 0; b < blocks; b += kItemBlocks, items += sizeof(Item)) {
-            const Item it = {i, int32_t(b)};
-            std::memcpy(items, &it, sizeof it);
-        }
-        first += blocks;
+        std::memcpy(at, &e, sizeof e);
+        first += blocks_in(t[i].numel);
     }
+    unsigned char *starts = at + sizeof(Segment) * size_t(need.items);
+    int32_t segment = 0;
+    int64_t known = -1;
+    each_segment(t, n, need.blocks, [&](int32_t tensor, int32_t block, int32_t count, int32_t before, int64_t worker) {
+        for (; known < worker; known++) std::memcpy(starts + 4 * (known + 1), &segment, 4);
+        const Segment s = {tensor, block, count, before};
+        std::memcpy(at, &s, sizeof s);
+        at += sizeof s;
+        segment++;
+    });
+    std::memcpy(starts + 4 * size_t(need.workers), &segment, 4);
     return NEST_OK;
 }
 
 size_t nest_grad_norm_workspace_size(const nest_table_info *info) {
     if (check_info(info)) return 0;
-    return (size_t(blocks_for(info->items)) * 4 + 255) & ~size_t(255);
+    return (size_t(info->workers + 1) * 4 + 255) & ~size_t(255);
 }
 
 int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_type, float max_norm, float *out,
@@ -522,11 +719,11 @@ int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_
         return NEST_E_INVALID;
     if (!workspace || ws_bytes < nest_grad_norm_workspace_size(info) || !aligned_to(workspace, 256))
         return NEST_E_WORKSPACE;
-    const int blocks = blocks_for(info->items);
+    const int blocks = info->workers > 1 ? info->workers : 1;
     float *part = static_cast<float *>(workspace);
     const int rc = with_type(grad_type, [&](auto t) {
-        return launch_kernel(norm_kernel<decltype(t)>, dim3(blocks), dim3(kThreads), 0, stream, 1, "norm launch", table,
-                             int(info->tensors), int(info->items), part);
+        return launch_kernel(norm_kernel<decltype(t)>, dim3(blocks), dim3(kThreads), 0, stream, 1, "norm launch",
+                             table_of(table, info), int(info->workers), part);
     });
     if (rc) return rc;
     return launch_kernel(norm_finish_kernel, dim3(1), dim3(kThreads), 0, stream, 1, "norm finish launch",
@@ -549,17 +746,23 @@ int nest_adamw(const nest_table_info *info, const void *table, const nest_adamw_
             !aligned_to(p->v_exp, 256))
             return NEST_E_INVALID;
     }
-    const StepArgs a = {table, info->tensors, int(info->items), float(p->lr), float(p->beta1), float(p->beta2),
+    const StepArgs a = {table_of(table, info), info->workers, float(p->lr), float(p->beta1), float(p->beta2),
                         float(1.0 - p->beta1), float(1.0 - p->beta2), float(p->eps), p->beta1, p->beta2, p->seed,
                         p->master, p->m, p->v, p->m_exp, p->v_exp, p->state, p->grad_scale};
-    const dim3 grid(blocks_for(info->items));
+    const dim3 grid(info->workers > 1 ? info->workers : 1);
     return with_type(p->weight_type, [&](auto w) {
         using W = decltype(w);
         return with_type(p->grad_type, [&](auto g) {
             using G = decltype(g);
-            return p->state_bits == 8
-                       ? launch_kernel(adamw_kernel<W, G, true>, grid, dim3(kThreads), 0, stream, 1, "adamw launch", a)
-                       : launch_kernel(adamw_kernel<W, G, false>, grid, dim3(kThreads), 0, stream, 1, "adamw launch", a);
+            if (p->state_bits == 32)
+                return launch_kernel(adamw_kernel<W, G, false>, grid, dim3(kThreads), 0, stream, 1, "adamw launch", a);
+            constexpr int kStages = int(sizeof(Stage<G>)) * kWarps * (kAhead + 1);
+            const int rc = cuda_status(cudaFuncSetAttribute(adamw_kernel<W, G, true>,
+                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kStages),
+                                       "adamw attribute");
+            return rc ? rc
+                      : launch_kernel(adamw_kernel<W, G, true>, grid, dim3(kThreads), kStages, stream, 1,
+                                      "adamw launch", a);
         });
     });
 }
@@ -571,7 +774,7 @@ int nest_adamw_values(const nest_table_info *info, const void *m, const void *v,
     if (!m || !v || !m_exp || !v_exp || !m_out || !v_out || !aligned_to(m, 256) || !aligned_to(v, 256) ||
         !aligned_to(m_out, 256) || !aligned_to(v_out, 256))
         return NEST_E_INVALID;
-    const int64_t grid_blocks = (info->blocks + kWarps - 1) / kWarps;
+    const int64_t grid_blocks = (info->blocks + 2 * kWarps - 1) / (2 * kWarps);
     const dim3 grid(unsigned(grid_blocks < kSMs * 8 ? grid_blocks : kSMs * 8));
     return launch_kernel(values_kernel, grid, dim3(kThreads), 0, stream, 1, "adamw values launch", info->blocks,
                          static_cast<const uint8_t *>(m), static_cast<const uint8_t *>(v), m_exp, v_exp,

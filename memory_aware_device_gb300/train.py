@@ -41,7 +41,7 @@ class RouteDesc(C.Structure):
 
 class TableInfo(C.Structure):
     _fields_ = [("table_bytes", C.c_int64), ("blocks", C.c_int64), ("items", C.c_int64), ("tensors", C.c_int32),
-                ("reserved", C.c_int32)]
+                ("workers", C.c_int32)]
 
 
 class AdamWArgs(C.Structure):

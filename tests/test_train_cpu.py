@@ -244,3 +244,32 @@ def test_noise_is_even():
     assert abs(c) < 5 / n ** 0.5
     m2, _ = ref.noise(12345, 8, np.arange(4096))
     assert abs(np.corrcoef(m.ravel(), m2.ravel())[0, 1]) < 5 / n ** 0.5
+
+
+@pytest.mark.parametrize("numels", [[1], [31] * 300, [256 * 9 + 1, 0, 5], [10**6, 3, 2 * 10**6], [40000] * 70,
+                                    [2**33, 7]])
+def test_table_covers_every_block_once(numels):
+    """The workers' segments are the tensors' blocks, each once; shares are even."""
+    rec = tensors(numels)
+    rc, info = query(rec)
+    assert rc == 0
+    packed = np.zeros(info.table_bytes, np.uint8)
+    assert train.lib().nest_table_pack(rec.ctypes.data, len(rec), C.byref(info), packed.ctypes.data) == 0
+    a, b = 48 * len(numels), 48 * len(numels) + 16 * info.items
+    entries = packed[:a].view(np.int64).reshape(-1, 6)
+    seg, starts = packed[a:b].view(np.int32).reshape(-1, 4), packed[b:].view(np.int32)
+    blocks = [-(-n // 256) for n in numels]
+    assert (entries[:, 2] == numels).all() and (entries[:, 3] == np.cumsum([0] + blocks[:-1])).all()
+    assert len(starts) == info.workers + 1 and starts[0] == 0 and starts[-1] == info.items
+    share = [seg[starts[w]:starts[w + 1], 2].sum() for w in range(info.workers)]
+    assert max(share) - min(share) <= 1 and sum(share) == info.blocks
+    runs = []
+    for w in range(info.workers):
+        before = 0
+        for t, block, count, skip in seg[starts[w]:starts[w + 1]].astype(np.int64):
+            assert count > 0 and skip == before and block + count <= blocks[t]
+            before += count
+            runs.append((entries[t, 3] + block, count))
+    runs.sort()
+    assert runs[0][0] == 0 and all(a + n == b for (a, n), (b, _) in zip(runs, runs[1:]))
+    assert sum(runs[-1]) == info.blocks
