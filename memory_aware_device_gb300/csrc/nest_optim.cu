@@ -1,8 +1,8 @@
 // The optimizer's operators over lists of tensors: gradient norm and AdamW step, with
 // moments in 32 or in 8 bits (definitions in nest_train.h).
 //
-// The list's blocks of 256 elements are divided evenly between workers, which thread blocks
-// take; a worker's blocks are a few segments, each of one tensor, and its warps take every
+// The list's blocks of 256 elements are divided evenly between workers, each of them a thread
+// block; a worker's blocks are a few segments, each of one tensor, and its warps take every
 // kWarps-th of them, a warp a whole block.  The packed table holds the tensors' entries, the
 // segments in order and where each worker's begin.
 #include <cmath>
@@ -17,7 +17,7 @@ namespace {
 constexpr int kBlock = NEST_OPT_BLOCK;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWorkers = kSMs * 8;   // at most
+constexpr int kWorkers = kSMs * 8;   // at most: the norm's thread blocks are all resident at once
 
 struct Entry {            // one tensor
     void *weight;
@@ -47,7 +47,7 @@ int64_t table_bytes(int64_t tensors, int64_t segments, int64_t workers) {
     return int64_t(sizeof(Entry)) * tensors + int64_t(sizeof(Segment)) * segments + 4 * (workers + 1);
 }
 
-// A worker's segments, 32 at a time, one per lane.
+// The segments of a thread block's workers, 32 at a time, one per lane.
 struct Segments {
     int from, to;
     Segment lane_s;
@@ -61,23 +61,22 @@ struct Segments {
         fetch(t);
     }
     // fn(entry, first, count) for each segment in which the warp has blocks: the first one in the
-    // tensor, and how many, kWarps apart.
+    // tensor, and how many, `warps` (a power of two) apart; warp: its number among those that
+    // share the worker.
     template <typename F>
-    __device__ __forceinline__ void each(const Table &t, F fn) {
-        const int warp = threadIdx.x >> 5;
+    __device__ __forceinline__ void each(const Table &t, int warp, int warps, F fn) {
         while (from < to) {
             const Segment all = lane_s;
             from += 32;
             if (from < to) fetch(t);
-            const int own = (warp - all.before) & (kWarps - 1);   // the warp's first block in the segment
+            const int own = (warp - all.before) & (warps - 1);   // the warp's first block in the segment
             uint32_t with = __ballot_sync(0xffffffffu, own < all.count);
             while (with) {
                 const int j = __ffs(with) - 1;
                 with &= with - 1;
                 const int skip = __shfl_sync(0xffffffffu, own, j), block = __shfl_sync(0xffffffffu, all.block, j);
                 const int count = __shfl_sync(0xffffffffu, all.count, j);
-                fn(t.entries[__shfl_sync(0xffffffffu, all.tensor, j)], block + skip,
-                   (count - skip + kWarps - 1) / kWarps);
+                fn(t.entries[__shfl_sync(0xffffffffu, all.tensor, j)], block + skip, (count - skip + warps - 1) / warps);
             }
         }
     }
@@ -177,15 +176,17 @@ __device__ __forceinline__ float block_sum(float v, float *sh) {
     return warp_sum(threadIdx.x < kWarps ? sh[threadIdx.x] : 0.0f);
 }
 
+constexpr int kNormsPerSm = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 8) norm_kernel(Table table, int workers, float *part) {
+__global__ void __launch_bounds__(kThreads, kNormsPerSm) norm_kernel(Table table, int workers, float *part) {
     __shared__ float sh[kWarps];
     __shared__ __align__(16) float room[kWarps][kBlock];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Sum sum;
-    Segments(table, blockIdx.x, workers).each(table, [&](const Entry &e, int block, int count) {
+    Segments(table, blockIdx.x, workers).each(table, warp, kWarps, [&](const Entry &e, int block, int count) {
         const T *g = static_cast<const T *>(e.grad) + int64_t(block) * kBlock;
         int64_t left = e.numel - int64_t(block) * kBlock;
         const bool vector = wide(g);
@@ -266,7 +267,7 @@ template <bool RARE>
 __device__ __forceinline__ void encode(const float (&m)[8], const float (&v)[8], int sm, int sv, uint32_t word,
                                        int lane, uint2 &cm, uint2 &cv) {
     const float fm = power2(RARE ? 8 - sm : -112 - sm), fv = power2(RARE ? -1 - sv : -96 - sv);
-    uint32_t pm[2] = {0, 0}, pv[2] = {0, 0};
+    uint32_t a[8], b[8];   // the codes in the upper byte
     word += 8 * lane * 0x9E3779B1u;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -279,18 +280,20 @@ __device__ __forceinline__ void encode(const float (&m)[8], const float (&v)[8],
             ym *= 0x1p-120f;
             yv *= 0x1p-95f;
         }
-        uint32_t a = (__float_as_uint(ym) + (x >> 12 & 0xFFFF0u)) >> 20;
-        uint32_t b = (__float_as_uint(yv) + (x << 4 & 0xFFFF0u)) >> 20;
+        uint32_t bm = __float_as_uint(ym), bv = __float_as_uint(yv);
         if (RARE) {
-            a = isfinite(m[i]) ? min(a, 0x7Eu) : 0x7Fu;
-            b = isfinite(v[i]) ? min(b, 0xFEu) : 0xFFu;
+            bm = isfinite(m[i]) ? min(bm, 0x7Eu << 20) : 0x7Fu << 20;
+            bv = isfinite(v[i]) ? min(bv, 0xFEu << 20) : 0xFFu << 20;
         }
-        a |= __float_as_uint(m[i]) >> 24 & 0x80u;
-        pm[i / 4] |= a << (8 * (i % 4));
-        pv[i / 4] |= b << (8 * (i % 4));
+        a[i] = (bm + (x >> 12 & 0xFFFF0u)) << 4;
+        b[i] = (bv + (x << 4 & 0xFFFF0u)) << 4;
+        a[i] = (a[i] & 0x7FFFFFFFu) | (__float_as_uint(m[i]) & 0x80000000u);
     }
-    cm = make_uint2(pm[0], pm[1]);
-    cv = make_uint2(pv[0], pv[1]);
+    const auto pack = [](const uint32_t *c) {   // the upper bytes of four words
+        return __byte_perm(__byte_perm(c[0], c[1], 0x0073), __byte_perm(c[2], c[3], 0x0073), 0x5410);
+    };
+    cm = make_uint2(pack(a), pack(a + 4));
+    cv = make_uint2(pack(b), pack(b + 4));
 }
 
 // Two codes with 4 exponent bits as two floats: the hardware's e4m3 conversion (0x7F is NaN there too).
@@ -328,11 +331,12 @@ __device__ __forceinline__ void decode_v(uint2 c, int s, float (&v)[8]) {
 
 // ---- AdamW --------------------------------------------------------------------------
 
+constexpr int kParts = 8, kPartsEight = 4;   // of a long list's worker; 201M weights: see the step kernel
 constexpr int kStepsPerSm = 3;   // thread blocks: up to 80 registers a thread
 
 struct StepArgs {
     Table table;
-    int workers;
+    int workers, parts;   // parts: thread blocks that share a worker, a power of two
     float lr, beta1, beta2, rest1, rest2, eps;
     double beta1d, beta2d;
     uint32_t seed;
@@ -435,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Segments segments(a.table, blockIdx.x, a.workers);   // under way with the step's state
+    const int step = kWarps * a.parts;   // between a warp's blocks
+    Segments segments(a.table, blockIdx.x / a.parts, a.workers);   // under way with the step's state
     if (threadIdx.x == 0) {   // what all share, by one thread: 64-bit arithmetic is slow
         const nest_adamw_state st = *a.state;
         shared.scale = a.grad_scale ? *a.grad_scale : 1.0f;
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
         __threadfence();
         before = atomicAdd(&a.state->ticket, 1u);
     }
-    segments.each(a.table, [&](const Entry &e, int b, int count) {
+    segments.each(a.table, blockIdx.x % a.parts * kWarps + warp, step, [&](const Entry &e, int b, int count) {
         W *weight = static_cast<W *>(e.weight);
         const G *grad = static_cast<const G *>(e.grad);
         const bool wide_w = wide(weight), wide_g = wide(grad);
@@ -466,10 +471,10 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
         // the warp's whole blocks here, where their parts are aligned, are copied ahead
         const int64_t past = e.numel / kBlock - b;
         const int whole = EIGHT && wide_g && (!kOwnMaster || wide_w) && past > 0
-                              ? int(past < int64_t(count) * kWarps ? (past + kWarps - 1) / kWarps : count) : 0;
+                              ? int(past < int64_t(count) * step ? (past + step - 1) / step : count) : 0;
         auto ahead = [&](int i) {
             if (i < whole) {
-                const int64_t j = int64_t(b + i * kWarps) * kBlock, own = e.first * kBlock + j;
+                const int64_t j = int64_t(b + i * step) * kBlock, own = e.first * kBlock + j;
                 const float *p;
                 if constexpr (kOwnMaster)
                     p = weight + j;
@@ -486,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
         }
         int lane_sm = 0, lane_sv = 0;   // scales of the warp's next 32 blocks, one per lane
         for (int k = 0; k < count; k++) {
-            const int64_t bk = b + k * kWarps, j0 = bk * kBlock, left = e.numel - j0;
+            const int64_t bk = b + k * step, j0 = bk * kBlock, left = e.numel - j0;
             const int n = int(left < kBlock ? left : kBlock);
             const int64_t block = e.first + bk, at = block * kBlock;
             alignas(16) G g[8];
@@ -496,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
             int sm, sv;
             if constexpr (EIGHT) {
                 if (k % 32 == 0 && k + lane < count) {
-                    lane_sm = a.m_exp[block + lane * kWarps];
-                    lane_sv = a.v_exp[block + lane * kWarps];
+                    lane_sm = a.m_exp[block + lane * step];
+                    lane_sv = a.v_exp[block + lane * step];
                 }
                 ahead(k + kAhead);
                 sm = __shfl_sync(0xffffffffu, lane_sm, k % 32);
@@ -746,10 +751,14 @@ int nest_adamw(const nest_table_info *info, const void *table, const nest_adamw_
             !aligned_to(p->v_exp, 256))
             return NEST_E_INVALID;
     }
-    const StepArgs a = {table_of(table, info), info->workers, float(p->lr), float(p->beta1), float(p->beta2),
+    // several thread blocks to a worker of a long list: its SMs finish at different times, and the
+    // quicker ones take more of them
+    const int most = p->state_bits == 8 ? kPartsEight : kParts;
+    const int parts = info->blocks >= int64_t(kWorkers) * kWarps * most ? most : 1;
+    const StepArgs a = {table_of(table, info), info->workers, parts, float(p->lr), float(p->beta1), float(p->beta2),
                         float(1.0 - p->beta1), float(1.0 - p->beta2), float(p->eps), p->beta1, p->beta2, p->seed,
                         p->master, p->m, p->v, p->m_exp, p->v_exp, p->state, p->grad_scale};
-    const dim3 grid(info->workers > 1 ? info->workers : 1);
+    const dim3 grid(info->workers > 1 ? info->workers * parts : 1);
     return with_type(p->weight_type, [&](auto w) {
         using W = decltype(w);
         return with_type(p->grad_type, [&](auto g) {
