@@ -383,19 +383,6 @@ __device__ __forceinline__ void store_own(uint8_t *p, int n, int lane, uint2 c) 
         if (8 * lane + i < n) p[8 * lane + i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
 }
 
-// Copies from global to shared memory that the thread waits for later.
-template <int BYTES>
-__device__ __forceinline__ void copy_ahead(void *to, const void *from) {
-    const uint32_t dst = uint32_t(__cvta_generic_to_shared(to));
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void copies_mark() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LATER>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
-
 // What a warp needs of a block whose moments are in 8 bits, each lane its own share in planes
 // of 16 or 8 bytes per lane.  The codes' decoding and encoding leave too few warps on an SM to
 // cover the memory's latency with one block each, so blocks are copied ahead.

@@ -25,6 +25,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "nest_train.cuh"
 
 namespace nest {
@@ -98,9 +100,9 @@ template <> struct Piece<8> { using type = uint2; };
 template <> struct Piece<16> { using type = uint4; };
 
 // Which expert a lane's i-th value is: pieces of C neighbours, one lane's after another's.
-template <int V, bool VEC, int LANES = 32>
+template <int V, bool VEC, int LANES = 32, int MOST = 8>
 struct Place {
-    static constexpr int C = VEC ? (V < 8 ? V : 8) : 1;
+    static constexpr int C = VEC ? (V < MOST ? V : MOST) : 1;
     static __device__ __forceinline__ int of(int i, int lane) { return (i / C) * (LANES * C) + lane * C + i % C; }
 };
 
@@ -131,6 +133,37 @@ __device__ __forceinline__ void store_piece(T *p, const T *from) {
         *reinterpret_cast<P *>(p) = *reinterpret_cast<const P *>(from);
     }
 }
+
+// The forward kernel's rows on their way through shared memory, in pieces of up to 16 bytes: each
+// warp has room for two sets of its rows, one being copied while the other is worked on.
+template <typename T, int LANES, int V>
+struct Rows {
+    using L = Place<V, true, LANES, 16 / int(sizeof(T))>;
+    T x[32 / LANES][LANES * V];
+
+    __device__ __forceinline__ void copy(const T *row, int experts, int lane) {
+        const int g = lane & (LANES - 1);
+#pragma unroll
+        for (int i = 0; i < V; i += L::C) {
+            const int e = L::of(i, g);
+            if (e < experts) copy_ahead<L::C * int(sizeof(T))>(&x[lane / LANES][e], row + e);   // E is a multiple of C
+        }
+    }
+    __device__ __forceinline__ void read(int experts, int lane, T (&to)[V]) const {
+        const int g = lane & (LANES - 1);
+#pragma unroll
+        for (int i = 0; i < V; i += L::C) {
+            const int e = L::of(i, g);
+            if (e < experts) {
+                using P = typename Piece<L::C * sizeof(T)>::type;
+                *reinterpret_cast<P *>(to + i) = *reinterpret_cast<const P *>(&x[lane / LANES][e]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < L::C; c++) to[i + c] = from_f32<T>(-INFINITY);
+            }
+        }
+    }
+};
 
 // A row as the lane holds it; minus infinity past the last expert.
 template <typename T, int V, bool VEC, int LANES = 32>
@@ -395,30 +428,52 @@ template <typename T, int LANES, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
     constexpr int kRows = 32 / LANES, kSlots = FEW ? 1 : 32 / LANES;
     constexpr uint32_t kIndex = LANES * V - 1;
-    using L = Place<V, VEC, LANES>;
-    extern __shared__ unsigned char sh[];
+    using R = Rows<T, LANES, V>;
+    using L = typename std::conditional<VEC, typename R::L, Place<V, false, LANES>>::type;
+    extern __shared__ __align__(16) unsigned char sh[];
     __shared__ float sh_dot[32], sh_all[kCluster];
     const int threads = blockDim.x, warps = threads >> 5;
-    float *sh_sum = reinterpret_cast<float *>(sh);                            // [warps][experts]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane & (LANES - 1);
+    R *const rows = reinterpret_cast<R *>(sh) + 2 * warp;                         // [warps][2] (VEC)
+    float *sh_sum = reinterpret_cast<float *>(sh + (VEC ? 2 * warps * sizeof(R) : 0));   // [warps][experts]
     int32_t *sh_count = reinterpret_cast<int32_t *>(sh_sum + warps * a.experts);   // [experts], then live rows
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane & (LANES - 1);
     const int64_t stride = int64_t(gridDim.x) * warps * kRows;
+    auto row_of = [&](int64_t t) { return static_cast<const T *>(a.logits) + t * a.row_stride; };
+    auto counts = [&](int64_t t) { return t < a.tokens && !(a.mask && !a.mask[t]); };
+    const int64_t begin = (int64_t(blockIdx.x) * warps + warp) * kRows + lane / LANES;
+    bool next_on = false;
+    if constexpr (VEC) {
+        next_on = counts(begin);
+        if (next_on) rows[0].copy(row_of(begin), a.experts, lane);
+        copies_mark();
+    }
     for (int e = threadIdx.x; e <= a.experts; e += threads) sh_count[e] = 0;
     __syncthreads();
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; i++) acc[i] = 0.0f;
-    int live = 0;
-    for (int64_t first = (int64_t(blockIdx.x) * warps + warp) * kRows; first < a.tokens; first += stride) {
-        const int64_t t = first + lane / LANES;
-        const bool in = t < a.tokens, on = in && !(a.mask && !a.mask[t]);
-        const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
-        T raw[V];
-        if (on) {
-            fetch_row<T, V, VEC, LANES>(a, row, g, raw);
+    int live = 0, turn = 0;
+    for (int64_t t = begin; t - lane / LANES < a.tokens; t += stride, turn ^= 1) {
+        const T *row = row_of(t);
+        const bool in = t < a.tokens;
+        alignas(16) T raw[V];
+        bool on;
+        if constexpr (VEC) {
+            __syncwarp();   // the other set of rows has been read by all
+            on = next_on;
+            next_on = counts(t + stride);
+            if (next_on) rows[turn ^ 1].copy(row_of(t + stride), a.experts, lane);
+            copies_mark();
+            copies_wait<1>();
+            __syncwarp();
+            if (on) rows[turn].read(a.experts, lane, raw);
         } else {
+            on = counts(t);
+            if (on) fetch_row<T, V, false, LANES>(a, row, g, raw);
+        }
+        if (!on) {
 #pragma unroll
             for (int i = 0; i < V; i++) raw[i] = from_f32<T>(-INFINITY);
         }
@@ -474,7 +529,12 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
             if (!is_live) id[s] = -1;
             gate[s] = 0.0f;
             if (id[s] >= 0) {
-                gate[s] = exp2_of(ex.of(to_f32(row[id[s] * a.col_stride])));
+                T chosen;
+                if constexpr (VEC)
+                    chosen = rows[turn].x[lane / LANES][id[s]];
+                else
+                    chosen = row[id[s] * a.col_stride];
+                gate[s] = exp2_of(ex.of(to_f32(chosen)));
                 atomicAdd(&sh_count[id[s]], 1);
             }
             total += gate[s];
@@ -668,9 +728,9 @@ int with_values(int experts, F fn) {
     return fn(Number<32>{});
 }
 
-template <typename T, int V>
+// Whether every row can be read in pieces of C neighbours.
+template <typename T, int V, int C>
 bool vector_rows(const RouteArgs &a) {
-    constexpr int C = Place<V, true>::C;
     return V > 1 && a.col_stride == 1 && a.experts % C == 0 && a.row_stride % C == 0 &&
            aligned_to(a.logits, C * sizeof(T));
 }
@@ -682,8 +742,10 @@ template <typename T>
 int launch_route_type(const RouteArgs &a, int blocks, int threads, void *stream) {
     return with_row(a.experts, [&](auto lanes, auto values) {
         constexpr int L = decltype(lanes)::v, V = decltype(values)::v;
-        const size_t smem = size_t(4) * (threads / 32 * a.experts + a.experts + 1);
-        const bool vec = vector_rows<T, V>(a), few = a.k <= 8;
+        using R = Rows<T, L, V>;
+        const bool vec = vector_rows<T, V, R::L::C>(a), few = a.k <= 8;
+        const size_t smem = (vec ? threads / 32 * 2 * sizeof(R) : 0) +
+                            size_t(4) * (threads / 32 * a.experts + a.experts + 1);
         auto kernel = vec ? (few ? route_kernel<T, L, V, true, true> : route_kernel<T, L, V, true, false>)
                           : (few ? route_kernel<T, L, V, false, true> : route_kernel<T, L, V, false, false>);
         if (smem > 40000) {
@@ -704,7 +766,7 @@ int launch_route_backward_type(RouteArgs a, void *stream) {
         a.vector_grad = a.grad_stride % C == 0 && aligned_to(a.grad, C * sizeof(T));
         const size_t smem = size_t(4) * S::kWarps * 32 * V;
         const int64_t b = (a.tokens + S::kWarps - 1) / S::kWarps, most = kSMs * S::kPerSm;
-        auto kernel = vector_rows<T, V>(a) ? route_backward_kernel<T, V, (V > 1)> : route_backward_kernel<T, V, false>;
+        auto kernel = vector_rows<T, V, C>(a) ? route_backward_kernel<T, V, (V > 1)> : route_backward_kernel<T, V, false>;
         return launch_kernel(kernel, dim3(unsigned(b < most ? b : most)), dim3(S::kThreads), smem, stream, 1,
                              "route backward launch", a);
     });
