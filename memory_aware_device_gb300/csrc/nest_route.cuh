@@ -56,7 +56,7 @@ struct RouteArgs {
 // number of warps up to that.
 template <int V>
 struct RouteShape {
-    static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 12 : 16;
+    static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 14 : 16;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kPerSm = V == 16 ? 2 : 1;
 };
@@ -738,22 +738,27 @@ bool vector_rows(const RouteArgs &a) {
 }  // namespace
 
 // Launches of one element type (each in its own translation unit).
+template <typename T, int L, int V, bool VEC, bool FEW>
+int launch_route_kernel(const RouteArgs &a, int blocks, int threads, void *stream) {
+    const auto smem = [](int warps, int experts) {
+        return (VEC ? warps * 2 * sizeof(Rows<T, L, V>) : 0) + size_t(4) * (warps * experts + experts + 1);
+    };
+    const size_t most = smem(RouteShape<V>::kWarps, L * V);
+    if (most > 48000)
+        if (const int rc = allow_shared<route_kernel<T, L, V, VEC, FEW>>(most, "route attribute")) return rc;
+    return launch_kernel(route_kernel<T, L, V, VEC, FEW>, dim3(blocks), dim3(threads), smem(threads / 32, a.experts),
+                         stream, a.joined ? blocks : 1, "route launch", a);
+}
+
 template <typename T>
 int launch_route_type(const RouteArgs &a, int blocks, int threads, void *stream) {
     return with_row(a.experts, [&](auto lanes, auto values) {
         constexpr int L = decltype(lanes)::v, V = decltype(values)::v;
-        using R = Rows<T, L, V>;
-        const bool vec = vector_rows<T, V, R::L::C>(a), few = a.k <= 8;
-        const size_t smem = (vec ? threads / 32 * 2 * sizeof(R) : 0) +
-                            size_t(4) * (threads / 32 * a.experts + a.experts + 1);
-        auto kernel = vec ? (few ? route_kernel<T, L, V, true, true> : route_kernel<T, L, V, true, false>)
-                          : (few ? route_kernel<T, L, V, false, true> : route_kernel<T, L, V, false, false>);
-        if (smem > 40000) {
-            const int rc = cuda_status(
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)), "route attribute");
-            if (rc) return rc;
-        }
-        return launch_kernel(kernel, dim3(blocks), dim3(threads), smem, stream, a.joined ? blocks : 1, "route launch", a);
+        const bool vec = vector_rows<T, V, Rows<T, L, V>::L::C>(a), few = a.k <= 8;
+        return vec ? few ? launch_route_kernel<T, L, V, true, true>(a, blocks, threads, stream)
+                         : launch_route_kernel<T, L, V, true, false>(a, blocks, threads, stream)
+               : few ? launch_route_kernel<T, L, V, false, true>(a, blocks, threads, stream)
+                     : launch_route_kernel<T, L, V, false, false>(a, blocks, threads, stream);
     });
 }
 

@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/nest_train.h"
 #include "nest_internal.cuh"
 
@@ -31,6 +33,21 @@ int with_type(int32_t t, F fn) {
     if (t == NEST_F32) return fn(float{});
     if (t == NEST_BF16) return fn(__nv_bfloat16{});
     return fn(__half{});
+}
+
+// Lets KERNEL have up to `bytes` of dynamic shared memory on the current device: asked for once per
+// device, as the question costs as much as a launch.
+template <auto KERNEL>
+int allow_shared(size_t bytes, const char *what) {
+    static std::atomic<uint64_t> done{0};
+    int device = 0;
+    if (const int rc = cuda_status(cudaGetDevice(&device), what)) return rc;
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return NEST_OK;
+    const int rc = cuda_status(
+        cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)), what);
+    if (!rc) done.fetch_or(bit, std::memory_order_relaxed);
+    return rc;
 }
 
 // Copies from global to shared memory that the thread waits for later.

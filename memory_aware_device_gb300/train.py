@@ -17,6 +17,7 @@ the caller's stream, and there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 from typing import NamedTuple, Sequence
 
@@ -110,18 +111,18 @@ def _type(t, what: str) -> int:
 
 def _want(t, what: str, dtype, shape, device):
     """t as a contiguous tensor of this type, shape and device, or an error."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
     return t
 
 
-class _On:
-    """Makes a call's device current, and the stream given (new tensors belong to it), which is
-    recorded as a user of `used`; entered, the stream's handle."""
+class _Guard:
+    """A device made current, and a stream (new tensors belong to it), which is recorded as a user
+    of `used`; `leave` undoes it."""
 
-    def __init__(self, device, stream, used=()):
-        import torch
+    def __init__(self, device, stream, used):
+        torch = _torch
         self.guards = []
         if device.index != torch.cuda.current_device():
             self.guards.append(torch.cuda.device(device))
@@ -131,38 +132,23 @@ class _On:
                 for t in used:
                     if t is not None:
                         t.record_stream(stream)
-        self.index = device.index
-
-    def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return _raw_stream(self.index)
 
-    def __exit__(self, *exc):
+    def leave(self):
         for g in reversed(self.guards):
-            g.__exit__(*exc)
+            g.__exit__(None, None, None)
 
 
-class _Here:
-    """The current device and stream as they are."""
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        return _raw_stream(self.index)
-
-    def __exit__(self, *exc):
-        pass
-
-
-def _on(device, stream, used=()):
+def _enter(device, stream, used=()):
+    """Before a call on this device and stream (None = the device's current one): what has to be
+    left after it, or None where both are current."""
     torch = _torch or _load_torch()
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}: the operators run on CUDA devices only")
     if stream is None and device.index == torch.cuda.current_device():
-        return _Here(device.index)
-    return _On(device, stream, used)
+        return None
+    return _Guard(device, stream, used)
 
 
 # ---------------------------------------------------------------------------------
@@ -188,12 +174,12 @@ class Routing(NamedTuple):
         i, f = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
         out = _Buffers(torch.empty((tokens, k), **i), torch.empty((tokens, k), **f), torch.empty(experts, **i),
                        torch.empty(1, **i), torch.empty(experts, **f), torch.empty((), **f))
-        out.call = _RouteCall(tokens, experts, k, device, out)
+        out.call = _RouteCall(tokens, experts, k, device)
         return out
 
 
 class _Buffers(Routing):
-    """Buffers of `Routing.empty`, with the arguments of calls that write them."""
+    """Buffers of `Routing.empty`, with the workspace of calls that write them."""
     call = None
 
 
@@ -204,24 +190,21 @@ def _route_workspace(ref) -> int:
     return size
 
 
-class _RouteCall:
-    """The arguments of nest_route that stay the same for given sizes and result buffers."""
+@functools.lru_cache(maxsize=1024)
+def _described(*fields):
+    """A description of these numbers, by reference (what is passed on, not what it is of)."""
+    return C.byref(RouteDesc(*fields))
 
-    def __init__(self, tokens, experts, k, device, out):
+
+class _RouteCall:
+    """The workspace of calls of these sizes."""
+
+    def __init__(self, tokens, experts, k, device):
         import torch
         self.key = (tokens, experts, k, device)
-        self.desc = RouteDesc(tokens, experts, k, 0, 0, F32, 0)
-        self.ref = C.byref(self.desc)
-        size = _route_workspace(self.ref)
+        size = _route_workspace(_described(tokens, experts, k, 0, 0, F32, 0))
         self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
         self.tail = (self.workspace.data_ptr(), size)
-
-
-def _route_desc(logits, k: int, normalize: bool) -> RouteDesc:
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [tokens, experts], not of shape {tuple(logits.shape)}")
-    T, E = logits.shape
-    return RouteDesc(T, E, k, logits.stride(0), logits.stride(1), _type(logits, "logits"), 1 if normalize else 0)
 
 
 def _mask_ptr(mask, logits):
@@ -246,8 +229,9 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
     call = getattr(out, "call", None)
     if call is None or call.key != (T, E, k, dev):
         call = None
-        _route_workspace(C.byref(RouteDesc(T, E, k, 0, 0, dtype, 0)))
-    with _on(dev, stream, (logits, mask) + tuple(out or ())) as s:
+        _route_workspace(_described(T, E, k, 0, 0, dtype, 0))
+    guard = _enter(dev, stream, () if stream is None else (logits, mask, *(out or ())))
+    try:
         if out is None:
             out = Routing.empty(T, E, k, dev)
             call = out.call
@@ -259,15 +243,17 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
             _want(out.tokens, "out.tokens", torch.int32, (1,), dev)
             _want(out.mean_prob, "out.mean_prob", torch.float32, (E,), dev)
             _want(out.loss, "out.loss", torch.float32, (), dev)
-            call = _RouteCall(T, E, k, dev, out)
+            call = _RouteCall(T, E, k, dev)
         elif stream is not None:
             call.workspace.record_stream(stream)
-        d = call.desc
-        d.row_stride, d.col_stride = logits.stride()
-        d.dtype = dtype
-        d.normalize = 1 if normalize else 0
-        rc = _lib.nest_route(call.ref, logits.data_ptr(), None if mask is None else _mask_ptr(mask, logits),
-                             *[t.data_ptr() for t in out], *call.tail, s)
+        ids, weights, counts, tokens, mean_prob, loss = out
+        rc = _lib.nest_route(_described(T, E, k, *logits.stride(), dtype, 1 if normalize else 0), logits.data_ptr(),
+                             None if mask is None else _mask_ptr(mask, logits), ids.data_ptr(), weights.data_ptr(),
+                             counts.data_ptr(), tokens.data_ptr(), mean_prob.data_ptr(), loss.data_ptr(), *call.tail,
+                             _raw_stream(dev.index))
+    finally:
+        if guard is not None:
+            guard.leave()
     _check(rc, "nest_route")
     return out
 
@@ -277,10 +263,13 @@ def route_backward(logits, routing: Routing, grad_weights=None, grad_loss=None, 
     """nest_route_backward: gradient with respect to the logits, in their type, from the gradients
     of the weights (float32 [T, k]) and of the loss (float32 scalar tensor); None counts as zero.
     routing, mask and normalize as in the forward call."""
-    d = _route_desc(logits, routing.ids.shape[-1], normalize)
+    dtype = _type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [tokens, experts], not of shape {tuple(logits.shape)}")
     torch, dev = _torch, logits.device
-    T, E, k = d.tokens, d.experts, d.k
+    T, E = logits.shape
     ids, weights, counts, tokens = routing[:4]
+    k = ids.shape[-1]
     if T:   # an empty batch reads none of them
         _want(ids, "routing.ids", torch.int32, (T, k), dev)
         _want(weights, "routing.weights", torch.float32, (T, k), dev)
@@ -292,17 +281,25 @@ def route_backward(logits, routing: Routing, grad_weights=None, grad_loss=None, 
         _want(grad_loss, "grad_loss", torch.float32, grad_loss.shape, dev)
         if grad_loss.numel() != 1:
             raise ValueError(f"grad_loss must be one number, not of shape {tuple(grad_loss.shape)}")
-    used = (logits, mask, ids, weights, counts, tokens, grad_weights, grad_loss, out)
-    with _on(dev, stream, used) as s:
+    guard = _enter(dev, stream, () if stream is None else
+                   (logits, mask, ids, weights, counts, tokens, grad_weights, grad_loss, out))
+    try:
         if out is None:
             out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev or \
-                (E > 1 and out.stride(1) != 1) or (T > 1 and out.stride(0) < E):
-            raise ValueError(f"out must be a {logits.dtype} tensor of shape {(T, E)} on {dev} with rows of its own")
+            step = E
+        else:
+            step, col = out.stride() if out.dim() == 2 else (0, 0)
+            if out.dtype is not logits.dtype or out.shape != logits.shape or out.device != dev or \
+                    (E > 1 and col != 1) or (T > 1 and step < E):
+                raise ValueError(f"out must be a {logits.dtype} tensor of shape {(T, E)} on {dev} with rows of its own")
         rc = lib().nest_route_backward(
-            C.byref(d), logits.data_ptr(), _mask_ptr(mask, logits), ids.data_ptr(), weights.data_ptr(),
+            _described(T, E, k, *logits.stride(), dtype, 1 if normalize else 0), logits.data_ptr(),
+            None if mask is None else _mask_ptr(mask, logits), ids.data_ptr(), weights.data_ptr(),
             counts.data_ptr(), tokens.data_ptr(), None if grad_weights is None else grad_weights.data_ptr(),
-            None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), max(out.stride(0), E), s)
+            None if grad_loss is None else grad_loss.data_ptr(), out.data_ptr(), max(step, E), _raw_stream(dev.index))
+    finally:
+        if guard is not None:
+            guard.leave()
     _check(rc, "nest_route_backward")
     return out
 
@@ -399,10 +396,18 @@ class _Table:
         self.tail = (self.out.data_ptr(), self.workspace.data_ptr(), ws)
 
     def norm(self, max_norm, stream):
-        with _on(self.device, stream) as s:
-            rc = _lib.nest_grad_norm(*self.head, self.grad_type, max_norm, *self.tail, s)
+        guard = _enter(self.device, stream, () if stream is None else self.held())
+        try:
+            rc = _lib.nest_grad_norm(*self.head, self.grad_type, max_norm, *self.tail, _raw_stream(self.device.index))
+        finally:
+            if guard is not None:
+                guard.leave()
         _check(rc, "nest_grad_norm")
         return self.out
+
+    def held(self):
+        """Every tensor that the list's calls use."""
+        return (self.table, self.workspace, self.out, *self.keep[0], *self.keep[1])
 
 
 class GradNorm:
@@ -424,8 +429,8 @@ class AdamW:
     weights, grads: lists of contiguous CUDA tensors, each list of one type (float32, bfloat16 or
     float16); the step reads the gradients and updates the weights in place.  The object owns the
     float32 master weights (weights of 16 bits only), the moments m and v (state_bits 32: float32;
-    8: uint8 codes with the scales m_exp and v_exp) and the device's step count.  Buffers hold
-    the tensors in order, each from a multiple of 256 elements on (`starts`).  weight_decay and
+    8: uint8 codes with the scales m_exp and v_exp) and the device's step count: copy into them to
+    set them.  Buffers hold the tensors in order, each from a multiple of 256 elements on (`starts`).  weight_decay and
     lr_scale: one number, or one per tensor."""
 
     def __init__(self, weights: Sequence, grads: Sequence, state_bits: int = 32, betas=(0.9, 0.999),
@@ -456,6 +461,8 @@ class AdamW:
                                ptr(self.master), ptr(self.m), ptr(self.v), ptr(self.m_exp), ptr(self.v_exp),
                                self._state.data_ptr(), None)
         self._ref = C.byref(self._args)
+        self._codes = tuple(ptr(t) for t in (self.m, self.v, self.m_exp, self.v_exp))
+        self._length = n
         self.set_step(0)
 
     def set_step(self, step: int):
@@ -493,20 +500,31 @@ class AdamW:
                 raise ValueError(f"grad_scale must be one float32 number on {tb.device}")
             a.grad_scale = grad_scale.data_ptr()
         a.lr = lr
-        with _on(tb.device, stream, () if grad_scale is None else (grad_scale,)) as s:
-            rc = _lib.nest_adamw(*tb.head, self._ref, s)
+        guard = _enter(tb.device, stream, () if stream is None else (grad_scale, *self._held()))
+        try:
+            rc = _lib.nest_adamw(*tb.head, self._ref, _raw_stream(tb.device.index))
+        finally:
+            if guard is not None:
+                guard.leave()
         _check(rc, "nest_adamw")
+
+    def _held(self):
+        return (self._state, self.master, self.m, self.v, self.m_exp, self.v_exp, *self._table.held())
 
     def state_values(self, stream=None):
         """(m, v): the moments, laid out like the object's buffers.  With 8-bit states new bfloat16
         tensors with the exact values of the codes, else the float32 buffers themselves."""
-        import torch
         if self.state_bits == 32:
             return self.m, self.v
-        tb = self._table
-        with _on(tb.device, stream, (self.m, self.v, self.m_exp, self.v_exp)) as s:
-            m, v = (torch.empty(self.m.numel(), dtype=torch.bfloat16, device=tb.device) for _ in "mv")
-            rc = _lib.nest_adamw_values(tb.head[0], self.m.data_ptr(), self.v.data_ptr(),
-                                         self.m_exp.data_ptr(), self.v_exp.data_ptr(), m.data_ptr(), v.data_ptr(), s)
+        tb, kind = self._table, _torch.bfloat16
+        guard = _enter(tb.device, stream, () if stream is None else self._held())
+        try:
+            m = _torch.empty(self._length, dtype=kind, device=tb.device)
+            v = _torch.empty(self._length, dtype=kind, device=tb.device)
+            rc = _lib.nest_adamw_values(tb.head[0], *self._codes, m.data_ptr(), v.data_ptr(),
+                                        _raw_stream(tb.device.index))
+        finally:
+            if guard is not None:
+                guard.leave()
         _check(rc, "nest_adamw_values")
         return m, v
