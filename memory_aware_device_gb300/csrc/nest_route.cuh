@@ -9,8 +9,7 @@
 // Choice of the k largest.  A logit becomes a 32-bit word whose order is that of the logits,
 // with its lowest bits replaced by the complement of the expert's index: all words of a row
 // differ, and among logits that agree in the bits kept the lower index is the larger word.
-// Each lane sorts its words once and keeps as many as can be chosen; then k rounds take the
-// maximum over the row's lanes, and the lane that had it moves its list up.  16-bit logits
+// Each lane sorts its words once and keeps the largest; then k rounds take the maximum over the row's lanes, and the lane that had it moves its list up.  16-bit logits
 // lose nothing to the index.  With 32-bit logits up to 10 bits are lost, and the word comes
 // from the exponent (x - top) log2(e), negative for every x, which may round two logits to
 // one: one more round gives the largest word left, and if two of these neighbours agree in
@@ -264,50 +263,63 @@ __device__ __forceinline__ bool row_any(bool b) {
     return (all >> (threadIdx.x & 31 & ~(LANES - 1)) & ((1u << (LANES & 31)) - 1)) != 0;
 }
 
-// Sorts w[A .. A + N) downwards (N a power of two): Batcher's merging of odd and even parts.
+template <int I, int J, int V>
+__device__ __forceinline__ void exchange(uint32_t (&w)[V]) {   // the larger to I
+    const uint32_t hi = max(w[I], w[J]), lo = min(w[I], w[J]);
+    w[I] = hi;
+    w[J] = lo;
+}
+// Batcher's merge of the sorted elements A, A + 2 R, .. and A + R, A + 3 R, .. below A + N.
+template <int A, int N, int R, int V>
+__device__ __forceinline__ void merge_odd_even(uint32_t (&w)[V]);
+template <int I, int END, int R, int V>
+__device__ __forceinline__ void exchange_neighbours(uint32_t (&w)[V]) {
+    if constexpr (I + R < END) {
+        exchange<I, I + R>(w);
+        exchange_neighbours<I + 2 * R, END, R>(w);
+    }
+}
+template <int A, int N, int R, int V>
+__device__ __forceinline__ void merge_odd_even(uint32_t (&w)[V]) {
+    if constexpr (2 * R < N) {
+        merge_odd_even<A, N, 2 * R>(w);
+        merge_odd_even<A + R, N, 2 * R>(w);
+        exchange_neighbours<A + R, A + N, R>(w);
+    } else {
+        exchange<A, A + R>(w);
+    }
+}
+// Sorts w[A .. A + N) downwards, N a power of two.  (By recursion: a loop that the compiler leaves
+// rolled would put w into memory.)
 template <int A, int N, int V>
 __device__ __forceinline__ void sort_down(uint32_t (&w)[V]) {
-#pragma unroll
-    for (int p = 1; p < N; p *= 2)
-#pragma unroll
-        for (int q = p; q > 0; q /= 2)
-#pragma unroll
-            for (int j = q % p; j < N - q; j += 2 * q)
-#pragma unroll
-                for (int i = 0; i < q; i++)
-                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const int u = A + i + j, l = u + q;
-                        const uint32_t hi = max(w[u], w[l]), lo = min(w[u], w[l]);
-                        w[u] = hi;
-                        w[l] = lo;
-                    }
+    if constexpr (N > 1) {
+        sort_down<A, N / 2>(w);
+        sort_down<A + N / 2, N / 2>(w);
+        merge_odd_even<A, N, 1>(w);
+    }
 }
 
-// Leaves the 8 largest of w, downwards, in w[0 .. 8): sorted eights, merged in pairs.  Of two
-// sorted eights the larger of each element and the other's mirror image are the 8 largest, in
-// an order that three rounds of exchanges sort.
-template <int V>
-__device__ __forceinline__ void largest_eight(uint32_t (&w)[V]) {
-    static_assert(V % 8 == 0, "whole eights");
-    sort_down<0, 8>(w);
-    if constexpr (V >= 16) sort_down<8, 8>(w);
-    if constexpr (V >= 32) {
-        sort_down<16, 8>(w);
-        sort_down<24, 8>(w);
-    }
+// Leaves the N largest of w, downwards, in w[0 .. N): sorted runs of N, merged in pairs.  Of two
+// sorted runs the larger of each element and the other's mirror image are the N largest, in an
+// order that log2(N) rounds of exchanges sort.
+template <int N, int V>
+__device__ __forceinline__ void keep_largest(uint32_t (&w)[V]) {
+    static_assert(V % N == 0 && V / N <= 4, "whole runs, at most four");
+    sort_down<0, N>(w);
+    if constexpr (V / N >= 2) sort_down<N, N>(w);
+    if constexpr (V / N >= 3) sort_down<2 * N, N>(w);
+    if constexpr (V / N >= 4) sort_down<3 * N, N>(w);
 #pragma unroll
-    for (int step = 8; step < V; step *= 2)
+    for (int step = N; step < V; step *= 2)
 #pragma unroll
         for (int at = 0; at + step < V; at += 2 * step) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                // the other's mirror image is read before either is changed: it is not written
-                w[at + i] = max(w[at + i], w[at + step + 7 - i]);
-            }
+            for (int i = 0; i < N; i++) w[at + i] = max(w[at + i], w[at + step + N - 1 - i]);
 #pragma unroll
-            for (int q = 4; q; q /= 2)
+            for (int q = N / 2; q; q /= 2)
 #pragma unroll
-                for (int i = 0; i < 8; i++)
+                for (int i = 0; i < N; i++)
                     if (!(i & q)) {
                         const uint32_t hi = max(w[at + i], w[at + i + q]), lo = min(w[at + i], w[at + i + q]);
                         w[at + i] = hi;
@@ -351,22 +363,20 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const T *row,
 }
 
 // Lane g of a row's LANES gets in slot s the row's chosen expert number s LANES + g, or -1.  w:
-// the words of the lane's values.  FEW: k is at most 8, and one slot is enough.  again: the row's
+// the words of the lane's values.  FEW: k is at most 8, and one slot is enough; lists of 8 words
+// serve it, and lists of 16 any k, but for rows that draw on one lane more often than that.  again: the row's
 // words cannot be used; idle: nothing is chosen in the row.
 template <typename T, int V, int LANES, bool FEW, int SLOTS>
 __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_t (&w)[V], bool again, bool idle,
                                        int (&id)[SLOTS]) {
     constexpr uint32_t kIndex = LANES * V - 1;   // the bits that hold the index
     constexpr bool kWhole = sizeof(T) == 2;      // no bit of a logit is lost
-    constexpr int kList = FEW && V > 8 ? 8 : V;
+    constexpr int kMost = FEW ? 8 : 16, kList = V < kMost ? V : kMost;   // words kept of a lane's
     const int k = a.k, g = threadIdx.x & (LANES - 1);
     uint32_t mine[SLOTS], last = 0;
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) mine[s] = 0;
-    if constexpr (kList < V)
-        largest_eight<V>(w);
-    else
-        sort_down<0, V>(w);
+    keep_largest<kList>(w);
     if constexpr (FEW) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
@@ -388,14 +398,14 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
                 if (g == j) mine[s] = last;
                 if (w[0] == last) {
 #pragma unroll
-                    for (int i = 0; i + 1 < V; i++) w[i] = w[i + 1];
-                    w[V - 1] = 0;
+                    for (int i = 0; i + 1 < kList; i++) w[i] = w[i + 1];
+                    w[kList - 1] = 0;
                 }
             }
     }
+    // a lane whose words are used up may have had more (8 of them and k = 8: no more was wanted)
+    if (kList < V && !(FEW && kWhole)) again |= row_any<LANES>(w[0] == 0u);
     if (!kWhole) {
-        // a list of 8 that is used up may have had more
-        if (kList < V) again |= row_any<LANES>(w[0] == 0u);
         uint32_t next = row_largest<LANES>(w[0]);
         bool close = ((last ^ next) & ~kIndex) == 0;
 #pragma unroll
