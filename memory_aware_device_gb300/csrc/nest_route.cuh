@@ -1,10 +1,10 @@
 // Kernels of the routing operators (definitions in nest_train.h), one instantiation per
 // element type in nest_route_f32.cu, nest_route_bf16.cu and nest_route_f16.cu.
 //
-// Forward, a warp takes 32 / LANES rows at a time, each held in the registers of LANES lanes
-// with up to 32 values per lane, so that the logits are read once and what is done per row
-// (reductions, rounds, results) is shared by several rows; backward, a row at a time.  Logits are
-// read in pieces of up to 32 bytes per lane where alignment allows (VEC).
+// A warp takes 32 / LANES rows at a time, each held in the registers of LANES lanes, so that the
+// logits are read once and what is done per row (reductions, rounds, results) is shared by
+// several rows: forward up to 32 values per lane, backward, which has little of that, 8 where
+// the row allows.  Logits are read in pieces per lane where alignment allows (VEC).
 //
 // Choice of the k largest.  A logit becomes a 32-bit word whose order is that of the logits,
 // with its lowest bits replaced by the complement of the expert's index: all words of a row
@@ -196,37 +196,6 @@ struct RowExp {
     __device__ __forceinline__ float near(float x) const { return fmaf(x, kLog2e, -shift); }
     __device__ __forceinline__ float of(float x) const { return far ? (x - top) * kLog2e : near(x); }
 };
-
-// Whether a fetched row is live; x, its largest value, e = exp(x - top) and their sum.
-template <typename T, int V>
-__device__ __forceinline__ bool gates_of(const T (&raw)[V], float (&x)[V], float (&e)[V], float &top, float &sum) {
-    top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-        x[i] = to_f32(raw[i]);
-        top = fmaxf(top, x[i]);
-    }
-    top = warp_max(top);
-    if (!(top > -INFINITY)) {   // closed, unless NaN is in it
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < V; i++) nan |= isnan(x[i]);
-        if (!__any_sync(0xffffffffu, nan)) return false;
-    }
-    const RowExp ex(top);
-    if (ex.far) {
-#pragma unroll
-        for (int i = 0; i < V; i++) e[i] = exp2_of(ex.of(x[i]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; i++) e[i] = exp2_of(ex.near(x[i]));
-    }
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; i++) sum += e[i];
-    sum = warp_sum(sum);
-    return true;
-}
 
 // Over the LANES lanes of a row.
 template <int LANES>
@@ -630,78 +599,119 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
 // w grad_weight for plain ones, dot = sum of w grad_weight over the row's chosen; only plain
 // gates leave dot in the row's mean.  The counts enter as c - k n / E: a constant in d
 // drops out of the gradient, and without it the subtraction of the mean loses no digits.
-// The k terms reach their experts' lanes through the warp's row of shared memory.
-template <typename T, int V, bool VEC>
+// The k terms reach their experts' lanes through the row's share of shared memory.
+template <typename T, int LANES, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(BackwardShape<V>::kThreads, BackwardShape<V>::kPerSm) route_backward_kernel(RouteArgs a) {
-    constexpr int kWarps = BackwardShape<V>::kWarps;
-    using L = Place<V, VEC>;
-    extern __shared__ unsigned char sh[];
+    constexpr int kWarps = BackwardShape<V>::kWarps, kRows = 32 / LANES, kSlots = FEW ? 1 : 32 / LANES;
+    using L = Place<V, VEC, LANES>;
+    extern __shared__ __align__(16) unsigned char sh[];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *extra = reinterpret_cast<float *>(sh) + warp * (32 * V);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane & (LANES - 1);
+    float *const extra = reinterpret_cast<float *>(sh) + warp * (32 * V) + lane / LANES * (LANES * V);   // the row's
 #pragma unroll
-    for (int i = 0; i < V; i++) extra[lane + 32 * i] = 0.0f;
+    for (int i = 0; i < V; i++) extra[g + LANES * i] = 0.0f;
     const float n = float(*a.live), even = float(a.k) * n / float(a.experts);
     const float f = a.grad_loss && n > 0.0f ? *a.grad_loss * float(a.experts) / (float(a.k) * n * n) : 0.0f;
     float own[V];
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        const int e = L::of(i, lane);
+        const int e = L::of(i, g);
         own[i] = e < a.experts ? f * (float(a.counts[e]) - even) : 0.0f;
     }
-    __syncwarp();
-    const int64_t stride = int64_t(gridDim.x) * kWarps;
-    int64_t t = int64_t(blockIdx.x) * kWarps + warp;
-    T raw[V];
-    int id = -1;
-    float w = 0.0f, u = 0.0f;
-    auto fetch = [&](int64_t row) {
-        if (row >= a.tokens || (a.mask && !a.mask[row])) return false;
-        fetch_row<T, V, VEC>(a, static_cast<const T *>(a.logits) + row * a.row_stride, lane, raw);
-        id = -1;
-        w = u = 0.0f;
-        if (a.grad_weights && lane < a.k) {
-            id = a.ids[row * a.k + lane];
-            w = a.weights[row * a.k + lane];
-            u = a.grad_weights[row * a.k + lane];
-            if (uint32_t(id) >= uint32_t(a.experts)) {
-                id = -1;
-                w = u = 0.0f;
-            }
-        }
-        return true;
-    };
-    bool on = fetch(t);
-    for (; t < a.tokens; t += stride) {
-        float x[V], e[V], top, sum;
-        const bool is_live = on && gates_of<T, V>(raw, x, e, top, sum);
-        const float dot = warp_sum(w * u), term = a.normalize ? w * (u - dot) : w * u;
-        const int to = id;
-        on = fetch(t + stride);
-        T out[V];
-        if (is_live) {
-            float mean = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; i++) mean = fmaf(e[i], own[i], mean);
-            const float inv = __fdividef(1.0f, sum);
-            mean = warp_sum(mean) * inv;
-            if (!a.normalize) mean += dot;
-            if (to >= 0) extra[to] = term;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < V; i++)
-                out[i] = from_f32<T>(fmaf(e[i] * inv, own[i] - mean, extra[L::of(i, lane)]));
-            __syncwarp();
-            if (to >= 0) extra[to] = 0.0f;
+    const int64_t stride = int64_t(gridDim.x) * kWarps * kRows;
+    alignas(16) T raw[V];
+    int id[kSlots];
+    float w[kSlots], u[kSlots];
+    // what row t needs, as the lane holds it; whether the row counts
+    auto fetch = [&](int64_t t) {
+        const bool on = t < a.tokens && !(a.mask && !a.mask[t]);
+        if (on) {
+            fetch_row<T, V, VEC, LANES>(a, static_cast<const T *>(a.logits) + t * a.row_stride, g, raw);
         } else {
 #pragma unroll
-            for (int i = 0; i < V; i++) out[i] = from_f32<T>(0.0f);
+            for (int i = 0; i < V; i++) raw[i] = from_f32<T>(-INFINITY);
         }
+#pragma unroll
+        for (int s = 0; s < kSlots; s++) {
+            const int j = s * LANES + g;
+            id[s] = -1;
+            w[s] = u[s] = 0.0f;
+            if (on && a.grad_weights && j < a.k) {
+                id[s] = a.ids[t * a.k + j];
+                w[s] = a.weights[t * a.k + j];
+                u[s] = a.grad_weights[t * a.k + j];
+                if (uint32_t(id[s]) >= uint32_t(a.experts)) {
+                    id[s] = -1;
+                    w[s] = u[s] = 0.0f;
+                }
+            }
+        }
+        return on;
+    };
+    int64_t t = (int64_t(blockIdx.x) * kWarps + warp) * kRows + lane / LANES;
+    bool on = fetch(t);
+    for (; t - lane / LANES < a.tokens; t += stride) {
+        float e[V], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            e[i] = to_f32(raw[i]);
+            top = fmaxf(top, e[i]);
+        }
+        top = row_max<LANES>(top);
+        bool is_live = top > -INFINITY;
+        if (__any_sync(0xffffffffu, on && !is_live)) {   // closed, unless NaN is in it
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < V; i++) nan |= isnan(e[i]);
+            is_live |= row_any<LANES>(nan);
+        }
+        const RowExp ex(top > -INFINITY ? top : 0.0f);
+        if (__any_sync(0xffffffffu, ex.far)) {
+#pragma unroll
+            for (int i = 0; i < V; i++) e[i] = exp2_of(ex.of(e[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) e[i] = exp2_of(ex.near(e[i]));
+        }
+        float sum = 0.0f, mean = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            sum += e[i];
+            mean = fmaf(e[i], own[i], mean);
+        }
+#pragma unroll
+        for (int s = 0; s < kSlots; s++) dot = fmaf(w[s], u[s], dot);
+        sum = row_sum<LANES>(sum);
+        mean = row_sum<LANES>(mean);
+        dot = row_sum<LANES>(dot);
+        const float inv = __fdividef(1.0f, sum);
+        mean *= inv;
+        if (!a.normalize) mean += dot;
+        int to[kSlots];
+        __syncwarp();   // the last rows' terms are gone
+#pragma unroll
+        for (int s = 0; s < kSlots; s++) {
+            to[s] = id[s];
+            if (to[s] >= 0) extra[to[s]] = a.normalize ? w[s] * (u[s] - dot) : w[s] * u[s];
+        }
+        on = fetch(t + stride);
+        __syncwarp();
+        alignas(16) T out[V];
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            const float d = fmaf(e[i] * inv, own[i] - mean, extra[L::of(i, g)]);
+            out[i] = from_f32<T>(is_live ? d : 0.0f);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < kSlots; s++)
+            if (to[s] >= 0) extra[to[s]] = 0.0f;
+        if (t >= a.tokens) continue;
         T *row = static_cast<T *>(a.grad) + t * a.grad_stride;
 #pragma unroll
         for (int i = 0; i < V; i += L::C) {
-            const int e0 = L::of(i, lane);
+            const int e0 = L::of(i, g);
             if (e0 >= a.experts) continue;
             if (VEC && a.vector_grad) {
                 store_piece<T, L::C>(row + e0, out + i);
@@ -727,15 +737,15 @@ int with_row(int experts, F fn) {
     return fn(Number<32>{}, Number<32>{});
 }
 
-// fn(values): a row of `experts` in a whole warp.
+// fn(lanes, values) likewise for the backward kernel: at most 8 values each up to a whole warp.
 template <typename F>
-int with_values(int experts, F fn) {
-    if (experts <= 32) return fn(Number<1>{});
-    if (experts <= 64) return fn(Number<2>{});
-    if (experts <= 128) return fn(Number<4>{});
-    if (experts <= 256) return fn(Number<8>{});
-    if (experts <= 512) return fn(Number<16>{});
-    return fn(Number<32>{});
+int with_backward_row(int experts, F fn) {
+    if (experts <= 32) return fn(Number<8>{}, Number<4>{});
+    if (experts <= 64) return fn(Number<8>{}, Number<8>{});
+    if (experts <= 128) return fn(Number<16>{}, Number<8>{});
+    if (experts <= 256) return fn(Number<32>{}, Number<8>{});
+    if (experts <= 512) return fn(Number<32>{}, Number<16>{});
+    return fn(Number<32>{}, Number<32>{});
 }
 
 // Whether every row can be read in pieces of C neighbours.
@@ -774,14 +784,17 @@ int launch_route_type(const RouteArgs &a, int blocks, int threads, void *stream)
 
 template <typename T>
 int launch_route_backward_type(RouteArgs a, void *stream) {
-    return with_values(a.experts, [&](auto v) {
-        constexpr int V = decltype(v)::v;
+    return with_backward_row(a.experts, [&](auto lanes, auto values) {
+        constexpr int N = decltype(lanes)::v, V = decltype(values)::v;
         using S = BackwardShape<V>;
-        constexpr int C = Place<V, true>::C;
-        a.vector_grad = a.grad_stride % C == 0 && aligned_to(a.grad, C * sizeof(T));
+        using L = Place<V, true, N>;
+        a.vector_grad = a.grad_stride % L::C == 0 && aligned_to(a.grad, L::C * sizeof(T));
         const size_t smem = size_t(4) * S::kWarps * 32 * V;
-        const int64_t b = (a.tokens + S::kWarps - 1) / S::kWarps, most = kSMs * S::kPerSm;
-        auto kernel = vector_rows<T, V, C>(a) ? route_backward_kernel<T, V, (V > 1)> : route_backward_kernel<T, V, false>;
+        const int64_t rows = S::kWarps * 32 / N, b = (a.tokens + rows - 1) / rows, most = kSMs * S::kPerSm;
+        const bool vec = vector_rows<T, V, L::C>(a), few = a.k <= N;
+        auto kernel = vec ? few ? route_backward_kernel<T, N, V, true, true> : route_backward_kernel<T, N, V, true, N == 32>
+                          : few ? route_backward_kernel<T, N, V, false, true>
+                                : route_backward_kernel<T, N, V, false, N == 32>;
         return launch_kernel(kernel, dim3(unsigned(b < most ? b : most)), dim3(S::kThreads), smem, stream, 1,
                              "route backward launch", a);
     });
