@@ -383,33 +383,37 @@ __device__ __forceinline__ void store_own(uint8_t *p, int n, int lane, uint2 c) 
         if (8 * lane + i < n) p[8 * lane + i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
 }
 
-// What a warp needs of a block whose moments are in 8 bits, each lane its own share in planes
-// of 16 or 8 bytes per lane.  The codes' decoding and encoding leave too few warps on an SM to
-// cover the memory's latency with one block each, so blocks are copied ahead.
+// What a warp needs of a block whose moments are in 8 bits, as it lies in memory.  The codes'
+// decoding and encoding leave too few warps on an SM to cover the memory's latency with one
+// block each, so blocks are copied ahead.
 constexpr int kAhead = 3;
 template <typename G>
 struct Stage {
-    uint4 grad[sizeof(G) / 2][32];
-    uint4 master[2][32];
-    uint2 m[32], v[32];
+    alignas(16) G grad[kBlock];
+    alignas(16) float master[kBlock];
+    alignas(16) uint8_t m[kBlock], v[kBlock];
 
     __device__ __forceinline__ void copy(const G *g, const float *p, const uint8_t *cm, const uint8_t *cv, int lane) {
+        constexpr int kG = 16 / sizeof(G);   // neighbouring lanes copy neighbouring 16 bytes
 #pragma unroll
-        for (int i = 0; i < int(sizeof(G) / 2); i++) copy_ahead<16>(&grad[i][lane], g + 8 * lane + i * (16 / sizeof(G)));
+        for (int i = kG * lane; i < kBlock; i += 32 * kG) copy_ahead<16>(grad + i, g + i);
 #pragma unroll
-        for (int i = 0; i < 2; i++) copy_ahead<16>(&master[i][lane], p + 8 * lane + 4 * i);
-        copy_ahead<8>(&m[lane], cm + 8 * lane);
-        copy_ahead<8>(&v[lane], cv + 8 * lane);
+        for (int i = 4 * lane; i < kBlock; i += 32 * 4) copy_ahead<16>(master + i, p + i);
+        copy_ahead<8>(m + 8 * lane, cm + 8 * lane);
+        copy_ahead<8>(v + 8 * lane, cv + 8 * lane);
     }
     __device__ __forceinline__ void read(G (&g)[8], float (&p)[8], uint2 &cm, uint2 &cv, int lane) const {
 #pragma unroll
-        for (int i = 0; i < int(sizeof(G) / 2); i++) reinterpret_cast<uint4 *>(g)[i] = grad[i][lane];
+        for (int i = 0; i < int(sizeof(G) / 2); i++)
+            reinterpret_cast<uint4 *>(g)[i] = reinterpret_cast<const uint4 *>(grad + 8 * lane)[i];
 #pragma unroll
-        for (int i = 0; i < 2; i++) reinterpret_cast<uint4 *>(p)[i] = master[i][lane];
-        cm = m[lane];
-        cv = v[lane];
+        for (int i = 0; i < 2; i++)
+            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(master + 8 * lane)[i];
+        cm = *reinterpret_cast<const uint2 *>(m + 8 * lane);
+        cv = *reinterpret_cast<const uint2 *>(v + 8 * lane);
     }
 };
+
 // Magnitudes of m and v (as bits) from which a block's codes take the checked path: 1.75 * 2^14
 // and 1.75 * 2^30, above which the scale is no single factor; infinity; NaN.
 constexpr uint32_t kRareM = (uint32_t(14 + 127) << 23) | 0x600000u, kRareV = (uint32_t(30 + 127) << 23) | 0x600000u;
@@ -473,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
             copies_mark();
         };
         if constexpr (EIGHT) {
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < kAhead; i++) ahead(i);
         }
@@ -491,12 +496,14 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
                     lane_sm = a.m_exp[block + lane * step];
                     lane_sv = a.v_exp[block + lane * step];
                 }
+                __syncwarp();   // the block before is read, and its place free
                 ahead(k + kAhead);
                 sm = __shfl_sync(0xffffffffu, lane_sm, k % 32);
                 sv = __shfl_sync(0xffffffffu, lane_sv, k % 32);
             }
             if (EIGHT && k < whole) {
                 copies_wait<kAhead>();
+                __syncwarp();
                 stages[k % (kAhead + 1)].read(g, p, cm, cv, lane);
             } else {
                 load_block(grad + j0, n, wide_g, lane, room[warp], g);

@@ -117,7 +117,7 @@ def test_sizes(T, E, k, dtype):
     both(logits(T, E, dtype, T + E).cuda(), k, normalize=(T + k) % 2 == 0, dtype=dtype)
 
 
-@pytest.mark.parametrize("dtype,E,normalize", itertools.product(["fp32", "bf16"], [5, 64, 250], [True, False]))
+@pytest.mark.parametrize("dtype,E,normalize", list(itertools.product(["fp32", "bf16"], [5, 64, 250], [True, False])))
 def test_mask_closed_and_ties(dtype, E, normalize):
     """Padding rows full of NaN, closed experts (fewer than k open in the second call), equal logits."""
     x = logits(333, E, dtype, E, ties=True, closed=E // 4).cuda()
