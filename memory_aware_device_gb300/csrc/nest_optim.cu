@@ -760,7 +760,7 @@ int nest_adamw(const nest_table_info *info, const void *table, const nest_adamw_
             if (p->state_bits == 32)
                 return launch_kernel(adamw_kernel<W, G, false>, grid, dim3(kThreads), 0, stream, 1, "adamw launch", a);
             constexpr int kStages = int(sizeof(Stage<G>)) * kWarps * (kAhead + 1);
-            const int rc = allow_shared<adamw_kernel<W, G, true>>(kStages, "adamw attribute");
+            const int rc = allow<adamw_kernel<W, G, true>>(kStages, "adamw attribute");
             return rc ? rc
                       : launch_kernel(adamw_kernel<W, G, true>, grid, dim3(kThreads), kStages, stream, 1,
                                       "adamw launch", a);

@@ -72,9 +72,9 @@ int check(const nest_route_desc *d) {
 }
 
 // The forward kernel's blocks and threads, and whether the blocks are one cluster: up to
-// kJoined passes of it over the rows are quicker than a second launch.  A single block is no
-// larger than its rows need.
-constexpr int kJoined = 4;
+// kJoined passes of it over the rows (2048 x 64: two passes of a cluster 7.8 us, two launches 6.8).
+// A single block is no larger than its rows need.
+constexpr int kJoined = 1;
 struct Grid {
     int blocks, threads;
     bool joined;

@@ -12,8 +12,9 @@
 // Each lane sorts its words once and keeps the largest; then k rounds take the maximum over the row's lanes, and the lane that had it moves its list up.  16-bit logits
 // lose nothing to the index.  With 32-bit logits up to 10 bits are lost, and the word comes
 // from the exponent (x - top) log2(e), negative for every x, which may round two logits to
-// one: one more round gives the largest word left, and if two of these neighbours agree in
-// the bits kept, the row's choice is made again on whole logits.  So it is where a gate is NaN.
+// one: one more round gives the largest word left, and where two of these neighbours agree in
+// the bits kept their logits are compared.  Where more than two agree, or a gate is NaN, the
+// row's choice is made again on whole logits.
 //
 // Sums.  Every lane adds up the gates of its experts in registers, the block adds its warps in
 // order, and the blocks' rows are added in a fixed order, so no result depends on the order in
@@ -70,7 +71,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8;
+constexpr int kCluster = 8;   // blocks of the joined form, and of the kernel that adds up the others
 constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ float exp2_of(float x) {   // results below 2^-126 are 0
@@ -297,6 +298,21 @@ __device__ __forceinline__ void keep_largest(uint32_t (&w)[V]) {
         }
 }
 
+// Of values held one per chosen expert (number s LANES + g in slot s of lane g), the one of the
+// next and of the previous expert.
+template <int LANES, int SLOTS>
+__device__ __forceinline__ uint32_t following(const uint32_t (&v)[SLOTS], int s) {
+    const uint32_t in = __shfl_down_sync(0xffffffffu, v[s], 1, LANES);
+    const uint32_t over = __shfl_sync(0xffffffffu, v[s + 1 < SLOTS ? s + 1 : s], 0, LANES);
+    return (threadIdx.x & (LANES - 1)) == LANES - 1 ? over : in;
+}
+template <int LANES, int SLOTS>
+__device__ __forceinline__ uint32_t preceding(const uint32_t (&v)[SLOTS], int s) {
+    const uint32_t in = __shfl_up_sync(0xffffffffu, v[s], 1, LANES);
+    const uint32_t over = __shfl_sync(0xffffffffu, v[s > 0 ? s - 1 : s], LANES - 1, LANES);
+    return (threadIdx.x & (LANES - 1)) == 0 ? over : in;
+}
+
 // The choice on whole logits, which are read again, for the rows whose lanes have `wanted` set
 // (all lanes of the warp take part): lane g of a row's LANES gets in slot s the chosen expert
 // number s LANES + g, or -1.
@@ -342,7 +358,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
     constexpr bool kWhole = sizeof(T) == 2;      // no bit of a logit is lost
     constexpr int kMost = FEW ? 8 : 16, kList = V < kMost ? V : kMost;   // words kept of a lane's
     const int k = a.k, g = threadIdx.x & (LANES - 1);
-    uint32_t mine[SLOTS], last = 0;
+    uint32_t mine[SLOTS];
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) mine[s] = 0;
     keep_largest<kList>(w);
@@ -350,12 +366,12 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             if (j >= k) break;
-            last = row_largest<LANES>(w[0]);
+            const uint32_t last = row_largest<LANES>(w[0]);
             if (g == j) mine[0] = last;
             if (w[0] == last) {   // of a list only what the rounds left can reach is moved
 #pragma unroll
                 for (int i = 0; i < kList; i++)
-                    if (i < 8 - j) w[i] = i + 1 < kList ? w[i + 1 < kList ? i + 1 : i] : 0u;
+                    if (i < 9 - j) w[i] = i + 1 < kList ? w[i + 1 < kList ? i + 1 : i] : 0u;
             }
         }
     } else {
@@ -363,7 +379,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
         for (int s = 0; s < SLOTS; s++)
 #pragma unroll 1
             for (int j = 0; j < LANES && s * LANES + j < k; j++) {
-                last = row_largest<LANES>(w[0]);
+                const uint32_t last = row_largest<LANES>(w[0]);
                 if (g == j) mine[s] = last;
                 if (w[0] == last) {
 #pragma unroll
@@ -374,26 +390,76 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
     }
     // a lane whose words are used up may have had more (8 of them and k = 8: no more was wanted)
     if (kList < V && !(FEW && kWhole)) again |= row_any<LANES>(w[0] == 0u);
-    if (!kWhole) {
-        uint32_t next = row_largest<LANES>(w[0]);
-        bool close = ((last ^ next) & ~kIndex) == 0;
-#pragma unroll
-        for (int s = SLOTS - 1; s >= 0; s--) {   // each chosen word against the one after it
-            uint32_t up = __shfl_down_sync(0xffffffffu, mine[s], 1, LANES);
-            if (s + 1 < SLOTS) {
-                const uint32_t over = __shfl_sync(0xffffffffu, mine[s + 1 < SLOTS ? s + 1 : s], 0, LANES);
-                if (g == LANES - 1) up = over;
-            } else if (g == LANES - 1) {
-                up = ~mine[s];
-            }
-            close |= s * LANES + g < k - 1 && ((mine[s] ^ up) & ~kIndex) == 0;
-            // the words of closed experts and of logits that overflow the exponent are alike
-            close |= s * LANES + g < k && mine[s] <= kClosed;
-        }
-        again |= row_any<LANES>(close);
-    }
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) id[s] = mine[s] > kClosed ? int(kIndex - (mine[s] & kIndex)) : -1;
+    if (!kWhole) {
+        const uint32_t next = row_largest<LANES>(w[0]);
+        bool tie[SLOTS], any_tie = false, missing = false;   // with the word after it; nothing to choose
+#pragma unroll
+        for (int s = 0; s < SLOTS; s++) {
+            const int j = s * LANES + g;
+            uint32_t after = following<LANES, SLOTS>(mine, s);   // by every lane: it exchanges values
+            if (j == k - 1) after = next;
+            tie[s] = j < k && mine[s] > kClosed && ((mine[s] ^ after) & ~kIndex) == 0;
+            any_tie |= tie[s];
+            missing |= j < k && mine[s] <= kClosed;
+        }
+        if (__any_sync(0xffffffffu, any_tie && !idle)) {
+            // two words that agree: the logits decide, and the index as it did; more than two: again
+            if (w[0] == next) {
+#pragma unroll
+                for (int i = 0; i + 1 < kList; i++) w[i] = w[i + 1];
+                w[kList - 1] = 0;
+            }
+            const uint32_t second = row_largest<LANES>(w[0]);
+            const bool used_up = row_any<LANES>(w[0] == 0u);
+            const bool next_tie = ((next ^ second) & ~kIndex) == 0 || (kList < V && used_up);
+            const int next_id = int(kIndex - (next & kIndex));
+            float x[SLOTS];
+            uint32_t bits[SLOTS], flag[SLOTS], ids[SLOTS];
+            bool crowd = false;
+#pragma unroll
+            for (int s = 0; s < SLOTS; s++) {
+                x[s] = id[s] >= 0 && !idle ? to_f32(row[id[s] * a.col_stride]) : 0.0f;
+                bits[s] = __float_as_uint(x[s]);
+                flag[s] = tie[s];
+                ids[s] = uint32_t(id[s]);
+            }
+#pragma unroll
+            for (int s = 0; s < SLOTS; s++) {
+                const int j = s * LANES + g;
+                uint32_t other = following<LANES, SLOTS>(ids, s);
+                float y = __uint_as_float(following<LANES, SLOTS>(bits, s));
+                bool more = following<LANES, SLOTS>(flag, s);
+                const uint32_t before = preceding<LANES, SLOTS>(ids, s);
+                const float z = __uint_as_float(preceding<LANES, SLOTS>(bits, s));
+                const uint32_t flagged = preceding<LANES, SLOTS>(flag, s);
+                const bool behind = j > 0 && j < k && flagged;
+                if (j == k - 1) {
+                    other = uint32_t(next_id);
+                    y = tie[s] && !idle ? to_f32(row[next_id * a.col_stride]) : 0.0f;
+                    more = next_tie;
+                }
+                crowd |= tie[s] && more;
+                if (tie[s] && y > x[s])
+                    id[s] = int(other);
+                else if (behind && x[s] > z)
+                    id[s] = int(before);
+            }
+            again |= row_any<LANES>(crowd);
+        }
+        if (__any_sync(0xffffffffu, missing && !idle)) {   // closed, or finite with an exponent beyond the type
+            bool low = false;
+            if (!idle) {
+#pragma unroll 1
+                for (int e = g; e < a.experts; e += LANES) {
+                    const float x = to_f32(row[e * a.col_stride]);
+                    low |= x > -INFINITY && x < -2e38f;
+                }
+            }
+            again |= row_any<LANES>(low);
+        }
+    }
     if (__any_sync(0xffffffffu, again && !idle))
         choose_exactly<T, V, LANES, SLOTS>(a, row, again && !idle, id);
 }
@@ -764,8 +830,7 @@ int launch_route_kernel(const RouteArgs &a, int blocks, int threads, void *strea
         return (VEC ? warps * 2 * sizeof(Rows<T, L, V>) : 0) + size_t(4) * (warps * experts + experts + 1);
     };
     const size_t most = smem(RouteShape<V>::kWarps, L * V);
-    if (most > 48000)
-        if (const int rc = allow_shared<route_kernel<T, L, V, VEC, FEW>>(most, "route attribute")) return rc;
+    if (const int rc = allow<route_kernel<T, L, V, VEC, FEW>>(most, "route attribute")) return rc;
     return launch_kernel(route_kernel<T, L, V, VEC, FEW>, dim3(blocks), dim3(threads), smem(threads / 32, a.experts),
                          stream, a.joined ? blocks : 1, "route launch", a);
 }

@@ -38,14 +38,14 @@ int with_type(int32_t t, F fn) {
 // Lets KERNEL have up to `bytes` of dynamic shared memory on the current device: asked for once per
 // device, as the question costs as much as a launch.
 template <auto KERNEL>
-int allow_shared(size_t bytes, const char *what) {
+int allow(size_t bytes, const char *what) {
     static std::atomic<uint64_t> done{0};
     int device = 0;
     if (const int rc = cuda_status(cudaGetDevice(&device), what)) return rc;
     const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
     if (done.load(std::memory_order_relaxed) & bit) return NEST_OK;
-    const int rc = cuda_status(
-        cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)), what);
+    const int rc =
+        cuda_status(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)), what);
     if (!rc) done.fetch_or(bit, std::memory_order_relaxed);
     return rc;
 }

@@ -130,6 +130,24 @@ def test_mask_closed_and_ties(dtype, E, normalize):
     both(x, k, mask.cuda(), normalize, dtype=dtype)
 
 
+@pytest.mark.parametrize("E,k", [(6, 2), (32, 8), (33, 3), (64, 1), (64, 8), (100, 5), (200, 16), (256, 7), (256, 8),
+                                 (256, 12), (300, 8), (512, 16), (700, 6), (1024, 32)])
+def test_logits_that_differ_in_their_last_bits(E, k):
+    """32-bit logits a few units in the last place apart, alone, in pairs and in crowds, among the
+    chosen and at their end; large and small ones, and ones near 0 beside a large one."""
+    g = np.random.default_rng(E + k)
+    T = 500
+    x = g.normal(size=(T, E)).astype(np.float32) * np.exp(g.normal(size=(T, 1)) * 2).astype(np.float32)
+    for t in range(T):
+        for _ in range(g.integers(1, 6)):
+            crowd = g.permutation(E)[:g.integers(1, min(E, 2 + t % 9) + 1)]
+            v = np.sort(x[t])[-int(g.integers(1, min(E, k + 3) + 1))]
+            x[t, crowd] = (v.view(np.int32) + g.integers(-3, 4, len(crowd))).astype(np.int32).view(np.float32)
+        if t % 5 == 0:
+            x[t, g.integers(E)] = 200.0
+    both(torch.tensor(x).cuda(), k)
+
+
 def test_rows_that_leave_nothing():
     x = logits(40, 24, "fp32", 3).cuda()
     x[::3] = -float("inf")
