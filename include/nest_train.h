@@ -59,8 +59,11 @@ typedef struct {
     int32_t normalize;   /* 0 or 1 */
 } nest_route_desc;
 
-/* Device workspace of nest_route in bytes; its contents on entry are ignored.  0 when
- * the description breaks a limit. */
+/* Device workspace of nest_route in bytes, 0 when the description breaks a limit.  Its first
+ * NEST_TRAIN_TICKET bytes are zero on entry - the caller clears them once - and zero again
+ * when the call's work is done; the rest is scratch.  Calls that overlap need workspaces of
+ * their own. */
+#define NEST_TRAIN_TICKET 256
 size_t nest_route_workspace_size(const nest_route_desc *desc);
 
 /* DEVICE buffers: logits, mask (uint8 [T] or NULL), ids int32 [T][k], weights float
@@ -123,7 +126,8 @@ int nest_table_pack(const nest_tensor *tensors, int32_t n, const nest_table_info
  *   out[1] = min(1, max_norm / (out[0] + 1e-6)), NaN when out[0] is not finite
  * Squares are summed in 32 bits, with the rounding errors of the long sums added up beside
  * them; gradients beyond 1.8e19 overflow to an infinite norm.
- *   out   DEVICE float [2];  max_norm > 0 (may be infinite: out[1] = 1)              */
+ *   out   DEVICE float [2];  max_norm > 0 (may be infinite: out[1] = 1)
+ *   workspace   as nest_route's: its first NEST_TRAIN_TICKET bytes zero on entry and after */
 size_t nest_grad_norm_workspace_size(const nest_table_info *info);
 int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_type, float max_norm,
                    float *out, void *workspace, size_t ws_bytes, void *stream);

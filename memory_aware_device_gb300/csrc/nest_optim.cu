@@ -179,8 +179,10 @@ __device__ __forceinline__ float block_sum(float v, float *sh) {
 constexpr int kNormsPerSm = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kNormsPerSm) norm_kernel(Table table, int workers, float *part) {
+__global__ void __launch_bounds__(kThreads, kNormsPerSm) norm_kernel(Table table, int workers, uint32_t *ticket,
+                                                                     float *part, float max_norm, float *out) {
     __shared__ float sh[kWarps];
+    __shared__ bool last;
     __shared__ __align__(16) float room[kWarps][kBlock];
     pdl_wait();
     pdl_trigger();
@@ -215,19 +217,18 @@ __global__ void __launch_bounds__(kThreads, kNormsPerSm) norm_kernel(Table table
             left -= kWarps * kBlock;
         }
     });
-    const float s = block_sum(sum.value(), sh);
-    if (threadIdx.x == 0) part[blockIdx.x] = s;
-}
-
-__global__ void __launch_bounds__(kThreads) norm_finish_kernel(const float *part, int blocks, float max_norm,
-                                                               float *out) {
-    __shared__ float sh[kWarps];
-    pdl_wait();
-    pdl_trigger();
-    Sum sum;
+    const float own = block_sum(sum.value(), sh);
+    if (threadIdx.x == 0) {
+        part[blockIdx.x] = own;
+        last = last_ticket(ticket, gridDim.x);
+    }
+    __syncthreads();
+    if (!last) return;
+    // the last block adds what all have written
+    Sum total;
 #pragma unroll 8
-    for (int b = threadIdx.x; b < blocks; b += kThreads) sum.add(part[b]);
-    const float s = block_sum(sum.value(), sh);
+    for (int b = threadIdx.x; b < int(gridDim.x); b += kThreads) total.add(__ldcg(part + b));
+    const float s = block_sum(total.value(), sh);
     if (threadIdx.x == 0) {
         const float norm = sqrtf(s);
         out[0] = norm;
@@ -708,7 +709,7 @@ int nest_table_pack(const nest_tensor *t, int32_t n, const nest_table_info *info
 
 size_t nest_grad_norm_workspace_size(const nest_table_info *info) {
     if (check_info(info)) return 0;
-    return (size_t(info->workers + 1) * 4 + 255) & ~size_t(255);
+    return NEST_TRAIN_TICKET + ((size_t(info->workers + 1) * 4 + 255) & ~size_t(255));
 }
 
 int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_type, float max_norm, float *out,
@@ -719,14 +720,12 @@ int nest_grad_norm(const nest_table_info *info, const void *table, int32_t grad_
     if (!workspace || ws_bytes < nest_grad_norm_workspace_size(info) || !aligned_to(workspace, 256))
         return NEST_E_WORKSPACE;
     const int blocks = info->workers > 1 ? info->workers : 1;
-    float *part = static_cast<float *>(workspace);
-    const int rc = with_type(grad_type, [&](auto t) {
+    uint32_t *ticket = static_cast<uint32_t *>(workspace);
+    float *part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + NEST_TRAIN_TICKET);
+    return with_type(grad_type, [&](auto t) {
         return launch_kernel(norm_kernel<decltype(t)>, dim3(blocks), dim3(kThreads), 0, stream, 1, "norm launch",
-                             table_of(table, info), int(info->workers), part);
+                             table_of(table, info), int(info->workers), ticket, part, max_norm, out);
     });
-    if (rc) return rc;
-    return launch_kernel(norm_finish_kernel, dim3(1), dim3(kThreads), 0, stream, 1, "norm finish launch",
-                         static_cast<const float *>(part), blocks, max_norm, out);
 }
 
 int nest_adamw(const nest_table_info *info, const void *table, const nest_adamw_args *p, void *stream) {

@@ -1,67 +1,10 @@
-// Entry points of the routing operators: checks, launch shapes and the kernel that adds up
-// the blocks' sums (the others are in nest_route.cuh).
+// Entry points of the routing operators: checks and launch shapes (the kernels are in
+// nest_route.cuh).
 #include "nest_route.cuh"
 
 namespace nest {
 
 namespace {
-
-constexpr int kFinishWarps = 32;
-
-// The results from the blocks' rows of sums and counts, by the blocks of a cluster: each takes
-// groups of 32 experts.  A warp adds every 32nd row, then a warp adds an expert's 32 parts as
-// a tree.
-__global__ void __launch_bounds__(32 * kFinishWarps) route_finish_kernel(RouteArgs a, int rows) {
-    __shared__ float sh_p[kFinishWarps][33], sh_dot[kFinishWarps], sh_all[kCluster];
-    __shared__ int32_t sh_c[kFinishWarps][33];
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();   // every block has started; while the rows are still being written
-    pdl_wait();
-    pdl_trigger();
-    const int rank = int(blockIdx.x), ranks = int(gridDim.x);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int n = 0;
-    for (int r = lane; r < rows; r += 32) n += a.part_n[r];
-    float dot = 0.0f;
-    for (int first = 32 * rank; first < a.experts; first += 32 * ranks) {
-        float p = 0.0f;
-        int32_t c = 0;
-        if (first + lane < a.experts) {
-#pragma unroll 4
-            for (int r = warp; r < rows; r += kFinishWarps) {
-                p += a.part_p[int64_t(r) * a.experts + first + lane];
-                c += a.part_c[int64_t(r) * a.experts + first + lane];
-            }
-        }
-        sh_p[warp][lane] = p;
-        sh_c[warp][lane] = c;
-        __syncthreads();
-        p = warp_sum(sh_p[lane][warp]);
-        c = __reduce_add_sync(0xffffffffu, sh_c[lane][warp]);
-        if (first == 32 * rank) n = __reduce_add_sync(0xffffffffu, n);
-        p *= n ? 1.0f / float(n) : 0.0f;
-        if (lane == 0 && first + warp < a.experts) {
-            a.counts[first + warp] = c;
-            a.mean_prob[first + warp] = p;
-        }
-        dot = fmaf(p, float(c), dot);   // 0 past the last expert
-        __syncthreads();
-    }
-    if (lane == 0) sh_dot[warp] = dot;
-    __syncthreads();
-    if (warp == 0) {
-        dot = warp_sum(sh_dot[lane]);
-        if (lane == 0) *cluster.map_shared_rank(sh_all + rank, 0) = dot;
-    }
-    cluster.sync();
-    if (rank == 0 && warp == 0) {
-        dot = warp_sum(lane < ranks ? sh_all[lane < ranks ? lane : 0] : 0.0f);
-        if (lane == 0) {
-            *a.live = n;
-            *a.loss = loss_of(a, dot, n);
-        }
-    }
-}
 
 int check(const nest_route_desc *d) {
     if (!d || d->tokens < 0 || d->row_stride < 0 || d->col_stride < 0 || !valid_type(d->dtype) || d->experts < 1 ||
@@ -71,13 +14,9 @@ int check(const nest_route_desc *d) {
     return NEST_OK;
 }
 
-// The forward kernel's blocks and threads, and whether the blocks are one cluster: up to
-// kJoined passes of it over the rows (2048 x 64: two passes of a cluster 7.8 us, two launches 6.8).
-// A single block is no larger than its rows need.
-constexpr int kJoined = 1;
+// The forward kernel's blocks and threads; a block alone is no larger than its rows need.
 struct Grid {
     int blocks, threads;
-    bool joined;
 };
 Grid grid_of(const nest_route_desc *d) {
     Grid g;
@@ -86,8 +25,7 @@ Grid grid_of(const nest_route_desc *d) {
         constexpr int kPerWarp = 32 / decltype(lanes)::v, kRows = S::kWarps * kPerWarp;
         const int64_t b = (d->tokens + kRows - 1) / kRows, most = kSMs * S::kPerSm;
         const int64_t warps = (d->tokens + kPerWarp - 1) / kPerWarp;
-        g.joined = b <= kJoined * kCluster;
-        g.blocks = int(b < 1 ? 1 : g.joined && b > kCluster ? kCluster : b < most ? b : most);
+        g.blocks = int(b < 1 ? 1 : b < most ? b : most);
         g.threads = 32 * int(warps < 1 ? 1 : warps < S::kWarps ? warps : S::kWarps);
         return 0;
     });
@@ -117,8 +55,8 @@ extern "C" {
 
 size_t nest_route_workspace_size(const nest_route_desc *d) {
     if (check(d)) return 0;
-    const Grid g = grid_of(d);
-    return g.joined ? 256 : (size_t(g.blocks) * (8 * size_t(d->experts) + 4) + 255) & ~size_t(255);
+    const size_t blocks = size_t(grid_of(d).blocks);
+    return 256 + ((blocks > 1 ? blocks * (8 * size_t(row_pitch(d->experts)) + 4) + 255 : 0) & ~size_t(255));
 }
 
 int nest_route(const nest_route_desc *d, const void *logits, const uint8_t *mask, int32_t *ids, float *weights,
@@ -132,21 +70,16 @@ int nest_route(const nest_route_desc *d, const void *logits, const uint8_t *mask
     RouteArgs a = args_of(d, logits, mask);
     a.ids = ids;
     a.weights = weights;
-    a.part_p = static_cast<float *>(workspace);
-    a.part_c = reinterpret_cast<int32_t *>(a.part_p + int64_t(g.blocks) * d->experts);
-    a.part_n = a.part_c + int64_t(g.blocks) * d->experts;
+    a.ticket = static_cast<uint32_t *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + 256);
+    a.part_n = reinterpret_cast<int32_t *>(a.part + int64_t(g.blocks) * 2 * row_pitch(d->experts));
     a.counts = counts;
     a.live = live;
     a.mean_prob = mean_prob;
     a.loss = loss;
-    a.joined = g.joined;
-    const int rc = d->dtype == NEST_F32    ? launch_route_f32(a, g.blocks, g.threads, stream)
-                   : d->dtype == NEST_BF16 ? launch_route_bf16(a, g.blocks, g.threads, stream)
-                                           : launch_route_f16(a, g.blocks, g.threads, stream);
-    if (rc || g.joined) return rc;
-    const int groups = (d->experts + 31) / 32, cluster = groups < kCluster ? groups : kCluster;
-    return launch_kernel(route_finish_kernel, dim3(cluster), dim3(32 * kFinishWarps), 0, stream, cluster,
-                         "route finish launch", a, g.blocks);
+    return d->dtype == NEST_F32    ? launch_route_f32(a, g.blocks, g.threads, stream)
+           : d->dtype == NEST_BF16 ? launch_route_bf16(a, g.blocks, g.threads, stream)
+                                   : launch_route_f16(a, g.blocks, g.threads, stream);
 }
 
 int nest_route_backward(const nest_route_desc *d, const void *logits, const uint8_t *mask, const int32_t *ids,

@@ -16,14 +16,11 @@
 // the bits kept their logits are compared.  Where more than two agree, or a gate is NaN, the
 // row's choice is made again on whole logits.
 //
-// Sums.  Every lane adds up the gates of its experts in registers, the block adds its warps in
-// order, and the blocks' rows are added in a fixed order, so no result depends on the order in
-// which blocks run.  Few rows: the whole grid is one cluster, whose blocks read one
-// another's sums from shared memory, and the call is one launch.  Otherwise each block writes
-// its row of sums to the workspace and a second kernel adds them.
+// Sums.  Every lane adds up the gates of its experts in registers, and the block adds its warps
+// in order.  A block alone is done with that.  Otherwise each block writes its row of sums to
+// the workspace, and the last one to have done so adds the rows, in an order of their own: no
+// result depends on the order in which blocks run.
 #pragma once
-
-#include <cooperative_groups.h>
 
 #include <type_traits>
 
@@ -39,11 +36,11 @@ struct RouteArgs {
     // forward
     int32_t *ids;
     float *weights;
-    float *part_p;      // [blocks][experts], then counts likewise, then live rows; unused when joined
-    int32_t *part_c, *part_n;
+    uint32_t *ticket;   // 0 on entry
+    float *part;        // [blocks][2][pitch of the experts]: sums, then counts
+    int32_t *part_n;    // [blocks] live rows
     int32_t *counts, *live;
     float *mean_prob, *loss;
-    int joined;         // the grid is one cluster
     // backward
     const float *grad_weights, *grad_loss;
     void *grad;
@@ -56,9 +53,9 @@ struct RouteArgs {
 // number of warps up to that.
 template <int V>
 struct RouteShape {
-    static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 14 : 16;
+    static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 28 : 16;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kPerSm = V == 16 ? 2 : 1;
+    static constexpr int kPerSm = 1;
 };
 template <int V>
 struct BackwardShape {
@@ -69,9 +66,6 @@ struct BackwardShape {
 
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kCluster = 8;   // blocks of the joined form, and of the kernel that adds up the others
 constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ float exp2_of(float x) {   // results below 2^-126 are 0
@@ -464,10 +458,8 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
         choose_exactly<T, V, LANES, SLOTS>(a, row, again && !idle, id);
 }
 
-// From the sum over experts of count * mean.
-__device__ __forceinline__ float loss_of(const RouteArgs &a, float dot, int n) {
-    return n ? dot * float(a.experts) / (float(a.k) * float(n)) : 0.0f;
-}
+// Distance of the workspace's rows: whole pieces of 16 bytes.
+__host__ __device__ __forceinline__ int row_pitch(int experts) { return (experts + 3) & ~3; }
 
 template <typename T, int LANES, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
@@ -476,7 +468,8 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
     using R = Rows<T, LANES, V>;
     using L = typename std::conditional<VEC, typename R::L, Place<V, false, LANES>>::type;
     extern __shared__ __align__(16) unsigned char sh[];
-    __shared__ float sh_dot[32], sh_all[kCluster];
+    __shared__ float sh_dot[32];
+    __shared__ bool sh_last;
     const int threads = blockDim.x, warps = threads >> 5;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane & (LANES - 1);
     R *const rows = reinterpret_cast<R *>(sh) + 2 * warp;                         // [warps][2] (VEC)
@@ -606,56 +599,83 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
     live = __reduce_add_sync(0xffffffffu, g ? 0 : live);
     if (lane == 0 && live) atomicAdd(&sh_count[a.experts], live);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += threads) {
+    auto add_warps = [&](int e) {
         float s = 0.0f;
 #pragma unroll 4
         for (int w = 0; w < warps; w++) s += sh_sum[w * a.experts + e];
-        if (a.joined) {
-            sh_sum[e] = s;   // only this thread reads this column
-        } else {
-            a.part_p[int64_t(blockIdx.x) * a.experts + e] = s;
-            a.part_c[int64_t(blockIdx.x) * a.experts + e] = sh_count[e];
+        return s;
+    };
+    if (gridDim.x > 1) {
+        const int pitch = row_pitch(a.experts), blocks = int(gridDim.x);
+        float *own = a.part + int64_t(blockIdx.x) * 2 * pitch;
+        for (int e = threadIdx.x; e < a.experts; e += threads) {
+            own[e] = add_warps(e);
+            own[pitch + e] = __int_as_float(sh_count[e]);
         }
-    }
-    if (!a.joined) {
         if (threadIdx.x == 0) a.part_n[blockIdx.x] = sh_count[a.experts];
-        return;
+        __syncthreads();
+        if (threadIdx.x == 0) sh_last = last_ticket(a.ticket, blocks);
+        for (int e = threadIdx.x; e <= a.experts; e += threads) sh_count[e] = 0;
+        __syncthreads();
+        if (!sh_last) return;
+        // a warp adds every warps-th row, a lane four experts of each
+        if (warp == 0) {
+            int n = 0;
+            for (int r = lane; r < blocks; r += 32) n += __ldcg(a.part_n + r);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) sh_count[a.experts] = n;
+        }
+        constexpr int kAtOnce = (kSMs + RouteShape<V>::kWarps - 1) / RouteShape<V>::kWarps;   // a warp's rows
+        for (int e0 = 4 * lane; e0 < a.experts; e0 += 128) {
+            float4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+            int4 c = {0, 0, 0, 0};
+            for (int r0 = warp; r0 < blocks; r0 += warps * kAtOnce) {
+                float4 q[kAtOnce];
+                int4 d[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; i++) {
+                    q[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    d[i] = {0, 0, 0, 0};
+                    if (r0 + i * warps < blocks) {
+                        const float *row = a.part + int64_t(r0 + i * warps) * 2 * pitch + e0;
+                        q[i] = __ldcg(reinterpret_cast<const float4 *>(row));
+                        d[i] = __ldcg(reinterpret_cast<const int4 *>(row + pitch));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kAtOnce; i++) {
+                    p.x += q[i].x, p.y += q[i].y, p.z += q[i].z, p.w += q[i].w;
+                    c.x += d[i].x, c.y += d[i].y, c.z += d[i].z, c.w += d[i].w;
+                }
+            }
+            const float ps[4] = {p.x, p.y, p.z, p.w};
+            const int cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (e0 + i < a.experts) {
+                    sh_sum[warp * a.experts + e0 + i] = ps[i];
+                    atomicAdd(&sh_count[e0 + i], cs[i]);
+                }
+        }
+        __syncthreads();
     }
-    // the cluster's blocks share the experts, and the first one the loss
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = int(blockIdx.x), ranks = int(gridDim.x);
-    cluster.sync();
-    const int n = __reduce_add_sync(
-        0xffffffffu, lane < ranks ? *cluster.map_shared_rank(sh_count + a.experts, lane < ranks ? lane : 0) : 0);
+    const int n = sh_count[a.experts];
     const float over = n ? 1.0f / float(n) : 0.0f;
     float dot = 0.0f;
-    for (int e = rank * threads + int(threadIdx.x); e < a.experts; e += ranks * threads) {
-        float p = 0.0f;
-        int32_t c = 0;
-#pragma unroll
-        for (int r = 0; r < kCluster; r++)
-            if (r < ranks) {
-                p += cluster.map_shared_rank(sh_sum, r)[e];
-                c += cluster.map_shared_rank(sh_count, r)[e];
-            }
-        p *= over;
-        a.counts[e] = c;
-        a.mean_prob[e] = p;
-        dot = fmaf(p, float(c), dot);
+    for (int e = threadIdx.x; e < a.experts; e += threads) {
+        const float mean = add_warps(e) * over;
+        a.counts[e] = sh_count[e];
+        a.mean_prob[e] = mean;
+        dot = fmaf(mean, float(sh_count[e]), dot);
     }
     dot = warp_sum(dot);
     if (lane == 0) sh_dot[warp] = dot;
     __syncthreads();
     if (warp == 0) {
         dot = warp_sum(lane < warps ? sh_dot[lane] : 0.0f);
-        if (lane == 0) *cluster.map_shared_rank(sh_all + rank, 0) = dot;
-    }
-    cluster.sync();   // also keeps every block's sums until all have read them
-    if (rank == 0 && warp == 0) {
-        dot = warp_sum(lane < ranks ? sh_all[lane < ranks ? lane : 0] : 0.0f);
         if (lane == 0) {
             *a.live = n;
-            *a.loss = loss_of(a, dot, n);
+            *a.loss = n ? dot * float(a.experts) / (float(a.k) * float(n)) : 0.0f;
         }
     }
 }
@@ -832,7 +852,7 @@ int launch_route_kernel(const RouteArgs &a, int blocks, int threads, void *strea
     const size_t most = smem(RouteShape<V>::kWarps, L * V);
     if (const int rc = allow<route_kernel<T, L, V, VEC, FEW>>(most, "route attribute")) return rc;
     return launch_kernel(route_kernel<T, L, V, VEC, FEW>, dim3(blocks), dim3(threads), smem(threads / 32, a.experts),
-                         stream, a.joined ? blocks : 1, "route launch", a);
+                         stream, 1, "route launch", a);
 }
 
 template <typename T>

@@ -63,6 +63,18 @@ __device__ __forceinline__ void copies_mark() { asm volatile("cp.async.commit_gr
 template <int LATER>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
 
+// Takes a ticket, which is 0 again after `blocks` of them; whether it was the last.  By one thread
+// between two barriers of its block: what the block wrote before is seen by the block that
+// takes a later ticket.
+__device__ __forceinline__ bool last_ticket(uint32_t *ticket, uint32_t blocks) {
+    uint32_t before;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                 : "=r"(before)
+                 : "l"(ticket), "r"(blocks - 1)
+                 : "memory");
+    return before == blocks - 1;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

@@ -203,7 +203,7 @@ class _RouteCall:
         import torch
         self.key = (tokens, experts, k, device)
         size = _route_workspace(_described(tokens, experts, k, 0, 0, F32, 0))
-        self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)   # every call leaves its head zero
         self.tail = (self.workspace.data_ptr(), size)
 
 
@@ -390,7 +390,7 @@ class _Table:
         _check(lib().nest_table_pack(host.ctypes.data, n, C.byref(self.info), packed.ctypes.data), "nest_table_pack")
         self.table = torch.from_numpy(packed).to(self.device)
         ws = lib().nest_grad_norm_workspace_size(C.byref(self.info))
-        self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
+        self.workspace = torch.zeros(ws, dtype=torch.uint8, device=self.device)
         self.out = torch.empty(2, dtype=torch.float32, device=self.device)
         self.head = (C.byref(self.info), self.table.data_ptr())
         self.tail = (self.out.data_ptr(), self.workspace.data_ptr(), ws)
