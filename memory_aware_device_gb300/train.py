@@ -270,13 +270,18 @@ def route_backward(logits, routing: Routing, grad_weights=None, grad_loss=None, 
     T, E = logits.shape
     ids, weights, counts, tokens = routing[:4]
     k = ids.shape[-1]
-    if T:   # an empty batch reads none of them
-        _want(ids, "routing.ids", torch.int32, (T, k), dev)
-        _want(weights, "routing.weights", torch.float32, (T, k), dev)
-        _want(counts, "routing.counts", torch.int32, (E,), dev)
-        _want(tokens, "routing.tokens", torch.int32, (1,), dev)
+    i32, f32, one = torch.int32, torch.float32, (T, k)
+    if T and not (   # an empty batch reads none of them
+            ids.dtype is i32 and ids.shape == one and ids.is_contiguous() and ids.device == dev and
+            weights.dtype is f32 and weights.shape == one and weights.is_contiguous() and weights.device == dev and
+            counts.dtype is i32 and counts.shape == (E,) and counts.is_contiguous() and counts.device == dev and
+            tokens.dtype is i32 and tokens.shape == (1,) and tokens.device == dev):
+        _want(ids, "routing.ids", i32, one, dev)
+        _want(weights, "routing.weights", f32, one, dev)
+        _want(counts, "routing.counts", i32, (E,), dev)
+        _want(tokens, "routing.tokens", i32, (1,), dev)
     if grad_weights is not None:
-        _want(grad_weights, "grad_weights", torch.float32, (T, k), dev)
+        _want(grad_weights, "grad_weights", f32, one, dev)
     if grad_loss is not None:
         _want(grad_loss, "grad_loss", torch.float32, grad_loss.shape, dev)
         if grad_loss.numel() != 1:
