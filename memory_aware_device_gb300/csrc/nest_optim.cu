@@ -186,48 +186,60 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, kNormsPerSm) norm_kernel(Table table, int workers, uint32_t *ticket,
                                                                      float *part, float max_norm, float *out) {
     __shared__ float sh[kWarps];
-    __shared__ bool last;
-    __shared__ __align__(16) float room[kWarps][kBlock];
+    __shared__ bool done;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Sum sum;
     Segments(table, blockIdx.x, workers).each(table, warp, kWarps, [&](const Entry &e, int block, int count) {
-        const T *g = static_cast<const T *>(e.grad) + int64_t(block) * kBlock;
-        int64_t left = e.numel - int64_t(block) * kBlock;
-        const bool vector = wide(g);
+        // a tensor off alignment is read from the aligned address before it on, `off` elements early:
+        // its first block lacks them, and its last one has as many more
+        const T *g = static_cast<const T *>(e.grad);
+        const int off = int(reinterpret_cast<uintptr_t>(g) / sizeof(T) & 7), last = int((e.numel - 1) / kBlock);
+        const int64_t end = e.numel + off;
+        g -= off;
         while (count > 0) {
             float s = 0.0f;
-            if (vector && count > 1 && left >= (kWarps + 1) * kBlock) {   // two blocks' loads at once
+            const int64_t at = int64_t(block) * kBlock;
+            const bool begun = block > 0 || off == 0;
+            if (begun && count > 1 && block + kWarps < last) {   // two blocks' loads at once
                 alignas(16) T x[8], y[8];
-                load8(g + 8 * lane, x);
-                load8(g + kWarps * kBlock + 8 * lane, y);
+                load8(g + at + 8 * lane, x);
+                load8(g + at + kWarps * kBlock + 8 * lane, y);
 #pragma unroll
                 for (int i = 0; i < 8; i++) s = fmaf(to_f32(x[i]), to_f32(x[i]), s);
 #pragma unroll
                 for (int i = 0; i < 8; i++) s = fmaf(to_f32(y[i]), to_f32(y[i]), s);
                 count--;
-                g += kWarps * kBlock;
-                left -= kWarps * kBlock;
-            } else {
+                block += kWarps;
+            } else if (begun && block < last) {
                 alignas(16) T x[8];
-                load_block(g, int(left < kBlock ? left : kBlock), vector, lane, room[warp], x);
+                load8(g + at + 8 * lane, x);
 #pragma unroll
                 for (int i = 0; i < 8; i++) s = fmaf(to_f32(x[i]), to_f32(x[i]), s);
+            } else {
+                const int64_t stop = block < last ? at + kBlock : end;
+                T x[kBlock / 32 + 1];
+#pragma unroll
+                for (int c = 0; c <= kBlock / 32; c++) {
+                    const int64_t i = at + lane + 32 * c;
+                    x[c] = i >= off && i < stop ? g[i] : from_f32<T>(0.0f);
+                }
+#pragma unroll
+                for (int c = 0; c <= kBlock / 32; c++) s = fmaf(to_f32(x[c]), to_f32(x[c]), s);
             }
             sum.add(s);
             count--;
-            g += kWarps * kBlock;
-            left -= kWarps * kBlock;
+            block += kWarps;
         }
     });
     const float own = block_sum(sum.value(), sh);
     if (threadIdx.x == 0) {
         part[blockIdx.x] = own;
-        last = last_ticket(ticket, gridDim.x);
+        done = last_ticket(ticket, gridDim.x);
     }
     __syncthreads();
-    if (!last) return;
+    if (!done) return;
     // the last block adds what all have written
     Sum total;
 #pragma unroll 8
