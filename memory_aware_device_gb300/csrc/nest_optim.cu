@@ -407,23 +407,31 @@ __device__ __forceinline__ void store_own(uint8_t *p, int n, int lane, uint2 c) 
 constexpr int kAhead = 3;
 template <typename G>
 struct Stage {
-    alignas(16) G grad[kBlock];
+    static constexpr int kG = 16 / sizeof(G);
+    alignas(16) G grad[kBlock + kG];   // from an aligned address on
     alignas(16) float master[kBlock];
     alignas(16) uint8_t m[kBlock], v[kBlock];
 
-    __device__ __forceinline__ void copy(const G *g, const float *p, const uint8_t *cm, const uint8_t *cv, int lane) {
-        constexpr int kG = 16 / sizeof(G);   // neighbouring lanes copy neighbouring 16 bytes
+    // g: aligned; with off > 0 the block's gradients start `off` elements later.
+    __device__ __forceinline__ void copy(const G *g, int off, const float *p, const uint8_t *cm, const uint8_t *cv,
+                                         int lane) {
 #pragma unroll
-        for (int i = kG * lane; i < kBlock; i += 32 * kG) copy_ahead<16>(grad + i, g + i);
+        for (int i = kG * lane; i < kBlock; i += 32 * kG) copy_ahead<16>(grad + i, g + i);   // neighbours by neighbours
+        if (off && lane == 0) copy_ahead<16>(grad + kBlock, g + kBlock);
 #pragma unroll
         for (int i = 4 * lane; i < kBlock; i += 32 * 4) copy_ahead<16>(master + i, p + i);
         copy_ahead<8>(m + 8 * lane, cm + 8 * lane);
         copy_ahead<8>(v + 8 * lane, cv + 8 * lane);
     }
-    __device__ __forceinline__ void read(G (&g)[8], float (&p)[8], uint2 &cm, uint2 &cv, int lane) const {
+    __device__ __forceinline__ void read(int off, G (&g)[8], float (&p)[8], uint2 &cm, uint2 &cv, int lane) const {
+        if (off == 0) {
 #pragma unroll
-        for (int i = 0; i < int(sizeof(G) / 2); i++)
-            reinterpret_cast<uint4 *>(g)[i] = reinterpret_cast<const uint4 *>(grad + 8 * lane)[i];
+            for (int i = 0; i < int(sizeof(G) / 2); i++)
+                reinterpret_cast<uint4 *>(g)[i] = reinterpret_cast<const uint4 *>(grad + 8 * lane)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) g[i] = grad[off + 8 * lane + i];
+        }
 #pragma unroll
         for (int i = 0; i < 2; i++)
             reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(master + 8 * lane)[i];
@@ -482,19 +490,23 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
         const float lr = a.lr * e.lr_scale, decay = e.weight_decay;
         using S = Stage<G>;
         S *const stages = reinterpret_cast<S *>(sh) + warp * (kAhead + 1);
-        // the warp's whole blocks here, where their parts are aligned, are copied ahead
-        const int64_t past = e.numel / kBlock - b;
-        const int whole = EIGHT && wide_g && (!kOwnMaster || wide_w) && past > 0
+        // the warp's whole blocks here are copied ahead, gradients off alignment from the aligned
+        // address before them: not a tensor's first block then, and only as far as it goes; a single
+        // block has nothing to be ahead of
+        const int off = int(reinterpret_cast<uintptr_t>(grad) / sizeof(G) % S::kG);
+        const int64_t past = (off ? e.numel + off - S::kG : e.numel) / kBlock - b;
+        const int whole = EIGHT && count > 1 && (!kOwnMaster || wide_w) && past > 0
                               ? int(past < int64_t(count) * step ? (past + step - 1) / step : count) : 0;
+        const int from = off && b == 0;
         auto ahead = [&](int i) {
-            if (i < whole) {
+            if (i >= from && i < whole) {
                 const int64_t j = int64_t(b + i * step) * kBlock, own = e.first * kBlock + j;
                 const float *p;
                 if constexpr (kOwnMaster)
                     p = weight + j;
                 else
                     p = a.master + own;
-                stages[i % (kAhead + 1)].copy(grad + j, p, static_cast<const uint8_t *>(a.m) + own,
+                stages[i % (kAhead + 1)].copy(grad - off + j, off, p, static_cast<const uint8_t *>(a.m) + own,
                                               static_cast<const uint8_t *>(a.v) + own, lane);
             }
             copies_mark();
@@ -524,10 +536,10 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
                 sm = __shfl_sync(0xffffffffu, lane_sm, k % 32);
                 sv = __shfl_sync(0xffffffffu, lane_sv, k % 32);
             }
-            if (EIGHT && k < whole) {
+            if (EIGHT && k >= from && k < whole) {
                 copies_wait<kAhead>();
                 __syncwarp();
-                stages[k % (kAhead + 1)].read(g, p, cm, cv, lane);
+                stages[k % (kAhead + 1)].read(off, g, p, cm, cv, lane);
             } else {
                 load_block(grad + j0, n, wide_g, lane, room[warp], g);
                 if constexpr (EIGHT) {

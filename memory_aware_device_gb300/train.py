@@ -457,7 +457,7 @@ class AdamW:
         if weight_type != F32:
             self.master = torch.zeros(n, dtype=torch.float32, device=dev)
             for t, a in zip(weights, self.starts):
-                self.master[a:a + t.numel()] = t.reshape(-1)
+                self.master[a:a + t.numel()] = t.detach().reshape(-1)
         self._state = torch.zeros(STATE_DT.itemsize, dtype=torch.uint8, device=dev)
 
         def ptr(t):

@@ -76,6 +76,24 @@ def test_norm_of_nothing_and_of_too_much():
     assert abs(float(train.GradNorm([small]).run(1.0)[0]) - 1e-14) < 1e-19
 
 
+def test_norm_workspace_between_calls():
+    g = make([100003, 7, 65536], "bf16", 1)
+    norm = train.GradNorm(g)
+    want, ws = norm.run(1.0).clone(), norm._table.workspace
+    for _ in range(3):
+        ws[256:] = 255
+        assert torch.equal(norm.run(1.0), want) and (ws[:256] == 0).all()
+
+
+def test_parameters_that_require_gradients():
+    w = torch.nn.Parameter(torch.randn(70, 30, device="cuda").bfloat16())
+    w.grad = torch.randn_like(w)
+    opt = train.AdamW([w], [w.grad])
+    before = w.detach().clone()
+    opt.step(1e-2)
+    assert not opt.master.requires_grad and not torch.equal(w.detach(), before)
+
+
 # ---- step -------------------------------------------------------------------------
 
 def start(opt, seed, gscale):
@@ -206,6 +224,30 @@ def test_step_sizes(numels, bits):
         opt.set_step(9)
         start(opt, 4, 1e-4)
         check_step(opt, 10, 1e-3, decay, lr_scale=lr_scale)
+
+
+@pytest.mark.parametrize("bits,numels,wtype,gtype,shift", [
+    (8, [5000001, 300], "bf16", "bf16", 0), (8, [5000001, 300], "bf16", "bf16", 1), (8, [5000100], "fp32", "fp32", 3),
+    (8, [4000000, 1500003], "fp32", "fp16", 5), (8, [10100007, 5], "bf16", "bf16", 1),
+    (32, [20000123, 777], "bf16", "bf16", 0), (32, [5000001], "fp32", "bf16", 7)])
+def test_step_of_long_lists(bits, numels, wtype, gtype, shift):
+    """Lists in which a warp takes several blocks, and several thread blocks share a worker; with
+    gradients off alignment (and 32-bit weights with them)."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def room(n, kind, scale, off):
+        t = torch.zeros(n + off, dtype=TYPES[kind], device="cuda")
+        t[off:] = (torch.randn(n, generator=gen, device="cuda") * scale).to(TYPES[kind])
+        return t[off:]
+    w = [room(n, wtype, 0.05, shift % 3) for n in numels]
+    g = [room(n, gtype, 1e-3, shift) for n in numels]
+    decay = [0.1, 0.0][:len(numels)]
+    opt = train.AdamW(w, g, state_bits=bits, betas=(0.9, 0.95), weight_decay=decay, seed=77)
+    opt.set_step(20)
+    start(opt, 3, 1e-3)
+    check_step(opt, 21, 1e-3, decay, torch.tensor(0.7, device="cuda"))
+    want = np.sqrt(sum((f64(t) ** 2).sum() for t in g))
+    assert abs(float(opt.grad_norm()[0]) - want) <= 40 * U * want
 
 
 @pytest.mark.parametrize("bits", [32, 8])

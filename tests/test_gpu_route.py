@@ -287,6 +287,26 @@ def test_other_streams_and_graphs():
     assert torch.equal(grad, train.route_backward(x, want, want.weights))
 
 
+@pytest.mark.parametrize("T,E,k,dtype", [(12000, 256, 8, "fp32"), (10500, 300, 10, "bf16"), (40000, 64, 8, "fp16"),
+                                         (18000, 100, 4, "fp32"), (9000, 513, 12, "fp32")])
+def test_many_rows(T, E, k, dtype):
+    """Several passes of every block over the rows, and as many blocks as there are."""
+    both(logits(T, E, dtype, T + E).cuda(), k, dtype=dtype)
+
+
+def test_workspace_between_calls():
+    """The head of the workspace is zero after a call, whatever the rest of it held."""
+    x = logits(3000, 200, "fp32", 5).cuda()
+    want = train.route(x, 4)
+    out = train.Routing.empty(3000, 200, 4)
+    for _ in range(3):
+        out.call.workspace[256:] = 255
+        train.route(x, 4, out=out)
+        assert (out.call.workspace[:256] == 0).all()
+        for p, q in zip(want, out):
+            assert torch.equal(p, q)
+
+
 def test_refusals():
     x = logits(8, 16, "fp32", 1).cuda()
     r = train.route(x, 2)
