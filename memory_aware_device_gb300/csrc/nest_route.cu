@@ -1,10 +1,72 @@
-// Entry points of the routing operators: checks and launch shapes (the kernels are in
-// nest_route.cuh).
+// Entry points of the routing operators: checks, launch shapes and the kernel that adds up
+// long rows of sums (the others are in nest_route.cuh).
+#include <cooperative_groups.h>
+
 #include "nest_route.cuh"
 
 namespace nest {
 
 namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kAddWarps = 32, kCluster = 8;
+
+// The results from the blocks' rows of sums and counts, by the blocks of a cluster: each takes
+// groups of 32 experts.  A warp adds every 32nd row, then a warp adds an expert's 32 parts as
+// a tree.
+__global__ void __launch_bounds__(32 * kAddWarps) route_add_kernel(RouteArgs a, int rows) {
+    __shared__ float sh_p[kAddWarps][33], sh_dot[kAddWarps], sh_all[kCluster];
+    __shared__ int32_t sh_c[kAddWarps][33];
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();   // every block has started; while the rows are still being written
+    pdl_wait();
+    pdl_trigger();
+    const int rank = int(blockIdx.x), ranks = int(gridDim.x), pitch = row_pitch(a.experts);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n = 0;
+    for (int r = lane; r < rows; r += 32) n += a.part_n[r];
+    n = __reduce_add_sync(0xffffffffu, n);
+    const float over = n ? 1.0f / float(n) : 0.0f;
+    float dot = 0.0f;
+    for (int first = 32 * rank; first < a.experts; first += 32 * ranks) {
+        float p = 0.0f;
+        int32_t c = 0;
+        if (first + lane < a.experts) {
+#pragma unroll 4
+            for (int r = warp; r < rows; r += kAddWarps) {
+                const float *row = a.part + int64_t(r) * 2 * pitch + first + lane;
+                p += row[0];
+                c += __float_as_int(row[pitch]);
+            }
+        }
+        sh_p[warp][lane] = p;
+        sh_c[warp][lane] = c;
+        __syncthreads();
+        p = warp_sum(sh_p[lane][warp]) * over;
+        c = __reduce_add_sync(0xffffffffu, sh_c[lane][warp]);
+        if (lane == 0 && first + warp < a.experts) {
+            a.counts[first + warp] = c;
+            a.mean_prob[first + warp] = p;
+        }
+        dot = fmaf(p, float(c), dot);   // 0 past the last expert
+        __syncthreads();
+    }
+    if (lane == 0) sh_dot[warp] = dot;
+    __syncthreads();
+    if (warp == 0) {
+        dot = warp_sum(sh_dot[lane]);
+        if (lane == 0) *cluster.map_shared_rank(sh_all + rank, 0) = dot;
+    }
+    cluster.sync();
+    if (rank == 0 && warp == 0) {
+        dot = warp_sum(lane < ranks ? sh_all[lane < ranks ? lane : 0] : 0.0f);
+        if (lane == 0) {
+            *a.live = n;
+            *a.loss = loss_of(a, dot, n);
+        }
+    }
+}
 
 int check(const nest_route_desc *d) {
     if (!d || d->tokens < 0 || d->row_stride < 0 || d->col_stride < 0 || !valid_type(d->dtype) || d->experts < 1 ||
@@ -17,6 +79,7 @@ int check(const nest_route_desc *d) {
 // The forward kernel's blocks and threads; a block alone is no larger than its rows need.
 struct Grid {
     int blocks, threads;
+    bool apart;   // a second kernel adds the blocks' rows
 };
 Grid grid_of(const nest_route_desc *d) {
     Grid g;
@@ -27,6 +90,7 @@ Grid grid_of(const nest_route_desc *d) {
         const int64_t warps = (d->tokens + kPerWarp - 1) / kPerWarp;
         g.blocks = int(b < 1 ? 1 : b < most ? b : most);
         g.threads = 32 * int(warps < 1 ? 1 : warps < S::kWarps ? warps : S::kWarps);
+        g.apart = g.blocks > 1 && decltype(values)::v >= kApart;
         return 0;
     });
     return g;
@@ -77,9 +141,13 @@ int nest_route(const nest_route_desc *d, const void *logits, const uint8_t *mask
     a.live = live;
     a.mean_prob = mean_prob;
     a.loss = loss;
-    return d->dtype == NEST_F32    ? launch_route_f32(a, g.blocks, g.threads, stream)
-           : d->dtype == NEST_BF16 ? launch_route_bf16(a, g.blocks, g.threads, stream)
-                                   : launch_route_f16(a, g.blocks, g.threads, stream);
+    const int rc = d->dtype == NEST_F32    ? launch_route_f32(a, g.blocks, g.threads, stream)
+                   : d->dtype == NEST_BF16 ? launch_route_bf16(a, g.blocks, g.threads, stream)
+                                           : launch_route_f16(a, g.blocks, g.threads, stream);
+    if (rc || !g.apart) return rc;
+    const int groups = (d->experts + 31) / 32, cluster = groups < kCluster ? groups : kCluster;
+    return launch_kernel(route_add_kernel, dim3(cluster), dim3(32 * kAddWarps), 0, stream, cluster, "route sums launch",
+                         a, g.blocks);
 }
 
 int nest_route_backward(const nest_route_desc *d, const void *logits, const uint8_t *mask, const int32_t *ids,

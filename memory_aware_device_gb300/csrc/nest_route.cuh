@@ -20,8 +20,10 @@
 //
 // Sums.  Every lane adds up the gates of its experts in registers, and the block adds its warps
 // in order.  A block alone is done with that.  Otherwise each block writes its row of sums to
-// the workspace, and the last one to have done so adds the rows, in an order of their own: no
-// result depends on the order in which blocks run.
+// the workspace, and the last one to have done so adds the rows; rows of more than 128 experts
+// are more than one block should read, and a second kernel adds them (32768 x 1024: 47 us against
+// 63; 30011 x 72: 12.3 us in one launch against 13.9 in two).  Either way they are added in an
+// order of their own: no result depends on the order in which blocks run.
 #pragma once
 
 #include <type_traits>
@@ -460,12 +462,21 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
         choose_exactly<T, V, LANES, SLOTS>(a, row, again && !idle, id);
 }
 
+// From the sum over experts of count * mean.
+__device__ __forceinline__ float loss_of(const RouteArgs &a, float dot, int n) {
+    return n ? dot * float(a.experts) / (float(a.k) * float(n)) : 0.0f;
+}
+
+// Values per lane from which a second kernel adds the blocks' rows (over 128 experts).
+constexpr int kApart = 32;
+
 // Distance of the workspace's rows: whole pieces of 16 bytes.
 __host__ __device__ __forceinline__ int row_pitch(int experts) { return (experts + 3) & ~3; }
 
-// Measured: 262144 x 256 in 32 bits, k = 8: 91 us, 3.1 TB/s of the 285 MB that it must move, whose
+// Measured: 262144 x 256 in 32 bits, k = 8: 85 us, 3.4 TB/s of the 285 MB that it must move, whose
 // floor is 42 us.  250 instructions a row, for sorting above all, bound it: the integer pipe is
-// busy 57 % of the time, memory 38 %.  FEW (k up to 8) is worth it: 92 us against 137.
+// busy 57 % of the time, memory 38 %.  FEW (k up to 8) is worth it: 92 us against 137 with the
+// longer lists.
 template <typename T, int LANES, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
     constexpr int kRows = 32 / LANES, kSlots = FEW ? 1 : 32 / LANES;
@@ -618,6 +629,7 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
             own[pitch + e] = __int_as_float(sh_count[e]);
         }
         if (threadIdx.x == 0) a.part_n[blockIdx.x] = sh_count[a.experts];
+        if constexpr (V >= kApart) return;
         __syncthreads();
         if (threadIdx.x == 0) sh_last = last_ticket(a.ticket, blocks);
         for (int e = threadIdx.x; e <= a.experts; e += threads) sh_count[e] = 0;
@@ -680,7 +692,7 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
         dot = warp_sum(lane < warps ? sh_dot[lane] : 0.0f);
         if (lane == 0) {
             *a.live = n;
-            *a.loss = n ? dot * float(a.experts) / (float(a.k) * float(n)) : 0.0f;
+            *a.loss = loss_of(a, dot, n);
         }
     }
 }
