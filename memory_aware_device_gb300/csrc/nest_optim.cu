@@ -177,7 +177,7 @@ __device__ __forceinline__ float block_sum(float v, float *sh) {
 }
 
 // The norm.  Every gradient is read once, two blocks of a warp under way at a time; memory bounds it.
-// Measured: 201M values in 16 bits 64.5 us, 6.2 TB/s (a flat loop over one buffer 59 us); the
+// Measured: 201M values in 16 bits 63 us, 6.4 TB/s (a flat loop over one buffer 59 us); the
 // smallest lists 3.5 us.  All thread blocks of a long list are resident at once: with six times
 // as many 70 us.
 constexpr int kNormsPerSm = 8;
@@ -446,7 +446,7 @@ constexpr uint32_t kRareM = (uint32_t(14 + 127) << 23) | 0x600000u, kRareV = (ui
 
 // The step.  Memory bounds it: 28 bytes a weight with 16-bit weights and gradients and moments in
 // 32 bits, 16 with moments in 8 bits.  Measured over 201M weights, 32 bits: 818 us, 6.9 TB/s
-// (842 with one thread block per worker); 8 bits: 500 us, 6.4 TB/s (628 with one, and 543 with
+// (842 with one thread block per worker); 8 bits: 496 us, 6.5 TB/s (628 with one, and 543 with
 // 8 instead of 4; 575 with copies of 16 bytes at a stride of 32).  Three thread blocks to an SM,
 // up to 80 registers: with four the 32-bit step takes 868 us against 853.
 template <typename W, typename G, bool EIGHT>
