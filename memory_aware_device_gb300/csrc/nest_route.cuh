@@ -273,11 +273,17 @@ __device__ __forceinline__ void sort_down(uint32_t (&w)[V]) {
 // order that log2(N) rounds of exchanges sort.
 template <int N, int V>
 __device__ __forceinline__ void keep_largest(uint32_t (&w)[V]) {
-    static_assert(V % N == 0 && V / N <= 4, "whole runs, at most four");
+    static_assert(V % N == 0 && V / N <= 8, "whole runs, at most eight");
     sort_down<0, N>(w);
     if constexpr (V / N >= 2) sort_down<N, N>(w);
     if constexpr (V / N >= 3) sort_down<2 * N, N>(w);
     if constexpr (V / N >= 4) sort_down<3 * N, N>(w);
+    if constexpr (V / N == 8) {
+        sort_down<4 * N, N>(w);
+        sort_down<5 * N, N>(w);
+        sort_down<6 * N, N>(w);
+        sort_down<7 * N, N>(w);
+    }
 #pragma unroll
     for (int step = N; step < V; step *= 2)
 #pragma unroll
@@ -346,30 +352,31 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const T *row,
 }
 
 // Lane g of a row's LANES gets in slot s the row's chosen expert number s LANES + g, or -1.  w:
-// the words of the lane's values.  FEW: k is at most 8, and one slot is enough; lists of 8 words
-// serve it, and lists of 16 any k, but for rows that draw on one lane more often than that.  again: the row's
-// words cannot be used; idle: nothing is chosen in the row.
-template <typename T, int V, int LANES, bool FEW, int SLOTS>
+// the words of the lane's values.  MOST: how many of them are kept, 4, 8 or 16; k is at most that
+// for 4 and 8, where one slot is enough, and any for 16.  Rows that draw on one lane more often, or
+// as often where a tie has to be looked for, are chosen again.  again: the row's words cannot be
+// used; idle: nothing is chosen in the row.
+template <typename T, int V, int LANES, int MOST, int SLOTS>
 __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_t (&w)[V], bool again, bool idle,
                                        int (&id)[SLOTS]) {
     constexpr uint32_t kIndex = LANES * V - 1;   // the bits that hold the index
     constexpr bool kWhole = sizeof(T) == 2;      // no bit of a logit is lost
-    constexpr int kMost = FEW ? 8 : 16, kList = V < kMost ? V : kMost;   // words kept of a lane's
+    constexpr int kList = V < MOST ? V : MOST;   // words kept of a lane's
     const int k = a.k, g = threadIdx.x & (LANES - 1);
     uint32_t mine[SLOTS];
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) mine[s] = 0;
     keep_largest<kList>(w);
-    if constexpr (FEW) {
+    if constexpr (MOST <= 8) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
+        for (int j = 0; j < MOST; j++) {
             if (j >= k) break;
             const uint32_t last = row_largest<LANES>(w[0]);
             if (g == j) mine[0] = last;
             if (w[0] == last) {   // of a list only what the rounds left can reach is moved
 #pragma unroll
                 for (int i = 0; i < kList; i++)
-                    if (i < 9 - j) w[i] = i + 1 < kList ? w[i + 1 < kList ? i + 1 : i] : 0u;
+                    if (i < MOST + 1 - j) w[i] = i + 1 < kList ? w[i + 1 < kList ? i + 1 : i] : 0u;
             }
         }
     } else {
@@ -386,8 +393,8 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
                 }
             }
     }
-    // a lane whose words are used up may have had more (8 of them and k = 8: no more was wanted)
-    if (kList < V && !(FEW && kWhole)) again |= row_any<LANES>(w[0] == 0u);
+    // a lane whose words are used up may have had more (MOST of them and k = MOST: no more was wanted)
+    if (kList < V && !(MOST <= 8 && kWhole)) again |= row_any<LANES>(w[0] == 0u);
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) id[s] = mine[s] > kClosed ? int(kIndex - (mine[s] & kIndex)) : -1;
     if (!kWhole) {
@@ -475,11 +482,11 @@ __host__ __device__ __forceinline__ int row_pitch(int experts) { return (experts
 
 // Measured: 262144 x 256 in 32 bits, k = 8: 85 us, 3.4 TB/s of the 285 MB that it must move, whose
 // floor is 42 us.  250 instructions a row, for sorting above all, bound it: the integer pipe is
-// busy 57 % of the time, memory 38 %.  FEW (k up to 8) is worth it: 92 us against 137 with the
-// longer lists.
-template <typename T, int LANES, int V, bool VEC, bool FEW>
+// busy 57 % of the time, memory 38 %.  MOST, the words that a lane keeps: with 8 this takes 92 us
+// against 137 with 16; k = 2 with 4 takes 72 us against 81 with 8 (bfloat16 76 against 87).
+template <typename T, int LANES, int V, bool VEC, int MOST>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
-    constexpr int kRows = 32 / LANES, kSlots = FEW ? 1 : 32 / LANES;
+    constexpr int kRows = 32 / LANES, kSlots = MOST <= 8 ? 1 : 32 / LANES;
     constexpr uint32_t kIndex = LANES * V - 1;
     using R = Rows<T, LANES, V>;
     using L = typename std::conditional<VEC, typename R::L, Place<V, false, LANES>>::type;
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
         for (int i = 0; i < V; i++) acc[i] = fmaf(x[i], inv, acc[i]);
 
         int id[kSlots];
-        choose<T, V, LANES, FEW, kSlots>(a, row, w, isnan(sum) || (sizeof(T) == 4 && ex.far), !is_live, id);
+        choose<T, V, LANES, MOST, kSlots>(a, row, w, isnan(sum) || (sizeof(T) == 4 && ex.far), !is_live, id);
         float gate[kSlots], total = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSlots; s++) {
@@ -863,14 +870,14 @@ bool vector_rows(const RouteArgs &a) {
 }  // namespace
 
 // Launches of one element type (each in its own translation unit).
-template <typename T, int L, int V, bool VEC, bool FEW>
+template <typename T, int L, int V, bool VEC, int MOST>
 int launch_route_kernel(const RouteArgs &a, int blocks, int threads, void *stream) {
     const auto smem = [](int warps, int experts) {
         return (VEC ? warps * 2 * sizeof(Rows<T, L, V>) : 0) + size_t(4) * (warps * experts + experts + 1);
     };
     const size_t most = smem(RouteShape<V>::kWarps, L * V);
-    if (const int rc = allow<route_kernel<T, L, V, VEC, FEW>>(most, "route attribute")) return rc;
-    return launch_kernel(route_kernel<T, L, V, VEC, FEW>, dim3(blocks), dim3(threads), smem(threads / 32, a.experts),
+    if (const int rc = allow<route_kernel<T, L, V, VEC, MOST>>(most, "route attribute")) return rc;
+    return launch_kernel(route_kernel<T, L, V, VEC, MOST>, dim3(blocks), dim3(threads), smem(threads / 32, a.experts),
                          stream, 1, "route launch", a);
 }
 
@@ -878,11 +885,16 @@ template <typename T>
 int launch_route_type(const RouteArgs &a, int blocks, int threads, void *stream) {
     return with_row(a.experts, [&](auto lanes, auto values) {
         constexpr int L = decltype(lanes)::v, V = decltype(values)::v;
-        const bool vec = vector_rows<T, V, Rows<T, L, V>::L::C>(a), few = a.k <= 8;
-        return vec ? few ? launch_route_kernel<T, L, V, true, true>(a, blocks, threads, stream)
-                         : launch_route_kernel<T, L, V, true, false>(a, blocks, threads, stream)
-               : few ? launch_route_kernel<T, L, V, false, true>(a, blocks, threads, stream)
-                     : launch_route_kernel<T, L, V, false, false>(a, blocks, threads, stream);
+        const bool vec = vector_rows<T, V, Rows<T, L, V>::L::C>(a);
+        const auto with = [&](auto most) {
+            constexpr int M = decltype(most)::v;
+            return vec ? launch_route_kernel<T, L, V, true, M>(a, blocks, threads, stream)
+                       : launch_route_kernel<T, L, V, false, M>(a, blocks, threads, stream);
+        };
+        // a list of 4 serves 4 experts where ties need no word more, else 3
+        if constexpr (V > 4)
+            if (a.k < (sizeof(T) == 2 ? 5 : 4)) return with(Number<4>{});
+        return a.k <= 8 ? with(Number<8>{}) : with(Number<16>{});
     });
 }
 

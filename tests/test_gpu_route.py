@@ -148,6 +148,22 @@ def test_logits_that_differ_in_their_last_bits(E, k):
     both(torch.tensor(x).cuda(), k)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("E", [40, 64, 100, 128, 256, 300, 1000])
+def test_chosen_experts_side_by_side(E, dtype):
+    """The largest logits of a row are neighbours, or 4, 8, 16, 32 or 64 apart, in rising, falling and
+    equal order: however a row is laid out, some rows draw all their experts from one part of it."""
+    steps, T = [s for s in (1, 4, 8, 16, 32, 64) if s < E], 90
+    x = logits(T, E, dtype, E, spread=1.0)
+    for t in range(T):
+        step = steps[t % len(steps)]
+        at = (t + step * torch.arange(12)) % E
+        x[t, at] = {0: 8.0 - 0.25 * torch.arange(12.0), 1: 5.0 + 0.25 * torch.arange(12.0),
+                    2: torch.full((12,), 6.0)}[t // len(steps) % 3].to(x.dtype)
+    for k in (1, 2, 3, 4, 5, 8, 9):
+        both(x.cuda(), k, dtype=dtype)
+
+
 def test_rows_that_leave_nothing():
     x = logits(40, 24, "fp32", 3).cuda()
     x[::3] = -float("inf")
