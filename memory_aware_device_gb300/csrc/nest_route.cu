@@ -83,7 +83,7 @@ struct Grid {
 };
 Grid grid_of(const nest_route_desc *d) {
     Grid g;
-    with_row(d->experts, [&](auto lanes, auto values) {
+    with_row(d->experts, d->k, [&](auto lanes, auto values) {
         using S = RouteShape<decltype(values)::v>;
         constexpr int kPerWarp = 32 / decltype(lanes)::v, kRows = S::kWarps * kPerWarp;
         const int64_t b = (d->tokens + kRows - 1) / kRows, most = kSMs * S::kPerSm;

@@ -11,8 +11,8 @@
 // Choice of the k largest.  A logit becomes a 32-bit word whose order is that of the logits,
 // with its lowest bits replaced by the complement of the expert's index: all words of a row
 // differ, and among logits that agree in the bits kept the lower index is the larger word.
-// Each lane sorts its words once and keeps the largest; then k rounds take the maximum over the row's lanes, and the lane that had it moves its list up.  16-bit logits
-// lose nothing to the index.  With 32-bit logits up to 10 bits are lost, and the word comes
+// Each lane sorts its words once and keeps the largest; then k rounds take the maximum over the
+// row's lanes, and the lane that had it moves its list up.  16-bit logits lose nothing to the index.  With 32-bit logits up to 10 bits are lost, and the word comes
 // from the exponent (x - top) log2(e), negative for every x, which may round two logits to
 // one: one more round gives the largest word left, and where two of these neighbours agree in
 // the bits kept their logits are compared.  Where more than two agree, or a gate is NaN, the
@@ -57,7 +57,7 @@ struct RouteArgs {
 // number of warps up to that.
 template <int V>
 struct RouteShape {
-    static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 28 : 16;
+    static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 28 : V <= 24 ? 20 : 16;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kPerSm = 1;
 };
@@ -278,12 +278,10 @@ __device__ __forceinline__ void keep_largest(uint32_t (&w)[V]) {
     if constexpr (V / N >= 2) sort_down<N, N>(w);
     if constexpr (V / N >= 3) sort_down<2 * N, N>(w);
     if constexpr (V / N >= 4) sort_down<3 * N, N>(w);
-    if constexpr (V / N == 8) {
-        sort_down<4 * N, N>(w);
-        sort_down<5 * N, N>(w);
-        sort_down<6 * N, N>(w);
-        sort_down<7 * N, N>(w);
-    }
+    if constexpr (V / N >= 5) sort_down<4 * N, N>(w);
+    if constexpr (V / N >= 6) sort_down<5 * N, N>(w);
+    if constexpr (V / N >= 7) sort_down<6 * N, N>(w);
+    if constexpr (V / N >= 8) sort_down<7 * N, N>(w);
 #pragma unroll
     for (int step = N; step < V; step *= 2)
 #pragma unroll
@@ -351,6 +349,13 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const T *row,
     }
 }
 
+// The bits of a word that hold the index, for rows of up to n values.
+__host__ __device__ constexpr uint32_t index_bits(int n) {
+    uint32_t b = 1;
+    while (b < uint32_t(n)) b *= 2;
+    return b - 1;
+}
+
 // Lane g of a row's LANES gets in slot s the row's chosen expert number s LANES + g, or -1.  w:
 // the words of the lane's values.  MOST: how many of them are kept, 4, 8 or 16; k is at most that
 // for 4 and 8, where one slot is enough, and any for 16.  Rows that draw on one lane more often, or
@@ -359,7 +364,7 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const T *row,
 template <typename T, int V, int LANES, int MOST, int SLOTS>
 __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_t (&w)[V], bool again, bool idle,
                                        int (&id)[SLOTS]) {
-    constexpr uint32_t kIndex = LANES * V - 1;   // the bits that hold the index
+    constexpr uint32_t kIndex = index_bits(LANES * V);
     constexpr bool kWhole = sizeof(T) == 2;      // no bit of a logit is lost
     constexpr int kList = V < MOST ? V : MOST;   // words kept of a lane's
     const int k = a.k, g = threadIdx.x & (LANES - 1);
@@ -475,7 +480,7 @@ __device__ __forceinline__ float loss_of(const RouteArgs &a, float dot, int n) {
 }
 
 // Values per lane from which a second kernel adds the blocks' rows (over 128 experts).
-constexpr int kApart = 32;
+constexpr int kApart = 24;
 
 // Distance of the workspace's rows: whole pieces of 16 bytes.
 __host__ __device__ __forceinline__ int row_pitch(int experts) { return (experts + 3) & ~3; }
@@ -487,7 +492,7 @@ __host__ __device__ __forceinline__ int row_pitch(int experts) { return (experts
 template <typename T, int LANES, int V, bool VEC, int MOST>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
     constexpr int kRows = 32 / LANES, kSlots = MOST <= 8 ? 1 : 32 / LANES;
-    constexpr uint32_t kIndex = LANES * V - 1;
+    constexpr uint32_t kIndex = index_bits(LANES * V);
     using R = Rows<T, LANES, V>;
     using L = typename std::conditional<VEC, typename R::L, Place<V, false, LANES>>::type;
     extern __shared__ __align__(16) unsigned char sh[];
@@ -838,12 +843,14 @@ __global__ void __launch_bounds__(BackwardShape<V>::kThreads, BackwardShape<V>::
 template <int N> struct Number { static constexpr int v = N; };
 
 // fn(lanes, values): how a row of `experts` is held.  Eight lanes hold up to 32 values each;
-// longer rows take more lanes.
+// longer rows take more lanes.  24 values, whole runs of 4 and 8 words but not of 16, are for k up
+// to 8 (262144 x 160 in bfloat16, k = 6: 76 us against 93 with 32 values).
 template <typename F>
-int with_row(int experts, F fn) {
+int with_row(int experts, int k, F fn) {
     if (experts <= 32) return fn(Number<8>{}, Number<4>{});
     if (experts <= 64) return fn(Number<8>{}, Number<8>{});
     if (experts <= 128) return fn(Number<8>{}, Number<16>{});
+    if (experts <= 192 && k <= 8) return fn(Number<8>{}, Number<24>{});
     if (experts <= 256) return fn(Number<8>{}, Number<32>{});
     if (experts <= 512) return fn(Number<16>{}, Number<32>{});
     return fn(Number<32>{}, Number<32>{});
@@ -883,7 +890,7 @@ int launch_route_kernel(const RouteArgs &a, int blocks, int threads, void *strea
 
 template <typename T>
 int launch_route_type(const RouteArgs &a, int blocks, int threads, void *stream) {
-    return with_row(a.experts, [&](auto lanes, auto values) {
+    return with_row(a.experts, a.k, [&](auto lanes, auto values) {
         constexpr int L = decltype(lanes)::v, V = decltype(values)::v;
         const bool vec = vector_rows<T, V, Rows<T, L, V>::L::C>(a);
         const auto with = [&](auto most) {
@@ -894,7 +901,10 @@ int launch_route_type(const RouteArgs &a, int blocks, int threads, void *stream)
         // a list of 4 serves 4 experts where ties need no word more, else 3
         if constexpr (V > 4)
             if (a.k < (sizeof(T) == 2 ? 5 : 4)) return with(Number<4>{});
-        return a.k <= 8 ? with(Number<8>{}) : with(Number<16>{});
+        if constexpr (V == 24)
+            return with(Number<8>{});
+        else
+            return a.k <= 8 ? with(Number<8>{}) : with(Number<16>{});
     });
 }
 

@@ -131,7 +131,8 @@ def test_mask_closed_and_ties(dtype, E, normalize):
 
 
 @pytest.mark.parametrize("E,k", [(6, 2), (32, 8), (33, 3), (64, 1), (64, 8), (100, 5), (200, 16), (256, 7), (256, 8),
-                                 (256, 12), (300, 8), (512, 16), (700, 6), (1024, 32)])
+                                 (256, 12), (300, 8), (512, 16), (700, 6), (1024, 32),
+                                 (129, 3), (160, 6), (190, 8), (192, 8), (192, 4)])
 def test_logits_that_differ_in_their_last_bits(E, k):
     """32-bit logits a few units in the last place apart, alone, in pairs and in crowds, among the
     chosen and at their end; large and small ones, and ones near 0 beside a large one."""
@@ -149,7 +150,7 @@ def test_logits_that_differ_in_their_last_bits(E, k):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-@pytest.mark.parametrize("E", [40, 64, 100, 128, 256, 300, 1000])
+@pytest.mark.parametrize("E", [40, 64, 100, 128, 160, 190, 256, 300, 1000])
 def test_chosen_experts_side_by_side(E, dtype):
     """The largest logits of a row are neighbours, or 4, 8, 16, 32 or 64 apart, in rising, falling and
     equal order: however a row is laid out, some rows draw all their experts from one part of it."""
@@ -304,7 +305,7 @@ def test_other_streams_and_graphs():
 
 
 @pytest.mark.parametrize("T,E,k,dtype", [(12000, 256, 8, "fp32"), (10500, 300, 10, "bf16"), (40000, 64, 8, "fp16"),
-                                         (18000, 100, 4, "fp32"), (9000, 513, 12, "fp32")])
+                                         (30011, 160, 6, "bf16"), (14000, 190, 8, "fp32"), (18000, 100, 4, "fp32"), (9000, 513, 12, "fp32")])
 def test_many_rows(T, E, k, dtype):
     """Several passes of every block over the rows, and as many blocks as there are."""
     both(logits(T, E, dtype, T + E).cuda(), k, dtype=dtype)
