@@ -12,11 +12,12 @@
 // with its lowest bits replaced by the complement of the expert's index: all words of a row
 // differ, and among logits that agree in the bits kept the lower index is the larger word.
 // Each lane sorts its words once and keeps the largest; then k rounds take the maximum over the
-// row's lanes, and the lane that had it moves its list up.  16-bit logits lose nothing to the index.  With 32-bit logits up to 10 bits are lost, and the word comes
-// from the exponent (x - top) log2(e), negative for every x, which may round two logits to
-// one: one more round gives the largest word left, and where two of these neighbours agree in
-// the bits kept their logits are compared.  Where more than two agree, or a gate is NaN, the
-// row's choice is made again on whole logits.
+// row's lanes, and the lane that had it moves its list up.  16-bit logits lose nothing to the
+// index.  With 32-bit logits up to 10 bits are lost, and the word comes from the exponent
+// (x - top) log2(e), negative for every x, which may round two logits to one: one more round
+// gives the largest word left, and where two of these neighbours agree in the bits kept their
+// logits are compared.  Where more than two agree, or a gate is NaN, the row's choice is made
+// again on whole logits.
 //
 // Sums.  Every lane adds up the gates of its experts in registers, and the block adds its warps
 // in order.  A block alone is done with that.  Otherwise each block writes its row of sums to
