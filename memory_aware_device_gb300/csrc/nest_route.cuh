@@ -360,11 +360,11 @@ __host__ __device__ constexpr uint32_t index_bits(int n) {
 // Lane g of a row's LANES gets in slot s the row's chosen expert number s LANES + g, or -1.  w:
 // the words of the lane's values.  MOST: how many of them are kept, 4, 8 or 16; k is at most that
 // for 4 and 8, where one slot is enough, and any for 16.  Rows that draw on one lane more often, or
-// as often where a tie has to be looked for, are chosen again.  again: the row's words cannot be
-// used; idle: nothing is chosen in the row.
+// as often where a tie has to be looked for, are chosen again.  ex: the row's exponents; again: its
+// words cannot be used; idle: nothing is chosen in the row.
 template <typename T, int V, int LANES, int MOST, int SLOTS>
-__device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_t (&w)[V], bool again, bool idle,
-                                       int (&id)[SLOTS]) {
+__device__ __forceinline__ void choose(const RouteArgs &a, const T *row, const RowExp &ex, uint32_t (&w)[V],
+                                       bool again, bool idle, int (&id)[SLOTS]) {
     constexpr uint32_t kIndex = index_bits(LANES * V);
     constexpr bool kWhole = sizeof(T) == 2;      // no bit of a logit is lost
     constexpr int kList = V < MOST ? V : MOST;   // words kept of a lane's
@@ -459,13 +459,13 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const T *row, uint32_
             }
             again |= row_any<LANES>(crowd);
         }
-        if (__any_sync(0xffffffffu, missing && !idle)) {   // closed, or finite with an exponent beyond the type
+        if (__any_sync(0xffffffffu, missing && !idle)) {   // closed, or finite with an exponent below the type's range
             bool low = false;
             if (!idle) {
 #pragma unroll 1
                 for (int e = g; e < a.experts; e += LANES) {
                     const float x = to_f32(row[e * a.col_stride]);
-                    low |= x > -INFINITY && x < -2e38f;
+                    low |= x > -INFINITY && ex.of(x) == -INFINITY;
                 }
             }
             again |= row_any<LANES>(low);
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
         for (int i = 0; i < V; i++) acc[i] = fmaf(x[i], inv, acc[i]);
 
         int id[kSlots];
-        choose<T, V, LANES, MOST, kSlots>(a, row, w, isnan(sum) || (sizeof(T) == 4 && ex.far), !is_live, id);
+        choose<T, V, LANES, MOST, kSlots>(a, row, ex, w, isnan(sum) || (sizeof(T) == 4 && ex.far), !is_live, id);
         float gate[kSlots], total = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSlots; s++) {
