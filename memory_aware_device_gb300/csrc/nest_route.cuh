@@ -14,7 +14,7 @@
 // Each lane sorts its words once and keeps the largest; then k rounds take the maximum over the
 // row's lanes, and the lane that had it moves its list up.  16-bit logits lose nothing to the
 // index.  With 32-bit logits up to 10 bits are lost, and the word comes from the exponent
-// (x - top) log2(e), negative for every x, which may round two logits to one: one more round
+// (x - top) log2(e), at most 0 for every x, which may round two logits to one: one more round
 // gives the largest word left, and where two of these neighbours agree in the bits kept their
 // logits are compared.  Where more than two agree, or a gate is NaN, the row's choice is made
 // again on whole logits.
@@ -186,13 +186,14 @@ __device__ __forceinline__ void fetch_row(const RouteArgs &a, const T *row, int 
 // exp(x - top) as base 2 to the power r, r = (x - top) log2(e) by one multiply-add.  The
 // rounding of top log2(e), and the little that `shift` is more so that r is below 0 for every
 // x <= top, are the same factor in every gate of the row and leave with the division by their
-// sum.  A largest value near the type's end would overflow the product: far, the difference
-// is taken first.
+// sum.  That little grows with top: up to 2^20 it is at most about 1, a bit of the gates' range,
+// but from 10^8 on it would take all gates of a row to 0.  Beyond 2^20 (far) the difference is
+// taken first: r is then 0 or below, as exact, and in the same order.
 struct RowExp {
     float top, shift;
     bool far;
     __device__ __forceinline__ explicit RowExp(float t)
-        : top(t), shift(fmaf(t, kLog2e, fmaf(fabsf(t), 0x1p-20f, 0x1p-20f))), far(fabsf(t) > 1e38f) {}
+        : top(t), shift(fmaf(t, kLog2e, fmaf(fabsf(t), 0x1p-20f, 0x1p-20f))), far(fabsf(t) > 0x1p20f) {}
     __device__ __forceinline__ float near(float x) const { return fmaf(x, kLog2e, -shift); }
     __device__ __forceinline__ float of(float x) const { return far ? (x - top) * kLog2e : near(x); }
 };
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
 #pragma unroll
             for (int i = 0; i < V; i++) x[i] = ex.near(x[i]);
         }
-        if constexpr (sizeof(T) == 4) {   // r is below 0: its bits inverted are in order
+        if constexpr (sizeof(T) == 4) {   // r is below 0, or +0: its bits inverted are in order
 #pragma unroll
             for (int i = 0; i < V; i++) w[i] = (~__float_as_uint(x[i]) & ~kIndex) | (kIndex - L::of(i, g));
         }
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
         for (int i = 0; i < V; i++) acc[i] = fmaf(x[i], inv, acc[i]);
 
         int id[kSlots];
-        choose<T, V, LANES, MOST, kSlots>(a, row, ex, w, isnan(sum) || (sizeof(T) == 4 && ex.far), !is_live, id);
+        choose<T, V, LANES, MOST, kSlots>(a, row, ex, w, isnan(sum), !is_live, id);
         float gate[kSlots], total = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSlots; s++) {
