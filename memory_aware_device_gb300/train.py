@@ -322,6 +322,7 @@ def _gate_function():
             return tuple(r)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, _ids, grad_weights, _counts, _tokens, _mean, grad_loss):
             logits, mask, *r = ctx.saved_tensors
             return (route_backward(logits, Routing(*r), grad_weights.contiguous(), grad_loss.contiguous(), mask=mask,
@@ -335,7 +336,8 @@ _gate = None
 
 def gate(logits, k: int, mask=None, normalize: bool = True) -> Routing:
     """`route` with gradients: the result's weights and loss are differentiable in the logits (the
-    counts are constants of the gradient; mean_prob carries none)."""
+    counts are constants of the gradient; mean_prob carries none).  Once: a derivative of that
+    gradient raises."""
     global _gate
     if _gate is None:
         _gate = _gate_function()
