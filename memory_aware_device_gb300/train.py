@@ -146,7 +146,10 @@ def _enter(device, stream, used=()):
     torch = _torch or _load_torch()
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}: the operators run on CUDA devices only")
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
+    elif device.index == torch.cuda.current_device():
         return None
     return _Guard(device, stream, used)
 
