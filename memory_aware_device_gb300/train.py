@@ -200,7 +200,8 @@ def _described(*fields):
 
 
 class _RouteCall:
-    """The workspace of calls of these sizes."""
+    """The workspace of calls of these sizes, and its address: a deep copy gets its own, and nothing is
+    pickled (calls into unpickled buffers make one)."""
 
     def __init__(self, tokens, experts, k, device):
         import torch
@@ -208,6 +209,12 @@ class _RouteCall:
         size = _route_workspace(_described(tokens, experts, k, 0, 0, F32, 0))
         self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)   # every call leaves its head zero
         self.tail = (self.workspace.data_ptr(), size)
+
+    def __deepcopy__(self, memo):
+        return _RouteCall(*self.key)
+
+    def __reduce__(self):
+        return type(None), ()
 
 
 def _mask_ptr(mask, logits):
