@@ -471,6 +471,7 @@ class AdamW:
             for t, a in zip(weights, self.starts):
                 self.master[a:a + t.numel()] = t.detach().reshape(-1)
         self._state = torch.zeros(STATE_DT.itemsize, dtype=torch.uint8, device=dev)
+        self._used = None   # stream of the last step
 
         def ptr(t):
             return t.data_ptr() if t is not None else None
@@ -482,16 +483,25 @@ class AdamW:
         self._length = n
         self.set_step(0)
 
+    def _settle(self):
+        """Lets the last step finish if it is on another stream than the current one, which reads and
+        writes of the object's state come behind."""
+        if self._used is not None and self._used != _raw_stream(self._table.device.index):
+            _torch.cuda.synchronize(self._table.device)
+
     def set_step(self, step: int):
-        """Set the number of steps taken (synchronises; 0 at the start)."""
+        """Set the number of steps taken (synchronises; 0 at the start).  Steps enqueued before, on
+        whichever stream, come before it; replays of captured steps have to be waited for."""
         import torch
+        self._settle()
         rec = np.zeros(1, STATE_DT)
         rec["beta1_t"], rec["beta2_t"], rec["step"] = self.betas[0] ** step, self.betas[1] ** step, step
         self._state.copy_(torch.from_numpy(rec.view(np.uint8)))
 
     @property
     def steps(self) -> int:
-        """Steps taken (reads the device)."""
+        """Steps taken (reads the device, behind the steps enqueued before as in `set_step`)."""
+        self._settle()
         return int(self._state.cpu().numpy().view(STATE_DT)["step"][0])
 
     @property
@@ -519,7 +529,8 @@ class AdamW:
         a.lr = lr
         guard = _enter(tb.device, stream, () if stream is None else (grad_scale, *self._held()))
         try:
-            rc = _lib.nest_adamw(*tb.head, self._ref, _raw_stream(tb.device.index))
+            self._used = raw = _raw_stream(tb.device.index)
+            rc = _lib.nest_adamw(*tb.head, self._ref, raw)
         finally:
             if guard is not None:
                 guard.leave()

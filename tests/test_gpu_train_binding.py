@@ -22,3 +22,32 @@ def test_second_derivatives_of_gate_are_refused():
         (grad ** 2).sum().backward()
     plain, = torch.autograd.grad((train.gate(x, 2).weights[:, 0] ** 2 * x[:, 0] ** 2).sum(), x)
     assert torch.equal(plain, grad.detach())
+
+
+def small(bits=32, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = [torch.randn(n, generator=g, device="cuda").to(dtype) for n in (300, 7, 5000)]
+    return train.AdamW(w, [torch.randn(t.shape, generator=g, device="cuda").to(dtype) for t in w], state_bits=bits)
+
+
+def test_the_step_count_after_steps_on_another_stream():
+    """Read and set behind a step that another stream has yet to run."""
+    opt, side = small(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for n in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)      # about 50 ms
+        opt.step(1e-3, stream=side)
+        assert opt.steps == n + 1
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    opt.step(1e-3, stream=side)
+    opt.set_step(100)
+    assert opt.steps == 100
+    with torch.cuda.stream(side):               # the stream that is current there
+        torch.cuda._sleep(100_000_000)
+        opt.step(1e-3)
+    opt.set_step(200)
+    assert opt.steps == 200
+    opt.step(1e-3)
+    assert opt.steps == 201 and not opt._state[24:28].any()
