@@ -493,6 +493,8 @@ class AdamW:
         """Set the number of steps taken (synchronises; 0 at the start).  Steps enqueued before, on
         whichever stream, come before it; replays of captured steps have to be waited for."""
         import torch
+        if step < 0 or step != int(step):
+            raise ValueError(f"the number of steps taken is {step}: it is a whole number of at least 0")
         self._settle()
         rec = np.zeros(1, STATE_DT)
         rec["beta1_t"], rec["beta2_t"], rec["step"] = self.betas[0] ** step, self.betas[1] ** step, step

@@ -51,3 +51,15 @@ def test_the_step_count_after_steps_on_another_stream():
     assert opt.steps == 200
     opt.step(1e-3)
     assert opt.steps == 201 and not opt._state[24:28].any()
+
+
+@pytest.mark.parametrize("step", [-1, -1000, 0.5])
+def test_set_step_refuses(step):
+    opt = small()
+    opt.set_step(3)
+    with pytest.raises(ValueError):
+        opt.set_step(step)
+    assert opt.steps == 3
+    opt.set_step(0)
+    opt.step(1e-3)
+    assert opt.steps == 1 and all(torch.isfinite(w).all() for w in opt.weights)
