@@ -86,16 +86,18 @@ def _check(rc: int, what: str):
         raise NestError(rc, what)
 
 
-_torch = _codes = _raw_stream = None
+_torch = _codes = _raw_stream = _written = None
 
 
 def _load_torch():
-    """torch, imported at the first call, with what every call looks up."""
-    global _torch, _codes, _raw_stream
+    """torch, imported at the first call, with what every call looks up.  `_written` tells autograd
+    that tensors were written in place, so that a backward pass which saved them raises."""
+    global _torch, _codes, _raw_stream, _written
     import torch
     _codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _written = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
     _torch = torch
     return torch
 
@@ -241,6 +243,7 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
         call = None
         _route_workspace(_described(T, E, k, 0, 0, dtype, 0))
     guard = _enter(dev, stream, () if stream is None else (logits, mask, *(out or ())))
+    given = out is not None
     try:
         if out is None:
             out = Routing.empty(T, E, k, dev)
@@ -265,6 +268,8 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
         if guard is not None:
             guard.leave()
     _check(rc, "nest_route")
+    if given:
+        _written(out)
     return out
 
 
@@ -298,8 +303,9 @@ def route_backward(logits, routing: Routing, grad_weights=None, grad_loss=None, 
             raise ValueError(f"grad_loss must be one number, not of shape {tuple(grad_loss.shape)}")
     guard = _enter(dev, stream, () if stream is None else
                    (logits, mask, ids, weights, counts, tokens, grad_weights, grad_loss, out))
+    given = out is not None
     try:
-        if out is None:
+        if not given:
             out = torch.empty((T, E), dtype=logits.dtype, device=dev)
             step = E
         else:
@@ -316,6 +322,8 @@ def route_backward(logits, routing: Routing, grad_weights=None, grad_loss=None, 
         if guard is not None:
             guard.leave()
     _check(rc, "nest_route_backward")
+    if given:
+        _written((out,))
     return out
 
 
@@ -470,6 +478,8 @@ class AdamW:
             self.master = torch.zeros(n, dtype=torch.float32, device=dev)
             for t, a in zip(weights, self.starts):
                 self.master[a:a + t.numel()] = t.detach().reshape(-1)
+        # one tensor for each version counter: views share their base's
+        self._counters = list({id(b): b for b in (t if t._base is None else t._base for t in weights)}.values())
         self._state = torch.zeros(STATE_DT.itemsize, dtype=torch.uint8, device=dev)
         self._used = None   # stream of the last step
 
@@ -537,6 +547,7 @@ class AdamW:
             if guard is not None:
                 guard.leave()
         _check(rc, "nest_adamw")
+        _written(self._counters)
 
     def _held(self):
         return (self._state, self.master, self.m, self.v, self.m_exp, self.v_exp, *self._table.held())

@@ -63,3 +63,46 @@ def test_set_step_refuses(step):
     opt.set_step(0)
     opt.step(1e-3)
     assert opt.steps == 1 and all(torch.isfinite(w).all() for w in opt.weights)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_step_between_forward_and_backward_is_noticed(dtype):
+    """Weights that autograd has saved are written: backward raises, as after any write in place."""
+    base = torch.randn(40, device="cuda").to(dtype)
+    leaf = torch.randn(30, device="cuda").to(dtype).requires_grad_()
+    for bound, used in ((leaf.detach(), leaf), (leaf, leaf), (base[8:38], base[8:38]), (base[8:38].detach(), base)):
+        opt = train.AdamW([bound, torch.zeros(5, device="cuda", dtype=dtype)],
+                          [torch.ones(30, device="cuda", dtype=dtype), torch.ones(5, device="cuda", dtype=dtype)])
+        x = torch.ones_like(used, requires_grad=True)
+        y = (x * used).sum()
+        opt.step(1e-2)
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
+        (x * used).sum().backward()
+
+
+def test_steps_of_inference_tensors():
+    with torch.inference_mode():
+        w, g = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    opt = train.AdamW([w], [g])
+    opt.step(1e-2)
+    assert (w < 1).all()
+
+
+def test_buffers_written_between_forward_and_backward_are_noticed():
+    logits = torch.randn(64, 16, device="cuda")
+    kept, grad = train.Routing.empty(64, 16, 2), torch.ones(64, 16, device="cuda")
+    for out in (kept, train.Routing(*kept)):
+        train.route(logits, 2, out=out)
+        x, z = torch.ones(64, 2, device="cuda", requires_grad=True), torch.ones(64, 16, device="cuda", requires_grad=True)
+        y, z = (x * out.weights).sum(), (z * grad).sum()
+        train.route(logits, 2, out=out)
+        train.route_backward(logits, out, out.weights, out=grad)
+        for v in (y, z):
+            with pytest.raises(RuntimeError, match="inplace"):
+                v.backward()
+    with torch.inference_mode():
+        out = train.Routing.empty(64, 16, 2)
+        train.route(logits, 2, out=out)
+    train.route(logits, 2, out=out)
+    assert torch.equal(out.ids, kept.ids)
