@@ -386,7 +386,8 @@ class _Table:
         n, self.device = len(grads), grads[0].device
         if self.device.type != "cuda":
             raise ValueError(f"tensors are on {self.device}: the operators run on CUDA devices only")
-        self.keep = (list(grads), list(weights or ()))
+        # aliases: the storage whose addresses the table holds, also when a tensor is given another
+        self.keep = [t.detach() for t in (*grads, *(weights or ()))]
         rec = np.zeros(n, TENSOR_DT)
         for what, ts in (("grads", grads), ("weights", weights)):
             if ts is None:
@@ -432,12 +433,12 @@ class _Table:
 
     def held(self):
         """Every tensor that the list's calls use."""
-        return (self.table, self.workspace, self.out, *self.keep[0], *self.keep[1])
+        return (self.table, self.workspace, self.out, *self.keep)
 
 
 class GradNorm:
     """nest_grad_norm over a list of contiguous CUDA tensors of one type, bound by reference: the
-    tensors' storage is read by every `run`."""
+    storage that they have now is kept and read by every `run`."""
 
     def __init__(self, grads: Sequence):
         self._table = _Table(grads)
@@ -452,7 +453,8 @@ class AdamW:
     """nest_adamw over a list of tensors, bound by reference.
 
     weights, grads: lists of contiguous CUDA tensors, each list of one type (float32, bfloat16 or
-    float16); the step reads the gradients and updates the weights in place.  The object owns the
+    float16); the step reads the gradients and updates the weights in place, in the storage that they
+    have now, which is kept.  The object owns the
     float32 master weights (weights of 16 bits only), the moments m and v (state_bits 32: float32;
     8: uint8 codes with the scales m_exp and v_exp) and the device's step count: copy into them to
     set them.  Buffers hold the tensors in order, each from a multiple of 256 elements on (`starts`).  weight_decay and
@@ -481,6 +483,8 @@ class AdamW:
         # one tensor for each version counter: views share their base's
         self._counters = list({id(b): b for b in (t if t._base is None else t._base for t in weights)}.values())
         self._state = torch.zeros(STATE_DT.itemsize, dtype=torch.uint8, device=dev)
+        own = (self._state, self.master, self.m, self.v, self.m_exp, self.v_exp)
+        self._own = [t.detach() for t in own if t is not None]   # what the calls use, whatever the names hold later
         self._used = None   # stream of the last step
 
         def ptr(t):
@@ -550,7 +554,7 @@ class AdamW:
         _written(self._counters)
 
     def _held(self):
-        return (self._state, self.master, self.m, self.v, self.m_exp, self.v_exp, *self._table.held())
+        return (*self._own, *self._table.held())
 
     def state_values(self, stream=None):
         """(m, v): the moments, laid out like the object's buffers.  With 8-bit states new bfloat16

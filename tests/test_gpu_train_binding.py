@@ -106,3 +106,21 @@ def test_buffers_written_between_forward_and_backward_are_noticed():
         train.route(logits, 2, out=out)
     train.route(logits, 2, out=out)
     assert torch.equal(out.ids, kept.ids)
+
+
+def test_bound_storage_stays():
+    """Parameters that are given other storage: what was bound is neither freed nor reused."""
+    w = torch.nn.Parameter(torch.ones(100_000, device="cuda"))
+    w.grad = torch.ones_like(w)
+    opt = train.AdamW([w], [w.grad], weight_decay=0.0)
+    bound, w.data = w.data_ptr(), torch.full_like(w.data, 3.0)
+    others = [torch.full_like(w.data, 7.0) for _ in range(8)]
+    assert bound not in [t.data_ptr() for t in others]
+    opt.step(1e-2)
+    assert all((t == 7).all() for t in others) and (w == 3).all()
+    at = [t.data_ptr() for t in (opt.m, opt.v)]
+    opt.m = opt.v = None
+    others += [torch.full((100_096,), 7.0, device="cuda") for _ in range(8)]
+    assert not set(at) & {t.data_ptr() for t in others}
+    opt.step(1e-2)
+    assert all((t == 7).all() for t in others)
