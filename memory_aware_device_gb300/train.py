@@ -386,22 +386,14 @@ class _Table:
         n, self.device = len(grads), grads[0].device
         if self.device.type != "cuda":
             raise ValueError(f"tensors are on {self.device}: the operators run on CUDA devices only")
+        rec = self.rec = np.zeros(n, TENSOR_DT)
+        rec["numel"] = [t.numel() for t in grads]
+        rec["grad"] = self._addresses("grads", grads, grads[0].dtype)
+        if weights is not None:
+            rec["weight"] = self._addresses("weights", weights, weights[0].dtype if len(weights) else None)
+        rec["weight_decay"], rec["lr_scale"] = weight_decay, lr_scale
         # aliases: the storage whose addresses the table holds, also when a tensor is given another
         self.keep = [t.detach() for t in (*grads, *(weights or ()))]
-        rec = np.zeros(n, TENSOR_DT)
-        for what, ts in (("grads", grads), ("weights", weights)):
-            if ts is None:
-                continue
-            if len(ts) != n:
-                raise ValueError(f"{len(ts)} {what} for {n} tensors")
-            for i, t in enumerate(ts):
-                if t.dtype != ts[0].dtype or t.device != self.device or not t.is_contiguous() or \
-                        t.numel() != grads[i].numel():
-                    raise ValueError(f"{what}[{i}] must be a contiguous {ts[0].dtype} tensor of {grads[i].numel()} "
-                                     f"elements on {self.device}")
-                rec["grad" if what == "grads" else "weight"][i] = t.data_ptr()
-        rec["numel"] = [t.numel() for t in grads]
-        rec["weight_decay"], rec["lr_scale"] = weight_decay, lr_scale
         if weights is not None:
             at = np.argsort(rec["weight"], kind="stable")
             at = at[rec["numel"][at] > 0]
@@ -410,16 +402,36 @@ class _Table:
                 raise ValueError("weights overlap")
         self.grad_type = _type(grads[0], "grads")
         self.info = TableInfo()
-        host = np.ascontiguousarray(rec)
-        _check(lib().nest_table_query(host.ctypes.data, n, C.byref(self.info)), "nest_table_query")
-        packed = np.zeros(self.info.table_bytes, np.uint8)
-        _check(lib().nest_table_pack(host.ctypes.data, n, C.byref(self.info), packed.ctypes.data), "nest_table_pack")
-        self.table = torch.from_numpy(packed).to(self.device)
+        _check(lib().nest_table_query(rec.ctypes.data, n, C.byref(self.info)), "nest_table_query")
+        self.table = self._packed().to(self.device)
         ws = lib().nest_grad_norm_workspace_size(C.byref(self.info))
         self.workspace = torch.zeros(ws, dtype=torch.uint8, device=self.device)
         self.out = torch.empty(2, dtype=torch.float32, device=self.device)
         self.head = (C.byref(self.info), self.table.data_ptr())
         self.tail = (self.out.data_ptr(), self.workspace.data_ptr(), ws)
+
+    def _addresses(self, what, ts, dtype):
+        """The tensors' addresses, or an error where they are not the list's."""
+        if len(ts) != len(self.rec):
+            raise ValueError(f"{len(ts)} {what} for {len(self.rec)} tensors")
+        for i, (t, n) in enumerate(zip(ts, self.rec["numel"].tolist())):
+            if t.dtype != dtype or t.device != self.device or not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"{what}[{i}] must be a contiguous {dtype} tensor of {n} elements on {self.device}")
+        return [t.data_ptr() for t in ts]
+
+    def _packed(self):
+        import torch
+        packed = np.zeros(self.info.table_bytes, np.uint8)
+        _check(lib().nest_table_pack(self.rec.ctypes.data, len(self.rec), C.byref(self.info), packed.ctypes.data),
+               "nest_table_pack")
+        return torch.from_numpy(packed)
+
+    def bind_grads(self, grads):
+        import torch
+        self.rec["grad"] = self._addresses("grads", grads, self.keep[0].dtype)
+        torch.cuda.synchronize(self.device)     # calls under way read the table and the gradients before
+        self.table.copy_(self._packed())        # in its place: captured calls read it too
+        self.keep[:len(grads)] = [t.detach() for t in grads]
 
     def norm(self, max_norm, stream):
         guard = _enter(self.device, stream, () if stream is None else self.held())
@@ -447,6 +459,10 @@ class GradNorm:
         """float32 [2]: the global norm, and min(1, max_norm / (norm + 1e-6)), NaN when the norm is
         not finite.  The same buffer every call; calls that overlap on the GPU race on it."""
         return self._table.norm(max_norm, stream)
+
+    def bind_grads(self, grads: Sequence):
+        """Read these tensors from now on: as many, of the same type and sizes (synchronises)."""
+        self._table.bind_grads(grads)
 
 
 class AdamW:
@@ -527,6 +543,13 @@ class AdamW:
         further 1/256 of the bf16 weight bytes."""
         per = 2 * self.state_bits // 8 + (4 if self.master is not None else 0)
         return per // 2
+
+    def bind_grads(self, grads: Sequence):
+        """Read these gradients from now on - after they were allocated anew, as by a zero_grad that
+        sets them to None: as many tensors, of the same type and sizes.  Moments and step count stay,
+        and captured steps read the new ones too (synchronises)."""
+        self._table.bind_grads(grads)
+        self.grads = list(grads)
 
     def grad_norm(self, max_norm: float = math.inf, stream=None):
         """Norm and clip scale of the gradients, as `GradNorm.run`."""

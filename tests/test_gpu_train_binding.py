@@ -124,3 +124,43 @@ def test_bound_storage_stays():
     assert not set(at) & {t.data_ptr() for t in others}
     opt.step(1e-2)
     assert all((t == 7).all() for t in others)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_bound_anew(bits):
+    """The list goes on with new gradient tensors: same moments, count and results as one that kept its own;
+    a captured step reads the new ones too."""
+    a, b = small(bits), small(bits)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.step(1e-3, grad_scale=b.grad_norm(1.0)[1])
+    for n in range(4):
+        new = [torch.randn_like(g) for g in a.grads]
+        for g, x in zip(a.grads, new):
+            g.copy_(x)
+        b.bind_grads(new)
+        assert all(p is q for p, q in zip(b.grads, new))
+        del new
+        norm = a.grad_norm(1.0)
+        a.step(1e-3, grad_scale=norm[1])
+        if n % 2:
+            graph.replay()
+        else:
+            b.step(1e-3, grad_scale=b.grad_norm(1.0)[1])
+        for p, q in zip((*a.weights, a.master, a.m, a.v), (*b.weights, b.master, b.m, b.v)):
+            assert torch.equal(p, q)
+    assert a.steps == b.steps == 4
+
+
+def test_binding_refusals():
+    opt = small()
+    good = [torch.zeros_like(g) for g in opt.grads]
+    before = opt.grads
+    for bad in (good[:2], [], good[:2] + [good[2].float()], good[:2] + [good[2][1:]], good[:2] + [good[2].cpu()],
+                good[:2] + [torch.zeros(10000, device="cuda", dtype=good[2].dtype)[::2]]):
+        with pytest.raises(ValueError):
+            opt.bind_grads(bad)
+    assert opt.grads is before
+    norm = train.GradNorm(good)
+    norm.bind_grads([g + 1 for g in good])
+    assert abs(float(norm.run()[0]) - 5307 ** 0.5) < 1e-3
