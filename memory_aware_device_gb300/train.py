@@ -211,6 +211,18 @@ class _RouteCall:
         size = _route_workspace(_described(tokens, experts, k, 0, 0, F32, 0))
         self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)   # every call leaves its head zero
         self.tail = (self.workspace.data_ptr(), size)
+        self.streams = set()   # which come behind the clearing
+        if device.type == "cuda":
+            self.made = torch.cuda.current_stream(device)
+            self.streams.add(self.made.cuda_stream)
+
+    def join(self):
+        """Before the first call on another stream than the one that clears the workspace.  (A capture
+        cannot wait for what is outside it; its replays come later.)"""
+        if not _torch.cuda.is_current_stream_capturing():
+            here = _torch.cuda.current_stream(self.key[3])
+            here.wait_stream(self.made)
+            self.streams.add(here.cuda_stream)
 
     def __deepcopy__(self, memo):
         return _RouteCall(*self.key)
@@ -260,10 +272,13 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
         elif stream is not None:
             call.workspace.record_stream(stream)
         ids, weights, counts, tokens, mean_prob, loss = out
+        raw = _raw_stream(dev.index)
+        if raw not in call.streams:
+            call.join()
         rc = _lib.nest_route(_described(T, E, k, *logits.stride(), dtype, 1 if normalize else 0), logits.data_ptr(),
                              None if mask is None else _mask_ptr(mask, logits), ids.data_ptr(), weights.data_ptr(),
                              counts.data_ptr(), tokens.data_ptr(), mean_prob.data_ptr(), loss.data_ptr(), *call.tail,
-                             _raw_stream(dev.index))
+                             raw)
     finally:
         if guard is not None:
             guard.leave()
@@ -403,9 +418,9 @@ class _Table:
         self.grad_type = _type(grads[0], "grads")
         self.info = TableInfo()
         _check(lib().nest_table_query(rec.ctypes.data, n, C.byref(self.info)), "nest_table_query")
-        self.table = self._packed().to(self.device)
         ws = lib().nest_grad_norm_workspace_size(C.byref(self.info))
         self.workspace = torch.zeros(ws, dtype=torch.uint8, device=self.device)
+        self.table = self._packed().to(self.device)   # waits for the stream, the clearing with it
         self.out = torch.empty(2, dtype=torch.float32, device=self.device)
         self.head = (C.byref(self.info), self.table.data_ptr())
         self.tail = (self.out.data_ptr(), self.workspace.data_ptr(), ws)

@@ -164,3 +164,33 @@ def test_binding_refusals():
     norm = train.GradNorm(good)
     norm.bind_grads([g + 1 for g in good])
     assert abs(float(norm.run()[0]) - 5307 ** 0.5) < 1e-3
+
+
+def test_workspaces_are_clear_on_whichever_stream_the_first_call_is():
+    """The clearing is late, on the stream where the buffers were made; the first call is elsewhere."""
+    x = torch.randn(5000, 64, device="cuda")
+    want, side = train.route(x, 4), torch.cuda.Stream()
+    size = train.Routing.empty(5000, 64, 4).call.workspace.numel()
+    torch.cuda.synchronize()
+    for inside in (False, True):
+        dirty = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        del dirty
+        torch.cuda._sleep(100_000_000)      # about 50 ms
+        out = train.Routing.empty(5000, 64, 4)
+        if inside:
+            with torch.cuda.stream(side):
+                train.route(x, 4, out=out)
+        else:
+            train.route(x, 4, out=out, stream=side)
+        side.synchronize()
+        for p, q in zip(want, out):
+            assert torch.equal(p, q)
+    grads = [torch.randn(100_000, device="cuda") for _ in range(3)]
+    want = train.GradNorm(grads).run(1.0).clone()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    norm = train.GradNorm(grads)
+    got = norm.run(1.0, stream=side)
+    side.synchronize()
+    assert torch.equal(want, got)
