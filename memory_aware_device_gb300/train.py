@@ -211,7 +211,7 @@ class _RouteCall:
         size = _route_workspace(_described(tokens, experts, k, 0, 0, F32, 0))
         self.workspace = torch.zeros(size, dtype=torch.uint8, device=device)   # every call leaves its head zero
         self.tail = (self.workspace.data_ptr(), size)
-        self.streams = set()   # which come behind the clearing
+        self.streams = set()   # which come behind the clearing, and which the workspace's memory waits for
         if device.type == "cuda":
             self.made = torch.cuda.current_stream(device)
             self.streams.add(self.made.cuda_stream)
@@ -219,8 +219,9 @@ class _RouteCall:
     def join(self):
         """Before the first call on another stream than the one that clears the workspace.  (A capture
         cannot wait for what is outside it; its replays come later.)"""
+        here = _torch.cuda.current_stream(self.key[3])
+        self.workspace.record_stream(here)
         if not _torch.cuda.is_current_stream_capturing():
-            here = _torch.cuda.current_stream(self.key[3])
             here.wait_stream(self.made)
             self.streams.add(here.cuda_stream)
 
@@ -269,8 +270,6 @@ def route(logits, k: int, mask=None, normalize: bool = True, out: Routing | None
             _want(out.mean_prob, "out.mean_prob", torch.float32, (E,), dev)
             _want(out.loss, "out.loss", torch.float32, (), dev)
             call = _RouteCall(T, E, k, dev)
-        elif stream is not None:
-            call.workspace.record_stream(stream)
         ids, weights, counts, tokens, mean_prob, loss = out
         raw = _raw_stream(dev.index)
         if raw not in call.streams:
@@ -424,6 +423,15 @@ class _Table:
         self.out = torch.empty(2, dtype=torch.float32, device=self.device)
         self.head = (C.byref(self.info), self.table.data_ptr())
         self.tail = (self.out.data_ptr(), self.workspace.data_ptr(), ws)
+        self.own = [self.table, self.workspace, self.out]   # made here, as an optimizer's buffers
+        self.streams = {torch.cuda.current_stream(self.device).cuda_stream}   # which their memory waits for
+
+    def join(self, raw):
+        """Before the first call on a stream."""
+        here = _torch.cuda.current_stream(self.device)
+        for t in self.own:
+            t.record_stream(here)
+        self.streams.add(raw)
 
     def _addresses(self, what, ts, dtype):
         """The tensors' addresses, or an error where they are not the list's."""
@@ -451,7 +459,10 @@ class _Table:
     def norm(self, max_norm, stream):
         guard = _enter(self.device, stream, () if stream is None else self.held())
         try:
-            rc = _lib.nest_grad_norm(*self.head, self.grad_type, max_norm, *self.tail, _raw_stream(self.device.index))
+            raw = _raw_stream(self.device.index)
+            if raw not in self.streams:
+                self.join(raw)
+            rc = _lib.nest_grad_norm(*self.head, self.grad_type, max_norm, *self.tail, raw)
         finally:
             if guard is not None:
                 guard.leave()
@@ -459,8 +470,8 @@ class _Table:
         return self.out
 
     def held(self):
-        """Every tensor that the list's calls use."""
-        return (self.table, self.workspace, self.out, *self.keep)
+        """The tensors that were given to the list."""
+        return self.keep
 
 
 class GradNorm:
@@ -515,7 +526,7 @@ class AdamW:
         self._counters = list({id(b): b for b in (t if t._base is None else t._base for t in weights)}.values())
         self._state = torch.zeros(STATE_DT.itemsize, dtype=torch.uint8, device=dev)
         own = (self._state, self.master, self.m, self.v, self.m_exp, self.v_exp)
-        self._own = [t.detach() for t in own if t is not None]   # what the calls use, whatever the names hold later
+        tb.own += [t.detach() for t in own if t is not None]   # what the calls use, whatever the names hold later
         self._used = None   # stream of the last step
 
         def ptr(t):
@@ -581,9 +592,11 @@ class AdamW:
                 raise ValueError(f"grad_scale must be one float32 number on {tb.device}")
             a.grad_scale = grad_scale.data_ptr()
         a.lr = lr
-        guard = _enter(tb.device, stream, () if stream is None else (grad_scale, *self._held()))
+        guard = _enter(tb.device, stream, () if stream is None else (grad_scale, *tb.held()))
         try:
             self._used = raw = _raw_stream(tb.device.index)
+            if raw not in tb.streams:
+                tb.join(raw)
             rc = _lib.nest_adamw(*tb.head, self._ref, raw)
         finally:
             if guard is not None:
@@ -591,21 +604,20 @@ class AdamW:
         _check(rc, "nest_adamw")
         _written(self._counters)
 
-    def _held(self):
-        return (*self._own, *self._table.held())
-
     def state_values(self, stream=None):
         """(m, v): the moments, laid out like the object's buffers.  With 8-bit states new bfloat16
         tensors with the exact values of the codes, else the float32 buffers themselves."""
         if self.state_bits == 32:
             return self.m, self.v
         tb, kind = self._table, _torch.bfloat16
-        guard = _enter(tb.device, stream, () if stream is None else self._held())
+        guard = _enter(tb.device, stream)
         try:
+            raw = _raw_stream(tb.device.index)
+            if raw not in tb.streams:
+                tb.join(raw)
             m = _torch.empty(self._length, dtype=kind, device=tb.device)
             v = _torch.empty(self._length, dtype=kind, device=tb.device)
-            rc = _lib.nest_adamw_values(tb.head[0], *self._codes, m.data_ptr(), v.data_ptr(),
-                                        _raw_stream(tb.device.index))
+            rc = _lib.nest_adamw_values(tb.head[0], *self._codes, m.data_ptr(), v.data_ptr(), raw)
         finally:
             if guard is not None:
                 guard.leave()

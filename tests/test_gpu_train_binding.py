@@ -194,3 +194,37 @@ def test_workspaces_are_clear_on_whichever_stream_the_first_call_is():
     got = norm.run(1.0, stream=side)
     side.synchronize()
     assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_buffers_freed_while_another_stream_uses_them(given):
+    """The memory of workspaces, tables and states is not another tensor's before the calls are done,
+    whether the other stream is current or given."""
+    x, side = torch.randn(5000, 64, device="cuda"), torch.cuda.Stream()
+    out = train.Routing.empty(5000, 64, 4)
+    weights = [torch.ones(100_000, device="cuda").bfloat16()]
+    grads = [torch.ones(100_000, device="cuda")]
+    opt, norm = train.AdamW(weights, grads, state_bits=8), train.GradNorm(grads)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)      # about 100 ms
+        for t in (x, *out, *weights, *grads):
+            t.record_stream(side)
+        if not given:
+            train.route(x, 4, out=out)
+            norm.run()
+            opt.step(1e-3, grad_scale=opt.grad_norm(1.0)[1])
+            opt.state_values()
+    if given:
+        train.route(x, 4, out=out, stream=side)
+        norm.run(stream=side)
+        opt.step(1e-3, grad_scale=opt.grad_norm(1.0, stream=side)[1], stream=side)
+        opt.state_values(stream=side)
+    hidden = [out.call.workspace, *norm._table.own, *opt._table.own]
+    at = {t.data_ptr(): t.numel() * t.element_size() for t in hidden}
+    assert len(at) == len(hidden)
+    del out, opt, norm, hidden
+    others = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in at.values() for _ in range(4)]
+    busy = not side.query()
+    assert not at.keys() & {t.data_ptr() for t in others}
+    assert busy     # else nothing was shown
