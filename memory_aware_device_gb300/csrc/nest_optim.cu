@@ -156,8 +156,8 @@ __device__ __forceinline__ void store_block(T *p, int n, bool vector, int lane, 
 // ---- gradient norm ----------------------------------------------------------------
 
 // A sum in 32 bits with the rounding error of every addition added up beside it (Knuth's
-// exact sum of two numbers).  64-bit additions are many times slower here: one for every 16
-// values of a thread took 5 of 76 us.
+// exact sum of two numbers).  64-bit additions are many times slower here: with one for every 16
+// values of a thread the norm of 201M values takes 64.4 us against 62.6.
 struct Sum {
     float hi = 0.0f, lo = 0.0f;
     __device__ __forceinline__ void add(float x) {
@@ -178,8 +178,8 @@ __device__ __forceinline__ float block_sum(float v, float *sh) {
 
 // The norm.  Every gradient is read once, two blocks of a warp under way at a time; memory bounds it.
 // Measured: 201M values in 16 bits 63 us, 6.4 TB/s (a flat loop over one buffer 59 us); the
-// smallest lists 3.5 us.  All thread blocks of a long list are resident at once: with six times
-// as many 70 us.
+// smallest lists 3.6 us.  All thread blocks of a long list are resident at once: with six times
+// as many 73 us.
 constexpr int kNormsPerSm = 8;
 
 template <typename T>
@@ -445,10 +445,10 @@ struct Stage {
 constexpr uint32_t kRareM = (uint32_t(14 + 127) << 23) | 0x600000u, kRareV = (uint32_t(30 + 127) << 23) | 0x600000u;
 
 // The step.  Memory bounds it: 28 bytes a weight with 16-bit weights and gradients and moments in
-// 32 bits, 16 with moments in 8 bits.  Measured over 201M weights, 32 bits: 818 us, 6.9 TB/s
-// (842 with one thread block per worker); 8 bits: 496 us, 6.5 TB/s (628 with one, and 543 with
-// 8 instead of 4; 575 with copies of 16 bytes at a stride of 32).  Three thread blocks to an SM,
-// up to 80 registers: with four the 32-bit step takes 868 us against 853.
+// 32 bits, 16 with moments in 8 bits.  Measured over 201M weights, 32 bits: 820 us, 6.9 TB/s
+// (839 with one thread block per worker); 8 bits: 498 us, 6.5 TB/s (537 with one, and 544 with
+// 8 instead of 4; 504 with a lane's copies side by side instead of 32 lanes').  Three thread blocks
+// to an SM, up to 80 registers: with four the 32-bit step takes 824 us, the 8-bit one the same.
 template <typename W, typename G, bool EIGHT>
 __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a) {
     constexpr bool kOwnMaster = sizeof(W) == 4;
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, kStepsPerSm) adamw_kernel(StepArgs a
     }
 }
 
-// The values of 8-bit moments.  201M weights: 188 us, 6.4 TB/s; memory bounds it.
+// The values of 8-bit moments.  201M weights: 191 us, 6.3 TB/s; memory bounds it.
 __global__ void __launch_bounds__(kThreads) values_kernel(int64_t blocks, const uint8_t *m, const uint8_t *v,
                                                           const int8_t *m_exp, const int8_t *v_exp,
                                                           __nv_bfloat16 *m_out, __nv_bfloat16 *v_out) {

@@ -3,10 +3,10 @@
 //
 // A warp takes 32 / LANES rows at a time, each held in the registers of LANES lanes, so that the
 // logits are read once and what is done per row (reductions, rounds, results) is shared by
-// several rows: forward up to 32 values per lane (262144 x 256: 115 us against 128 with 16 lanes of
-// 16 values), backward, which has little of that, 8 where the row allows (262144 x 64: 20 us
-// against 54 with a row to a warp).  Logits are read in pieces per lane where alignment allows
-// (VEC: forward 92 us against 107, backward 262144 x 64 20 against 31).
+// several rows: forward up to 32 values per lane (262144 x 256 in 32 bits, k = 8: 85 us against 104
+// with 16 lanes of 16 values), backward, which has little of that, 8 where the row allows (262144 x 64
+// in bfloat16, k = 2: 24 us against 78 with a row to a warp).  Logits are read in pieces per lane where
+// alignment allows (VEC: those two 85 us against 106 and 24 against 34).
 //
 // Choice of the k largest.  A logit becomes a 32-bit word whose order is that of the logits,
 // with its lowest bits replaced by the complement of the expert's index: all words of a row
@@ -22,9 +22,10 @@
 // Sums.  Every lane adds up the gates of its experts in registers, and the block adds its warps
 // in order.  A block alone is done with that.  Otherwise each block writes its row of sums to
 // the workspace, and the last one to have done so adds the rows; rows of more than 128 experts
-// are more than one block should read, and a second kernel adds them (32768 x 1024: 47 us against
-// 63; 30011 x 72: 12.3 us in one launch against 13.9 in two).  Either way they are added in an
-// order of their own: no result depends on the order in which blocks run.
+// are more than one block should read, and a second kernel adds them (32768 x 1024 in 32 bits: 48 us
+// against 57, 262144 x 256 85 against 92; 30011 x 72 in float16: 11.9 us in one launch against 12.3 in
+// two).  Either way they are added in an order of their own: no result depends on the order in
+// which blocks run.
 #pragma once
 
 #include <type_traits>
@@ -55,7 +56,9 @@ struct RouteArgs {
 
 // Largest block and blocks per SM that the kernels are compiled for, by the values per lane: the
 // registers of the values, of their words and of the sums.  The forward kernel takes any whole
-// number of warps up to that.
+// number of warps up to that.  Blocks of 28 and 20 warps leave it 72 and 96 registers, and up to 96
+// bytes of a thread go through memory; with 24 and 16 warps none do, and 262144 x 100 takes 51 us
+// against 50, 262144 x 160 71 against 66 (32 bits, k = 4 and 6).
 template <int V>
 struct RouteShape {
     static constexpr int kWarps = V <= 8 ? 32 : V <= 16 ? 28 : V <= 24 ? 20 : 16;
@@ -488,9 +491,14 @@ constexpr int kApart = 24;
 __host__ __device__ __forceinline__ int row_pitch(int experts) { return (experts + 3) & ~3; }
 
 // Measured: 262144 x 256 in 32 bits, k = 8: 85 us, 3.4 TB/s of the 285 MB that it must move, whose
-// floor is 42 us.  250 instructions a row, for sorting above all, bound it: the integer pipe is
-// busy 57 % of the time, memory 38 %.  MOST, the words that a lane keeps: with 8 this takes 92 us
-// against 137 with 16; k = 2 with 4 takes 72 us against 81 with 8 (bfloat16 76 against 87).
+// floor is 42 us.  250 instructions a row, for sorting above all, from four warps per scheduler, whose
+// waits for their own results they do not cover: issue slots are used 62 % of the time, the integer
+// pipe 65 %, memory 42 %.  A row of 16-bit logits costs as many (131072 x 256 in bfloat16 50 us, floor
+// 11).  MOST, the words that a lane keeps: with 8 this takes 85 us against 137 with 16; k = 2 with 4
+// takes 67 us against 75 with 8 (bfloat16 71 against 80).  With 16, k = 32 of 256 costs 870 instructions
+// a row (131072 rows in bfloat16 145 us, floor 15), k = 16 of 512 1160 (65536 rows in 32 bits 105, floor 21).
+// Rows whose choice is made again: 262144 x 256 with all logits of a row equal 473 us, with logits
+// that are bfloat16 numbers in 32 bits 171.
 template <typename T, int LANES, int V, bool VEC, int MOST>
 __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm) route_kernel(RouteArgs a) {
     constexpr int kRows = 32 / LANES, kSlots = MOST <= 8 ? 1 : 32 / LANES;
@@ -718,7 +726,10 @@ __global__ void __launch_bounds__(RouteShape<V>::kThreads, RouteShape<V>::kPerSm
 // drops out of the gradient, and without it the subtraction of the mean loses no digits.
 // The k terms reach their experts' lanes through the row's share of shared memory.
 // Measured: 131071 x 256 in 32 bits, k = 8: 48.7 us, 5.8 TB/s of 281 MB; 262144 rows 92 us, 6.1 TB/s.
-// Waits for memory bound it.  FEW: one slot per lane holds the k chosen.
+// Waits for memory bound it.  Short and 16-bit rows have as much to do for fewer bytes: 262144 x 64
+// in bfloat16, k = 2: 24 us, floor 11; 262144 x 16 in 32 bits 19, floor 6; 131072 x 256 in bfloat16,
+// k = 8: 39, floor 22: issue slots are used 47 to 63 % of the time, and loads are still what warps
+// wait for most.  FEW: one slot per lane holds the k chosen.
 template <typename T, int LANES, int V, bool VEC, bool FEW>
 __global__ void __launch_bounds__(BackwardShape<V>::kThreads, BackwardShape<V>::kPerSm) route_backward_kernel(RouteArgs a) {
     constexpr int kWarps = BackwardShape<V>::kWarps, kRows = 32 / LANES, kSlots = FEW ? 1 : 32 / LANES;
@@ -846,7 +857,7 @@ template <int N> struct Number { static constexpr int v = N; };
 
 // fn(lanes, values): how a row of `experts` is held.  Eight lanes hold up to 32 values each;
 // longer rows take more lanes.  24 values, whole runs of 4 and 8 words but not of 16, are for k up
-// to 8 (262144 x 160 in bfloat16, k = 6: 76 us against 93 with 32 values).
+// to 8 (262144 x 160 in bfloat16, k = 6: 70 us against 87 with 32 values).
 template <typename F>
 int with_row(int experts, int k, F fn) {
     if (experts <= 32) return fn(Number<8>{}, Number<4>{});
