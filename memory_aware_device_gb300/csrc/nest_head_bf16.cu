@@ -1,0 +1,11 @@
+// The output head's products in bfloat16.
+#include "nest_head.cuh"
+
+namespace nest {
+namespace head {
+int launch_gemm_bf16(Product p, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &args, int pairs,
+                     void *stream) {
+    return launch_gemm<__nv_bfloat16>(p, a, b, args, pairs, stream);
+}
+}  // namespace head
+}  // namespace nest

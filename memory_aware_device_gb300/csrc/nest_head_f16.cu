@@ -1,0 +1,11 @@
+// The output head's products in IEEE half precision.
+#include "nest_head.cuh"
+
+namespace nest {
+namespace head {
+int launch_gemm_f16(Product p, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &args, int pairs,
+                    void *stream) {
+    return launch_gemm<__half>(p, a, b, args, pairs, stream);
+}
+}  // namespace head
+}  // namespace nest
