@@ -11,25 +11,34 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Rows of 16-bit numbers that are copied to 16-byte aligned rows.
+struct Rows {
+    const uint16_t *from;
+    int64_t row_stride, col_stride, width;
+    uint16_t *to;
+    int64_t pitch;      // elements
+};
+
 struct RowArgs {
-    const void *hidden;
-    int64_t row_stride, col_stride;
-    int64_t tokens, hidden_size, packed;   // packed: elements of a compacted row
-    int32_t wide;                          // rows can be read 16 bytes at a time
+    Rows hidden;
+    int64_t tokens;
     const void *labels;                    // with labels
     int32_t wide_labels;
     int64_t vocab;
     const uint8_t *flags;                  // with a teacher: which tokens are live
-    int32_t chunk;                         // tokens per block
-    uint16_t *out;                         // [n][packed]
+    int32_t chunk, blocks;                 // tokens per block; the blocks after these copy weights
     int32_t *rows, *count;                 // [n], [1]
     int32_t *column;                       // [T], with labels
     uint32_t *ticket;
+    Rows weight;                           // to copy, or width 0
     // forward: of tokens that are not live
     float *losses, *lse;
     int32_t *live;
     // backward
     uint16_t *grad;                        // [T][D]
+    int32_t wide_grad;
+    const float *grad_losses;
+    float *parts;                          // [blocks] the largest finite |grad_losses| of live tokens
 };
 
 __device__ __forceinline__ int label_of(const RowArgs &a, int64_t t) {
@@ -41,80 +50,112 @@ __device__ __forceinline__ bool is_live(const RowArgs &a, int64_t t) {
     return a.flags ? a.flags[t] != 0 : label_of(a, t) >= 0;
 }
 
+// One row by a warp.  Rows off alignment are read from the aligned addresses around them and shifted: 16
+// bytes per lane whatever the offset.  (No 16 bytes are read of which the row has none.)
+__device__ __forceinline__ void copy_row(const Rows &x, int64_t source, int64_t target, int lane) {
+    const uint16_t *from = x.from + source * x.row_stride;
+    uint16_t *to = x.to + target * x.pitch;
+    if (x.col_stride != 1 && x.width != 1) {
+#pragma unroll 8
+        for (int64_t d = lane; d < x.width; d += 32) to[d] = from[d * x.col_stride];
+        return;
+    }
+    const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(from)) & 15;
+    const uint4 *base = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(from) - shift);
+    const int64_t units = (x.width + 7) / 8, last = (int64_t(shift) + 2 * x.width - 1) >> 4;
+    uint4 *out = reinterpret_cast<uint4 *>(to);
+    if (!shift) {
+#pragma unroll 4
+        for (int64_t u = lane; u < units; u += 32) out[u] = base[u];
+        return;
+    }
+    const bool two = shift & 8, one = shift & 4, part = shift & 2;
+#pragma unroll 4
+    for (int64_t u = lane; u < units; u += 32) {
+        const uint4 p = base[u], q = u < last ? base[u + 1] : make_uint4(0, 0, 0, 0);
+        uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 6; e++) w[e] = two ? w[e + 2] : w[e];
+#pragma unroll
+        for (int e = 0; e < 5; e++) w[e] = one ? w[e + 1] : w[e];
+#pragma unroll
+        for (int e = 0; e < 4; e++) w[e] = part ? __funnelshift_r(w[e], w[e + 1], 16) : w[e];
+        out[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+__device__ __forceinline__ void clear_row(uint16_t *to, int64_t width, bool wide, int lane) {
+    if (wide) {
+        for (int64_t u = lane; u < width / 8; u += 32) reinterpret_cast<uint4 *>(to)[u] = make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll 4
+        for (int64_t d = lane; d < width; d += 32) to[d] = 0;
+    }
+}
+
 // Lists the live tokens in order and copies their hidden states next to each other, so that the products
-// run over live tokens alone and nothing that another token holds enters a sum.  Every block counts the
-// live tokens before its own: a read of all labels, against rows of hidden states of a thousand times
-// their size.
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(RowArgs a) {
-    __shared__ int sh_sum[kRowThreads / 32], sh_before;
+// run over live tokens alone and nothing that another token holds enters a sum; behind them it clears the rows
+// that the last stage of tokens reads.  Every block counts the live tokens before its own and in all: a read
+// of all labels, against rows of hidden states of a thousand times their size.  Blocks past `blocks` copy
+// weights that TMA cannot read where they are.
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int kWarps = kRowThreads / 32;
+    __shared__ int sh_before[kWarps], sh_all[kWarps];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t first = int64_t(blockIdx.x) * a.chunk, end = min(first + a.chunk, a.tokens);
-    int before = 0;
-    for (int64_t t = threadIdx.x; t < first; t += kRowThreads) before += is_live(a, t);
-    before = __reduce_add_sync(0xffffffffu, before);
-    if (lane == 0) sh_sum[warp] = before;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int s = 0;
-        for (int w = 0; w < kRowThreads / 32; w++) s += sh_sum[w];
-        sh_before = s;
-        if (blockIdx.x == 0 && a.ticket) *a.ticket = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = int(blockIdx.x);
+    if (block >= a.blocks) {
+        const int64_t warps = int64_t(gridDim.x - a.blocks) * kWarps;
+        for (int64_t r = int64_t(block - a.blocks) * kWarps + warp; r < a.vocab; r += warps) copy_row(a.weight, r, r, lane);
+        return;
     }
+    const int64_t first = int64_t(block) * a.chunk, end = min(first + a.chunk, a.tokens);
+    int before = 0, all = 0;
+    for (int64_t t = threadIdx.x; t < a.tokens; t += kRowThreads) {
+        const int live = is_live(a, t);
+        all += live;
+        before += t < first ? live : 0;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) sh_before[warp] = before, sh_all[warp] = all;
     __syncthreads();
-    int at = sh_before;
-    const uint16_t *hidden = static_cast<const uint16_t *>(a.hidden);
+    before = all = 0;
+    for (int w = 0; w < kWarps; w++) before += sh_before[w], all += sh_all[w];
+    if (block == 0 && threadIdx.x == 0) {
+        *a.count = all;
+        if (a.live) *a.live = all;
+        if (a.ticket) *a.ticket = 0;
+    }
+    // rows from the last token to the end of its stage
+    for (int64_t r = all + block * kWarps + warp; r < (all + kDepth - 1) / kDepth * kDepth; r += a.blocks * kWarps)
+        clear_row(a.hidden.to + r * a.hidden.pitch, a.hidden.pitch, true, lane);
+    float top = 0.0f;
+    int at = before;
     for (int64_t t0 = first; t0 < end; t0 += 32) {
         // every warp finds the same 32 tokens' places and copies every eighth of them
         const int64_t t = t0 + lane;
         const bool live = t < end && is_live(a, t);
-        const uint32_t all = __ballot_sync(0xffffffffu, live);
+        const uint32_t set = __ballot_sync(0xffffffffu, live);
         if (warp == 0 && t < end) {
-            if (live) a.rows[at + __popc(all & ((1u << lane) - 1))] = int(t);
+            if (live) a.rows[at + __popc(set & ((1u << lane) - 1))] = int(t);
             if (a.column) a.column[t] = label_of(a, t);
             if (!live && a.losses) a.losses[t] = 0.0f, a.lse[t] = 0.0f;
-        }
-        for (int i = warp; i < 32 && t0 + i < end; i += kRowThreads / 32) {
-            const int64_t source = t0 + i;
-            if (all >> i & 1) {
-                uint16_t *to = a.out + int64_t(at + __popc(all & ((1u << i) - 1))) * a.packed;
-                const uint16_t *from = hidden + source * a.row_stride;
-                if (a.wide) {
-                    const int64_t units = a.hidden_size / 8;
-#pragma unroll 4
-                    for (int64_t u = lane; u < units; u += 32)
-                        reinterpret_cast<uint4 *>(to)[u] = reinterpret_cast<const uint4 *>(from)[u];
-                    for (int64_t d = units * 8 + lane; d < a.hidden_size; d += 32) to[d] = from[d];
-                } else {
-#pragma unroll 8
-                    for (int64_t d = lane; d < a.hidden_size; d += 32) to[d] = from[d * a.col_stride];
-                }
-            } else if (a.grad) {
-                uint16_t *to = a.grad + source * a.hidden_size;
-#pragma unroll 4
-                for (int64_t d = lane; d < a.hidden_size; d += 32) to[d] = 0;
+            if (live && a.grad_losses) {
+                const float g = fabsf(a.grad_losses[t]);
+                if (g < INFINITY) top = fmaxf(top, g);
             }
         }
-        at += __popc(all);
+        for (int i = warp; i < 32 && t0 + i < end; i += kWarps) {
+            if (set >> i & 1) copy_row(a.hidden, t0 + i, at + __popc(set & ((1u << i) - 1)), lane);
+            else if (a.grad) clear_row(a.grad + (t0 + i) * a.hidden.width, a.hidden.width, a.wide_grad, lane);
+        }
+        at += __popc(set);
     }
-    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
-        *a.count = at;
-        if (a.live) *a.live = at;
-    }
-}
-
-// Rows of weights that TMA cannot read where they are, into rows that it can.
-__global__ void __launch_bounds__(kRowThreads) pack_kernel(const uint16_t *from, int64_t row_stride,
-                                                          int64_t col_stride, int64_t rows, int64_t cols,
-                                                          uint16_t *to, int64_t pitch) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = int64_t(gridDim.x) * (kRowThreads / 32);
-    for (int64_t r = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
-#pragma unroll 8
-        for (int64_t d = lane; d < cols; d += 32) to[r * pitch + d] = from[r * row_stride + d * col_stride];
+    if (a.parts && warp == 0) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) a.parts[block] = top;
     }
 }
 
@@ -287,58 +328,53 @@ __global__ void __launch_bounds__(kJoinRows *kJoinParts) join_kernel(JoinArgs a)
     }
 }
 
-struct ScaleArgs {
-    const int32_t *count, *rows;
-    const float *lse, *grad_loss, *grad_losses;
-    float heat;
-    float lift;           // 2^15 in half precision
-    float *row_lse, *row_scale, *unit;
-    uint16_t *hidden;     // the compacted rows, of which those up to a stage's end become zeros
-    int64_t packed;
+struct SumArgs {
+    const int32_t *live, *rows;
+    int32_t piece_rows;         // of grad weight; grad hidden has n
+    int32_t cols;               // D
+    int32_t splits[2];
+    const float *sums[2];       // NULL: nothing to do
+    int64_t pitch[2];
+    uint16_t *out[2];
+    int32_t first_block;        // of grad weight
+    Scale by;
 };
 
-constexpr int kScaleThreads = 1024;
+constexpr int kSumTile = 64;
 
-// The rows' factors, by block 0; the others clear the rows that the last stage of tokens reads past n.
-__global__ void __launch_bounds__(kScaleThreads) scale_kernel(ScaleArgs a) {
-    __shared__ float sh_top[kScaleThreads / 32];
+// Adds the parts of results whose summed index was split, in order, and rounds them: tiles of 64 x 64, turned
+// from columns to rows in shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArgs a) {
+    __shared__ float tile[kSumTile][kSumTile + 1];
     pdl_wait();
     pdl_trigger();
-    const int n = *a.count;
-    if (blockIdx.x) {
-        const int64_t from = int64_t(n) * a.packed, to = int64_t((n + kDepth - 1) / kDepth * kDepth) * a.packed;
-        for (int64_t i = from + int64_t(blockIdx.x - 1) * kScaleThreads + threadIdx.x; i < to;
-             i += int64_t(gridDim.x - 1) * kScaleThreads)
-            a.hidden[i] = 0;
-        return;
-    }
-    const float share = a.grad_loss && n ? *a.grad_loss / float(n) : 0.0f;
-    float top = 0.0f;
-    if (a.grad_losses) {
-        for (int r = threadIdx.x; r < n; r += kScaleThreads) {
-            const float g = fabsf((share + a.grad_losses[a.rows[r]]) * a.heat);
-            if (g < INFINITY) top = fmaxf(top, g);
+    const int n = *a.live, kind = int(blockIdx.x) >= a.first_block, across = (a.cols + kSumTile - 1) / kSumTile;
+    const int at = int(blockIdx.x) - (kind ? a.first_block : 0), rows = kind ? a.piece_rows : n;
+    const int r0 = at / across * kSumTile, c0 = at % across * kSumTile;
+    if (r0 >= rows) return;
+    const int e = scale_exponent(a.by, share_of(a.by, n));
+    const float unit = ldexpf(1.0f / a.by.lift, e);
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const float *from = a.sums[kind] + int64_t(c0) * a.pitch[kind] + r0 + x;
+    const int64_t part = int64_t(a.cols) * a.pitch[kind];
+    if (r0 + x < rows) {
+#pragma unroll 4
+        for (int c = y; c < kSumTile && c0 + c < a.cols; c += 4) {
+            float v = 0.0f;
+#pragma unroll 4
+            for (int s = 0; s < a.splits[kind]; s++) v += from[s * part + int64_t(c) * a.pitch[kind]];
+            tile[x][c] = v * unit;
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if ((threadIdx.x & 31) == 0) sh_top[threadIdx.x >> 5] = top;
-        __syncthreads();
-        for (int w = 0; w < kScaleThreads / 32; w++) top = fmaxf(top, sh_top[w]);
-    } else {
-        const float g = fabsf(share * a.heat);
-        if (g < INFINITY) top = g;
     }
-    // the power of two above it: factors and results are scaled without rounding
-    int e = 0;
-    if (top > 0.0f) frexpf(top, &e);
-    e = max(-100, min(e, 100));
-    const float over = ldexpf(a.lift, -e);
-    for (int r = threadIdx.x; r < n; r += kScaleThreads) {
-        const int t = a.rows[r];
-        a.row_scale[r] = (share + (a.grad_losses ? a.grad_losses[t] : 0.0f)) * a.heat * over;
-        a.row_lse[r] = a.lse[t] * kLog2e;
+    __syncthreads();
+    for (int r = y; r < kSumTile && r0 + r < rows; r += 4) {
+        if (c0 + x < a.cols) {
+            const int64_t row = kind ? r0 + r : a.rows[r0 + r];
+            const T v = from_f32<T>(tile[r][x]);
+            a.out[kind][row * a.cols + c0 + x] = reinterpret_cast<const uint16_t &>(v);
+        }
     }
-    if (threadIdx.x == 0) *a.unit = ldexpf(1.0f / a.lift, e);
 }
 
 int check(const nest_head_desc *d) {
@@ -359,13 +395,46 @@ bool in_place(const nest_head_desc *d, const void *weight) {
            aligned_to(weight, 16);
 }
 
+constexpr int kPairs = kSMs / 2;
+
+// Parts of the summed index of the two gradients: one, unless there are fewer tiles than pairs of blocks or one
+// product's tiles are longer than an even share of all work.  A part is at least 16 stages (as long as
+// writing and reading its 256 KB of sums takes).
+void split(int64_t tokens, int64_t cols, int64_t hidden, int width, bool pieces, int32_t (&splits)[2]) {
+    const int64_t across = cdiv(hidden, width), row_tiles[2] = {cdiv(tokens, kTile), cdiv(cols, kTile)};
+    const int64_t steps[2] = {cdiv(cols, kDepth), cdiv(tokens, kDepth)};
+    const int64_t share = cdiv((row_tiles[0] * steps[0] + row_tiles[1] * steps[1]) * across, kPairs);
+    for (int i = 0; i < 2; i++) {
+        const int64_t most = cdiv(steps[i], share > 16 ? share : 16);
+        splits[i] = int32_t(most < 1 ? 1 : most);
+    }
+    if (pieces) splits[1] = 1;
+}
+
+// Columns of a tile of logits: the width for which the rounds of all pairs take least, counting 32 columns for
+// what a tile costs besides.
+int width_of(int64_t tokens, int64_t cols) {
+    int best = kTile;
+    int64_t least = INT64_MAX;
+    for (int w = kTile; w >= 128; w -= 32) {
+        const int64_t time = cdiv(cdiv(tokens, kTile) * cdiv(cols, w), kPairs) * (w + 32);
+        if (time < least) least = time, best = w;
+    }
+    return best;
+}
+
 struct Layout {
     int64_t packed;   // elements of a compacted row of hidden states or weights
     int64_t pitch;    // tokens, rounded up
     int64_t piece;    // columns of the vocabulary at a time (backward)
+    int32_t width;    // of the tiles of logits
+    int32_t grad_width;   // of the gradients' tiles
     int32_t tiles;    // column tiles (forward)
     int32_t join;     // blocks of the join
-    size_t count, ticket, unit, rows, column, shares, entropy, flags, hidden, weight, part, sums, row, dz, total;
+    int32_t chunk, row_blocks;   // of the list of live tokens
+    int32_t splits[2];
+    int64_t sums_pitch[2];
+    size_t count, ticket, rows, column, shares, entropy, flags, hidden, weight, part, sums, parts, dz, grad_sums[2], total;
 };
 
 // Pieces of the vocabulary: dz of a piece takes up to 256 MiB, or 8192 columns where that is more (the sums
@@ -384,8 +453,12 @@ Layout layout_of(const nest_head_desc *d, const void *weight, bool backward) {
     l.packed = align_up(d->hidden, 8);
     l.pitch = align_up(d->tokens > 0 ? d->tokens : 1, kTile);
     l.piece = piece_of(l.pitch, d->vocab);
-    l.tiles = int32_t((d->vocab + kTile - 1) / kTile);
-    l.join = d->tokens ? int32_t((d->tokens + kJoinRows - 1) / kJoinRows) : 1;
+    l.width = width_of(d->tokens, backward ? l.piece : d->vocab);
+    l.grad_width = d->hidden > kHalf ? kTile : kHalf;
+    l.tiles = int32_t(cdiv(d->vocab, l.width));
+    l.join = d->tokens ? int32_t(cdiv(d->tokens, kJoinRows)) : 1;
+    l.chunk = int32_t(align_up(d->tokens ? cdiv(d->tokens, kMostRowBlocks) : 1, d->tokens > 32 * kSMs ? 32 : 8));
+    l.row_blocks = d->tokens ? int32_t(cdiv(d->tokens, l.chunk)) : 1;
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t here = at;
@@ -394,7 +467,6 @@ Layout layout_of(const nest_head_desc *d, const void *weight, bool backward) {
     };
     l.count = take(4);
     l.ticket = take(4);
-    l.unit = take(4);
     l.rows = take(4 * d->tokens);
     const int64_t slots = d->tokens * (d->k ? d->k : 1);
     l.column = take(4 * slots);
@@ -409,9 +481,14 @@ Layout layout_of(const nest_head_desc *d, const void *weight, bool backward) {
         l.part = take(3 * 4 * int64_t(l.tiles) * l.pitch);
         l.sums = take(4 * l.join);
     } else {
-        l.row = take(2 * 4 * l.pitch);
+        const bool pieces = l.piece < d->vocab;
+        split(d->tokens, pieces ? l.piece : d->vocab, d->hidden, l.grad_width, pieces, l.splits);
+        l.sums_pitch[0] = l.pitch;
+        l.sums_pitch[1] = l.piece;
+        l.parts = take(4 * kMostRowBlocks);
         l.dz = take(2 * l.pitch * l.piece);
-        if (l.piece < d->vocab) l.sums = take(4 * l.pitch * d->hidden);
+        for (int i = 0; i < 2; i++)
+            if (l.splits[i] > 1 || (i == 0 && pieces)) l.grad_sums[i] = take(4 * l.splits[i] * d->hidden * l.sums_pitch[i]);
     }
     l.total = at;
     return l;
@@ -464,7 +541,7 @@ struct Call {
     template <typename T> T *at(size_t offset) const { return reinterpret_cast<T *>(ws + offset); }
 
     int start(const void *hidden, const void *w, const void *index, const void *teacher, const uint8_t *mask,
-              float *losses, float *lse, int32_t *live, void *grad) {
+              float *losses, float *lse, int32_t *live, void *grad, const float *grad_losses) {
         if (d->k) {
             TeacherArgs t = {};
             t.index = index;
@@ -490,18 +567,15 @@ struct Call {
             }
         }
         RowArgs r = {};
-        r.hidden = hidden;
-        r.row_stride = d->hidden_row;
-        r.col_stride = d->hidden_col;
+        r.hidden = Rows{static_cast<const uint16_t *>(hidden), d->hidden_row, d->hidden_col, d->hidden,
+                        at<uint16_t>(l.hidden), l.packed};
         r.tokens = d->tokens;
-        r.hidden_size = d->hidden;
-        r.packed = l.packed;
-        r.wide = (d->hidden_col == 1 || d->hidden == 1) && d->hidden_row % 8 == 0 && aligned_to(hidden, 16);
         r.labels = index;
         r.wide_labels = d->index_type == NEST_I64;
         r.vocab = d->vocab;
         r.flags = d->k ? at<uint8_t>(l.flags) : nullptr;
-        r.out = at<uint16_t>(l.hidden);
+        r.chunk = l.chunk;
+        r.blocks = l.row_blocks;
         r.rows = at<int32_t>(l.rows);
         r.count = at<int32_t>(l.count);
         r.column = d->k ? nullptr : at<int32_t>(l.column);
@@ -510,25 +584,22 @@ struct Call {
         r.lse = lse;
         r.live = live;
         r.grad = static_cast<uint16_t *>(grad);
-        const int64_t chunk = align_up((d->tokens + 511) / 512, 32);
-        r.chunk = int32_t(chunk < 32 ? 32 : chunk);
-        const int64_t blocks = (d->tokens + r.chunk - 1) / r.chunk;
-        if (const int rc = launch_kernel(rows_kernel, dim3(unsigned(blocks ? blocks : 1)), dim3(kRowThreads), 0, stream,
-                                         1, "head rows launch", r))
-            return rc;
+        r.wide_grad = d->hidden % 8 == 0 && aligned_to(grad, 16);
+        r.grad_losses = grad_losses;
+        r.parts = grad_losses ? at<float>(l.parts) : nullptr;
         weight = w;
         weight_pitch = d->weight_row;
+        int64_t copiers = 0;
         if (!in_place(d, w)) {
             weight = ws + l.weight;
             weight_pitch = l.packed;
-            const int64_t most = (d->vocab + kRowThreads / 32 - 1) / (kRowThreads / 32);
-            if (const int rc = launch_kernel(pack_kernel, dim3(unsigned(most < 8 * kSMs ? most : 8 * kSMs)),
-                                             dim3(kRowThreads), 0, stream, 1, "head weights launch",
-                                             static_cast<const uint16_t *>(w), d->weight_row, d->weight_col, d->vocab,
-                                             d->hidden, at<uint16_t>(l.weight), l.packed))
-                return rc;
+            r.weight = Rows{static_cast<const uint16_t *>(w), d->weight_row, d->weight_col, d->hidden,
+                            at<uint16_t>(l.weight), l.packed};
+            copiers = cdiv(d->vocab, kRowThreads / 32);
+            if (copiers > 8 * kSMs) copiers = 8 * kSMs;
         }
-        return NEST_OK;
+        return launch_kernel(rows_kernel, dim3(unsigned(l.row_blocks + copiers)), dim3(kRowThreads), 0, stream, 1,
+                             "head rows launch", r);
     }
 
     GemmArgs products() const {
@@ -536,6 +607,9 @@ struct Call {
         g.live = at<int32_t>(l.count);
         g.rows = at<int32_t>(l.rows);
         g.pitch = l.pitch;
+        g.depth = int32_t(d->hidden);
+        g.width = l.width;
+        g.how[0] = instruction(d->dtype, true, true, l.width);
         g.ids = at<int32_t>(l.column);
         g.shares = d->k ? at<float>(l.shares) : nullptr;
         g.k = d->k ? d->k : 1;
@@ -543,12 +617,10 @@ struct Call {
         return g;
     }
 
-    // `rows`: at most
-    int multiply(Product p, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, int64_t rows) const {
-        const int64_t tiles = (rows + kTile - 1) / kTile * ((g.cols + kTile - 1) / kTile);
-        const int pairs = int(tiles < kSMs / 2 ? tiles : kSMs / 2);
-        return d->dtype == NEST_BF16 ? launch_gemm_bf16(p, a, b, g, pairs, stream)
-                                     : launch_gemm_f16(p, a, b, g, pairs, stream);
+    int multiply(Product p, const Maps &maps, const GemmArgs &g, int64_t tiles) const {
+        const int pairs = int(tiles < kPairs ? tiles : kPairs);
+        return d->dtype == NEST_BF16 ? launch_gemm_bf16(p, maps, g, pairs, stream)
+                                     : launch_gemm_f16(p, maps, g, pairs, stream);
     }
 };
 
@@ -588,20 +660,20 @@ int nest_head_loss(const nest_head_desc *d, const void *hidden, const void *weig
     if (!loss || !live || (d->tokens && (!losses || !lse))) return NEST_E_INVALID;
     Call c = {d, layout_of(d, weight, false), static_cast<unsigned char *>(workspace), stream};
     if (!workspace || ws_bytes < c.l.total || !aligned_to(workspace, 256)) return NEST_E_WORKSPACE;
-    if (const int rc = c.start(hidden, weight, index, teacher, mask, losses, lse, live, nullptr)) return rc;
+    if (const int rc = c.start(hidden, weight, index, teacher, mask, losses, lse, live, nullptr, nullptr))
+        return rc;
     GemmArgs g = c.products();
     g.cols = int32_t(d->vocab);
-    g.depth = int32_t(d->hidden);
     const int64_t part = int64_t(c.l.tiles) * c.l.pitch;
     g.part_max = c.at<float>(c.l.part);
     g.part_sum = g.part_max + part;
     g.part_hit = g.part_sum + part;
     if (d->tokens) {
-        CUtensorMap a, b;
-        if (const int rc = encode(&a, d->dtype, c.at<void>(c.l.hidden), d->hidden, c.l.pitch, c.l.packed, kHalf))
-            return rc;
-        if (const int rc = encode(&b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, kHalf)) return rc;
-        if (const int rc = c.multiply(kLoss, a, b, g, d->tokens)) return rc;
+        Maps maps = {};
+        int rc = encode(&maps.a, d->dtype, c.at<void>(c.l.hidden), d->hidden, c.l.pitch, c.l.packed, kHalf);
+        if (!rc) rc = encode(&maps.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, c.l.width / 2);
+        if (!rc) rc = c.multiply(kLoss, maps, g, cdiv(d->tokens, kTile) * c.l.tiles);
+        if (rc) return rc;
     }
     JoinArgs j = {};
     j.count = g.live;
@@ -635,66 +707,73 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     Call c = {d, layout_of(d, weight, true), static_cast<unsigned char *>(workspace), stream};
     const Layout &l = c.l;
     if (!workspace || ws_bytes < l.total || !aligned_to(workspace, 256)) return NEST_E_WORKSPACE;
-    if (const int rc = c.start(hidden, weight, index, teacher, mask, nullptr, nullptr, nullptr, grad_hidden)) return rc;
-    ScaleArgs s = {};
-    s.count = c.at<int32_t>(l.count);
-    s.rows = c.at<int32_t>(l.rows);
-    s.lse = lse;
-    s.grad_loss = grad_loss;
-    s.grad_losses = grad_losses;
-    s.heat = d->temperature;
-    s.lift = d->dtype == NEST_F16 ? 32768.0f : 1.0f;
-    s.row_lse = c.at<float>(l.row);
-    s.row_scale = s.row_lse + l.pitch;
-    s.unit = c.at<float>(l.unit);
-    s.hidden = c.at<uint16_t>(l.hidden);
-    s.packed = l.packed;
-    if (const int rc = launch_kernel(scale_kernel, dim3(33), dim3(kScaleThreads), 0, stream, 1, "head scale launch", s))
+    if (const int rc =
+            c.start(hidden, weight, index, teacher, mask, nullptr, nullptr, nullptr, grad_hidden, grad_losses))
         return rc;
 
-    CUtensorMap hidden_rows, weight_rows, dz_rows, weight_cols, dz_cols, hidden_cols;
-    void *h = c.at<void>(l.hidden), *dz = c.at<void>(l.dz);
-    int rc = encode(&hidden_rows, d->dtype, h, d->hidden, l.pitch, l.packed, kHalf);
-    if (!rc) rc = encode(&weight_rows, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, kHalf);
-    if (!rc) rc = encode(&dz_rows, d->dtype, dz, l.piece, l.pitch, l.piece, kHalf);
-    if (!rc) rc = encode(&weight_cols, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, kDepth);
-    if (!rc) rc = encode(&dz_cols, d->dtype, dz, l.piece, l.pitch, l.piece, kDepth);
-    if (!rc) rc = encode(&hidden_cols, d->dtype, h, d->hidden, l.pitch, l.packed, kDepth);
+    void *h = c.at<void>(l.hidden);
+    uint16_t *dz = c.at<uint16_t>(l.dz);
+    Maps logits = {}, grads = {};
+    int rc = encode(&logits.a, d->dtype, h, d->hidden, l.pitch, l.packed, kHalf);
+    if (!rc) rc = encode(&logits.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, l.width / 2);
+    if (!rc) rc = encode(&grads.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, kDepth);
+    if (!rc) rc = encode(&grads.d, d->dtype, h, d->hidden, l.pitch, l.packed, kDepth);
     if (rc) return rc;
 
     GemmArgs g = c.products();
-    g.row_lse = s.row_lse;
-    g.row_scale = s.row_scale;
-    g.unit = s.unit;
-    for (int64_t first = 0; first < d->vocab; first += l.piece) {
-        const int64_t cols = d->vocab - first < l.piece ? d->vocab - first : l.piece;
-        GemmArgs p = g;
-        p.first_col = int32_t(first);
-        if (d->tokens) {
-            p.cols = int32_t(cols);
-            p.depth = int32_t(d->hidden);
-            p.out = dz;
-            p.out_pitch = l.piece;
-            p.wide = 1;
-            if (const int e = c.multiply(kDz, hidden_rows, weight_rows, p, d->tokens)) return e;
-            p.cols = int32_t(d->hidden);
-            p.depth = int32_t(cols);
-            p.out = grad_hidden;
-            p.out_pitch = d->hidden;
-            p.wide = d->hidden % 8 == 0 && aligned_to(grad_hidden, 16);
-            p.sums = c.at<float>(l.sums);
-            p.first = first == 0;
-            p.last = first + l.piece >= d->vocab;
-            if (const int e = c.multiply(kGradHidden, dz_rows, weight_cols, p, d->tokens)) return e;
-        }
-        p.m = int32_t(cols);
-        p.cols = int32_t(d->hidden);
-        p.out = static_cast<uint16_t *>(grad_weight) + first * d->hidden;
-        p.out_pitch = d->hidden;
-        p.wide = d->hidden % 8 == 0 && aligned_to(grad_weight, 16);
-        if (const int e = c.multiply(kGradWeight, dz_cols, hidden_cols, p, cols)) return e;
+    g.lse = lse;
+    g.by = Scale{grad_loss, grad_losses, c.at<float>(l.parts), l.row_blocks, d->temperature,
+                 d->dtype == NEST_F16 ? 32768.0f : 1.0f};
+    g.dz = dz;
+    g.dz_pitch = l.piece;
+    uint16_t *out[2] = {static_cast<uint16_t *>(grad_hidden), static_cast<uint16_t *>(grad_weight)};
+    for (int i = 0; i < 2; i++) {
+        g.wide[i] = d->hidden % 8 == 0 && aligned_to(out[i], 16);
+        g.splits[i] = l.splits[i];
+        g.sums[i] = l.grad_sums[i] ? c.at<float>(l.grad_sums[i]) : nullptr;
+        g.sums_pitch[i] = l.sums_pitch[i];
     }
-    return NEST_OK;
+    const int64_t across = cdiv(d->hidden, l.grad_width);
+    for (int64_t first = 0; first < d->vocab; first += l.piece) {
+        g.cols = int32_t(d->vocab - first < l.piece ? d->vocab - first : l.piece);
+        g.first_col = int32_t(first);
+        g.add = first > 0;
+        if (d->tokens) {
+            if ((rc = c.multiply(kDz, logits, g, cdiv(d->tokens, kTile) * cdiv(g.cols, l.width)))) return rc;
+            rc = encode(&grads.a, d->dtype, dz, g.cols, l.pitch, l.piece, kHalf);
+            if (!rc) rc = encode(&grads.c, d->dtype, dz, g.cols, l.pitch, l.piece, kDepth);
+            if (rc) return rc;
+        }
+        GemmArgs p = g;
+        p.width = l.grad_width;
+        p.how[0] = instruction(d->dtype, true, false, p.width);
+        p.how[1] = instruction(d->dtype, false, false, p.width);
+        p.out[0] = out[0];
+        p.out[1] = out[1] + first * d->hidden;
+        const int64_t tiles = (cdiv(d->tokens, kTile) * p.splits[0] + cdiv(p.cols, kTile) * p.splits[1]) * across;
+        if ((rc = c.multiply(kGrads, grads, p, tiles))) return rc;
+    }
+    if (!g.sums[0] && !g.sums[1]) return NEST_OK;
+    SumArgs s = {};
+    s.live = g.live;
+    s.rows = g.rows;
+    s.cols = g.depth;
+    s.by = g.by;
+    const int64_t wide = cdiv(d->hidden, kSumTile);
+    const int64_t blocks[2] = {g.sums[0] ? cdiv(d->tokens, kSumTile) * wide : 0,
+                               g.sums[1] ? cdiv(d->vocab, kSumTile) * wide : 0};
+    s.piece_rows = int32_t(d->vocab);
+    s.first_block = int32_t(blocks[0]);
+    for (int i = 0; i < 2; i++) {
+        s.splits[i] = g.splits[i];
+        s.sums[i] = g.sums[i];
+        s.pitch[i] = g.sums_pitch[i];
+        s.out[i] = out[i];
+    }
+    const dim3 grid(unsigned(blocks[0] + blocks[1]));
+    return d->dtype == NEST_BF16
+               ? launch_kernel(sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, 1, "head sums launch", s)
+               : launch_kernel(sum_kernel<__half>, grid, dim3(256), 0, stream, 1, "head sums launch", s);
 }
 
 }  // extern "C"

@@ -1,14 +1,14 @@
 // Matrix products of the output head (nest_head.h) on the tensor cores.
 //
-// One kernel for the four products, over tiles of 256 x 256 results made by a pair of thread blocks:
+// One kernel for the products, over tiles of up to 256 x 256 results made by a pair of thread blocks:
 // each of the two loads half of both operands' rows by TMA, one thread of the first issues tcgen05.mma
 // for both (cta_group::2, so that every operand byte is loaded once for the pair), and the results stay
-// in tensor memory until four warps per block reduce or round them.
+// in tensor memory until eight warps per block reduce or round them, while the next tile's products run.
 //
-//   loss         z = hidden weight^T    per row and tile: maximum, sum of exponentials, target logits
-//   dz           the same product       p - q, times the row's scale, in 16 bits
-//   grad hidden  dz weight              over a piece of the vocabulary
-//   grad weight  dz^T hidden            over the live tokens
+//   loss    z = hidden weight^T    per row and tile: maximum, sum of exponentials, target logits
+//   dz      the same product       p - q, times the row's factor, in 16 bits
+//   grads   dz weight and dz^T hidden over a piece of the vocabulary, in one launch: few long tiles of
+//           one and many short ones of the other fill each other's last round
 #pragma once
 
 #include <cuda.h>
@@ -21,45 +21,67 @@
 namespace nest {
 namespace head {
 
-constexpr int kTile = 256;        // rows and columns of results of a pair
+constexpr int kTile = 256;        // rows of results of a pair, and columns at most
 constexpr int kHalf = 128;        // rows of either operand that one block of the pair loads
 constexpr int kDepth = 64;        // of the summed index per stage: 128 bytes, the widest swizzle
 constexpr int kOperand = kHalf * kDepth * 2;   // bytes of one operand's half
 constexpr int kStage = 2 * kOperand;
 constexpr int kStages = 6;
-constexpr int kEpilogueWarps = 4;
+constexpr int kEpilogueWarps = 8;    // two for each quarter of the rows
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kStaging = 32 * 128;   // bytes: 32 rows of 64 results in 16 bits, per epilogue warp
 constexpr int kGroup = 8;            // row tiles that share a column tile's operand in L2
 constexpr int kNoColumn = 0x7fffffff;
+constexpr int kMostRowBlocks = 512;  // of the kernel that lists the live tokens
 
 struct Shared {   // after the stages and the staging
     uint64_t full[kStages], empty[kStages], done[2], free_[2], drain;
     uint32_t tmem;
 };
 constexpr size_t kSharedBytes = 1024 + size_t(kStages) * kStage + kEpilogueWarps * kStaging + sizeof(Shared);
+static_assert(kSharedBytes <= 232448, "shared memory of a block");
 
-enum Product { kLoss, kDz, kGradHidden, kGradWeight };
+enum Product { kLoss, kDz, kGrads };
+
+struct Maps {     // operands: loss and dz: hidden, weight; grads: dz, weight, dz again by columns, hidden
+    CUtensorMap a, b, c, d;
+};
+
+// What the gradients of the losses are scaled by.
+struct Scale {
+    const float *grad_loss;     // [1], NULL = 0
+    const float *grad_losses;   // [T], NULL = 0
+    const float *parts;         // with grad_losses: the largest finite size of each of `blocks` parts
+    int32_t blocks;
+    float heat;                 // h
+    float lift;                 // 2^15 in half precision
+};
 
 struct GemmArgs {
     const int32_t *live;      // n
     const int32_t *rows;      // [n] the live tokens
     int64_t pitch;            // tokens rounded up to a tile: rows of the compacted buffers
-    int32_t m, cols, depth;   // rows (grad weight), columns and summed length (not grad weight)
+    int32_t cols, depth;      // loss, dz: columns of the (piece of the) vocabulary, hidden size
     int32_t first_col;        // of the piece: where its columns start in the vocabulary
+    int32_t width;            // of a tile
+    uint32_t how[2];          // instruction descriptors: loss and dz or grad hidden; grad weight
     // targets, by token
     const int32_t *ids;       // [T][k] ascending, kNoColumn past the last
     const float *shares;      // [T][k], NULL = 1
     int32_t k;
     float scale;              // log2(e) / h
     float *part_max, *part_sum, *part_hit;   // loss: [column tile][pitch]
-    const float *row_lse, *row_scale;        // dz: [n], lse log2(e) and the row's factor
-    void *out;                // dz, or a gradient
-    int64_t out_pitch;        // elements
-    int32_t wide;             // rows of out are 16-byte aligned
-    float *sums;              // grad hidden: [column][pitch], over the pieces so far
-    int32_t first, last;      // piece
-    const float *unit;        // gradients: factor of the results
+    const float *lse;         // dz: [T]
+    Scale by;                 // dz, grads
+    uint16_t *dz;             // [pitch][dz_pitch]
+    int64_t dz_pitch;
+    // grads: hidden, weight
+    uint16_t *out[2];
+    int32_t wide[2];          // rows of out are 16-byte aligned
+    int32_t splits[2];        // parts of the summed index
+    float *sums[2];           // [split][column][row], where results are not final; else NULL
+    int64_t sums_pitch[2];
+    int32_t add;              // a later piece: sums of grad hidden go on
 };
 
 __device__ __forceinline__ uint32_t shared_address(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -147,11 +169,12 @@ __device__ __forceinline__ uint64_t descriptor(uint32_t address) {
 // Descriptor steps of 16 summed indices.
 template <bool ALONG> constexpr uint32_t kStep = ALONG ? 32 >> 4 : (16 * 128) >> 4;
 
-// Sums in 32 bits, the operands' type and direction, 256 x 256 results.
-template <typename T, bool A_ALONG, bool B_ALONG>
-constexpr uint32_t kInstruction = 1u << 4 | uint32_t(std::is_same<T, __nv_bfloat16>::value) << 7 |
-                                  uint32_t(std::is_same<T, __nv_bfloat16>::value) << 10 | uint32_t(!A_ALONG) << 15 |
-                                  uint32_t(!B_ALONG) << 16 | uint32_t(kTile >> 3) << 17 | uint32_t(kTile >> 4) << 24;
+// Instruction descriptor: sums in 32 bits, the operands' type and direction, 256 x width results.
+inline uint32_t instruction(int32_t dtype, bool a_along, bool b_along, int width) {
+    const uint32_t type = dtype == NEST_BF16;
+    return 1u << 4 | type << 7 | type << 10 | uint32_t(!a_along) << 15 | uint32_t(!b_along) << 16 |
+           uint32_t(width >> 3) << 17 | uint32_t(kTile >> 4) << 24;
+}
 
 __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t how, uint32_t add) {
     asm volatile(
@@ -202,16 +225,100 @@ template <> __device__ __forceinline__ uint32_t pack_two<__half>(float low, floa
     return reinterpret_cast<const uint32_t &>(v);
 }
 
-// The tiles in the order in which they are taken: groups of kGroup row tiles, column by column.
+// A tile of results and the stages of its summed index; kind 1: grad weight.
+struct Tile {
+    int kind, row, col, split, from, steps;
+};
+
+// One product's tiles in the order in which they are taken: for each part of the summed index, groups of
+// kGroup row tiles, column by column.
 struct Tiles {
-    int rows, cols;
-    __device__ __forceinline__ void at(int i, int &row, int &col) const {
-        const int per = kGroup * cols, g = i / per, left = i - g * per;
+    int rows, cols, splits, steps;
+    __device__ __forceinline__ int per() const { return (steps + splits - 1) / splits; }
+    __device__ __forceinline__ int count() const { return rows * cols * splits; }
+    __device__ __forceinline__ void at(int i, Tile &t) const {
+        t.split = i / (rows * cols);
+        i -= t.split * rows * cols;
+        const int group = kGroup * cols, g = i / group, left = i - g * group;
         const int high = min(kGroup, rows - g * kGroup);
-        col = left / high;
-        row = g * kGroup + left - col * high;
+        t.col = left / high;
+        t.row = g * kGroup + left - t.col * high;
+        t.from = t.split * per();
+        t.steps = max(0, min(per(), steps - t.from));
     }
 };
+
+// The tiles of one pair.  Loss, dz: every pairs-th.  Grads: the product with the longer tiles first, every
+// pairs-th of its tiles; pairs that get one less then take as many of the other product's tiles as make up for it,
+// and the rest goes to all pairs in turn.
+struct Work {
+    Tiles long_, short_;
+    int kind;                 // of the longer
+    int pair, pairs, i, extra, idle;
+
+    __device__ __forceinline__ void start(const Tiles &h, const Tiles &w, bool two) {
+        pair = int(blockIdx.x >> 1);
+        pairs = int(gridDim.x >> 1);
+        kind = two && w.per() > h.per();
+        long_ = kind ? w : h;
+        short_ = kind ? h : w;
+        i = pair;
+        const int over = long_.count() % pairs;
+        idle = over ? pairs - over : 0;      // pairs with one less: the last ones
+        extra = two && idle ? (long_.per() + short_.per() / 2) / max(1, short_.per()) : 0;
+        if (!two) short_.rows = 0;
+    }
+    // phases of i: [0, count) the longer; then, from `count` on, idle rounds and common rounds of the shorter
+    int phase = 0, j = 0;
+    __device__ __forceinline__ bool next(Tile &t) {
+        if (phase == 0) {
+            if (i < long_.count()) {
+                long_.at(i, t);
+                t.kind = kind;
+                i += pairs;
+                return true;
+            }
+            phase = 1;
+        }
+        if (phase == 1) {
+            const int mine = pair - (pairs - idle);
+            if (mine >= 0 && j < extra) {
+                const int at = mine + j++ * idle;
+                if (at < short_.count()) {
+                    short_.at(at, t);
+                    t.kind = !kind;
+                    return true;
+                }
+            }
+            phase = 2;
+            i = extra * idle + pair;
+        }
+        if (i >= short_.count()) return false;
+        short_.at(i, t);
+        t.kind = !kind;
+        i += pairs;
+        return true;
+    }
+};
+
+// Exponent e of the power of two that gradients are taken relative to: 2^e is above the size of every finite
+// factor, so that dz is below 1 (2^15 where it is lifted) and both scalings are exact.  By all lanes of a warp.
+__device__ __forceinline__ int scale_exponent(const Scale &s, float share) {
+    float top = 0.0f;
+    if (s.grad_losses) {
+        for (int b = threadIdx.x & 31; b < s.blocks; b += 32) top = fmaxf(top, s.parts[b]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    if (fabsf(share) < INFINITY) top += fabsf(share);
+    top = fminf(top * s.heat, 8e37f);
+    int e = 0;
+    if (top > 0.0f) frexpf(top, &e);
+    return max(-100, e);
+}
+__device__ __forceinline__ float share_of(const Scale &s, int n) {
+    return s.grad_loss && n ? *s.grad_loss / float(n) : 0.0f;
+}
 
 // A token's targets from a column on, in ascending order.
 struct Targets {
@@ -235,10 +342,23 @@ struct Targets {
     __device__ __forceinline__ void advance() { next = ++j < k ? id[j] : kNoColumn; }
 };
 
+// v[i] by five steps of halving: an index that the compiler does not see would move v to memory.
+__device__ __forceinline__ float pick(const float (&v)[32], int i) {
+    float t[16];
+#pragma unroll
+    for (int e = 0; e < 16; e++) t[e] = i & 16 ? v[e + 16] : v[e];
+#pragma unroll
+    for (int e = 0; e < 8; e++) t[e] = i & 8 ? t[e + 8] : t[e];
+#pragma unroll
+    for (int e = 0; e < 4; e++) t[e] = i & 4 ? t[e + 4] : t[e];
+#pragma unroll
+    for (int e = 0; e < 2; e++) t[e] = i & 2 ? t[e + 2] : t[e];
+    return i & 1 ? t[1] : t[0];
+}
+
 // 64 results of each of the warp's 32 rows, through shared memory so that a row's are written together.
 // `to`: where this lane's row goes, or NULL where nothing is written; `left`: columns that exist from here on.
-template <typename T>
-__device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigned char *staging, T *to, int left,
+__device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigned char *staging, uint16_t *to, int left,
                                            bool wide, int lane) {
     uint4 *mine = reinterpret_cast<uint4 *>(staging) + lane * 8;
 #pragma unroll
@@ -250,7 +370,7 @@ __device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigne
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int r = 4 * i + (lane >> 3);
-        T *p = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, row, r));
+        uint16_t *p = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, row, r));
         const uint4 v = reinterpret_cast<const uint4 *>(staging)[r * 8 + (unit ^ (r & 7))];
         const int rest = left - 8 * unit;
         if (p && rest > 0) {
@@ -259,10 +379,9 @@ __device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigne
                 *reinterpret_cast<uint4 *>(p) = v;
             } else {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                uint16_t *h = reinterpret_cast<uint16_t *>(p);
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    if (e < rest) h[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+                    if (e < rest) p[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
             }
         }
     }
@@ -271,9 +390,7 @@ __device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigne
 
 template <Product P, typename T>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, GemmArgs a) {
-    // operands whose rows in memory run along the summed index
-    constexpr bool kAAlong = P != kGradWeight, kBAlong = P == kLoss || P == kDz;
+    gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmArgs a) {
     extern __shared__ unsigned char raw[];
     unsigned char *base = raw + ((1024 - (shared_address(raw) & 1023)) & 1023);   // the swizzle's alignment
     unsigned char *staging = base + kStages * kStage;
@@ -308,36 +425,40 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
     const uint32_t tmem = sh.tmem;
     const int n = *a.live;
-    const int m = P == kGradWeight ? a.m : n;
-    const int steps = ((P == kGradWeight ? n : a.depth) + kDepth - 1) / kDepth;
-    const Tiles tiles = {(m + kTile - 1) / kTile, (a.cols + kTile - 1) / kTile};
-    const int count = tiles.rows * tiles.cols, pair = int(blockIdx.x >> 1), pairs = int(gridDim.x >> 1);
+    const int row_tiles = (n + kTile - 1) / kTile, col_tiles = ((P == kGrads ? a.depth : a.cols) + a.width - 1) / a.width;
+    Work work;
+    work.start(Tiles{row_tiles, col_tiles, P == kGrads ? a.splits[0] : 1,
+                     ((P == kGrads ? a.cols : a.depth) + kDepth - 1) / kDepth},
+               Tiles{(a.cols + kTile - 1) / kTile, col_tiles, a.splits[1], (n + kDepth - 1) / kDepth}, P == kGrads);
+    Tile t;
 
     if (warp == 0 && lane == 0) {
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int i = pair; ok && i < count; i += pairs) {
-            int row, col;
-            tiles.at(i, row, col);
-            const int y = row * kTile + int(half) * kHalf, x = col * kTile + int(half) * kHalf;
-            for (int kb = 0; kb < steps; kb++) {
+        const int width = a.width / 2;     // columns that this block loads
+        const uint32_t bytes = 2 * (kOperand + uint32_t(width) * kDepth * 2);
+        while (ok && work.next(t)) {
+            const int y = t.row * kTile + int(half) * kHalf, x = t.col * a.width + int(half) * width;
+            for (int kb = 0; kb < t.steps; kb++) {
                 ok = barrier_wait(&sh.empty[s], phase ^ 1);
                 if (!ok) break;
                 const uint32_t to = shared_address(base + s * kStage), bar = in_first(shared_address(&sh.full[s]));
-                if (half == 0) barrier_expect(&sh.full[s], 2 * kStage);
-                if constexpr (kAAlong) {
-                    load_box(&map_a, to, bar, kb * kDepth, y);
+                const int k0 = (t.from + kb) * kDepth;
+                if (half == 0) barrier_expect(&sh.full[s], bytes);
+                if constexpr (P != kGrads) {
+                    load_box(&maps.a, to, bar, k0, y);
+                    load_box(&maps.b, to + kOperand, bar, k0, a.first_col + x);
                 } else {
-                    load_box(&map_a, to, bar, y, kb * kDepth);
-                    load_box(&map_a, to + kOperand / 2, bar, y + 64, kb * kDepth);
-                }
-                if constexpr (kBAlong) {
-                    load_box(&map_b, to + kOperand, bar, kb * kDepth, a.first_col + x);
-                } else {   // grad hidden: the piece's rows of the weights; grad weight: tokens
-                    const int r = (P == kGradHidden ? a.first_col : 0) + kb * kDepth;
-                    load_box(&map_b, to + kOperand, bar, x, r);
-                    load_box(&map_b, to + kOperand + kOperand / 2, bar, x + 64, r);
+                    if (t.kind == 0) {
+                        load_box(&maps.a, to, bar, k0, y);
+                    } else {
+                        load_box(&maps.c, to, bar, y, k0);
+                        load_box(&maps.c, to + kOperand / 2, bar, y + 64, k0);
+                    }
+                    const CUtensorMap *map = t.kind ? &maps.d : &maps.b;
+                    const int r = k0 + (t.kind ? 0 : a.first_col);
+                    for (int c = 0; c < width; c += 64) load_box(map, to + kOperand + c * kDepth * 2, bar, x + c, r);
                 }
                 if (++s == kStages) s = 0, phase ^= 1;
             }
@@ -349,24 +470,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             while (nanoseconds() - start < 10000000) __nanosleep(1000);
         }
     } else if (warp == 1 && lane == 0 && half == 0) {
-        constexpr uint32_t how = kInstruction<T, kAAlong, kBAlong>;
         int s = 0, use = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int i = pair; ok && i < count && steps; i += pairs, use++) {
+        while (ok && work.next(t)) {
+            if (!t.steps) continue;
             const int acc = use & 1;
             ok = barrier_wait(&sh.free_[acc], ((use >> 1) & 1) ^ 1);
+            use++;
             if (!ok) break;
             fence_after();
-            for (int kb = 0; kb < steps; kb++) {
+            for (int kb = 0; kb < t.steps; kb++) {
                 ok = barrier_wait(&sh.full[s], phase);
                 if (!ok) break;
                 fence_after();
                 const uint32_t at = shared_address(base + s * kStage);
-                const uint64_t da = descriptor<kAAlong>(at), db = descriptor<kBAlong>(at + kOperand);
+                // operands whose rows in memory run along the summed index: both; dz; none
+                auto stage = [&](auto a_along, auto b_along, uint32_t how) {
+                    constexpr bool kA = decltype(a_along)::value, kB = decltype(b_along)::value;
+                    const uint64_t da = descriptor<kA>(at), db = descriptor<kB>(at + kOperand);
 #pragma unroll
-                for (int q = 0; q < kDepth / 16; q++)
-                    multiply(tmem + acc * kTile, da + q * kStep<kAAlong>, db + q * kStep<kBAlong>, how, kb | q);
+                    for (int q = 0; q < kDepth / 16; q++)
+                        multiply(tmem + acc * kTile, da + q * kStep<kA>, db + q * kStep<kB>, how, kb | q);
+                };
+                if constexpr (P != kGrads) stage(std::true_type{}, std::true_type{}, a.how[0]);
+                else if (t.kind == 0) stage(std::true_type{}, std::false_type{}, a.how[0]);
+                else stage(std::false_type{}, std::false_type{}, a.how[1]);
                 commit(&sh.empty[s]);
                 if (++s == kStages) s = 0, phase ^= 1;
             }
@@ -378,56 +507,64 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 2) {
         const int quarter = warp & 3;   // the lanes of tensor memory that this warp may read
-        unsigned char *mine = staging + quarter * kStaging;
+        const int side = (warp - 2) >> 2;   // of the two warps of a quarter: every second chunk of columns each
+        unsigned char *mine = staging + (warp - 2) * kStaging;
         const int local = int(half) * kHalf + quarter * 32 + lane;
-        const float unit = P == kGradHidden || P == kGradWeight ? *a.unit : 1.0f;
         const float nan = __int_as_float(0x7fc00000);
+        float share = 0.0f, over = 1.0f, unit = 1.0f;
+        if constexpr (P != kLoss) {
+            share = share_of(a.by, n);
+            const int e = scale_exponent(a.by, share);
+            over = ldexpf(a.by.lift, -e) * a.by.heat;
+            unit = ldexpf(1.0f / a.by.lift, e);
+        }
         bool ok = true;
         int use = 0;
-        for (int i = pair; i < count; i += pairs, use++) {
-            int row, col;
-            tiles.at(i, row, col);
-            const int acc = use & 1, r = row * kTile + local, c0 = col * kTile;
-            const bool there = r < m;
+        while (work.next(t)) {
+            const int acc = use & 1, r = t.row * kTile + local, c0 = t.col * a.width;
+            const bool there = r < (t.kind ? a.cols : n);
             const uint32_t from = tmem + acc * kTile + (uint32_t(quarter * 32) << 16);
             int token = -1;
-            if constexpr (P != kGradWeight) token = there ? a.rows[r] : -1;
+            if (t.kind == 0 && there) token = a.rows[r];
             Targets hits;
             float lse = 0.0f, factor = 0.0f;
-            if constexpr (P == kLoss) hits.start(a, token, c0);
+            if constexpr (P != kGrads) hits.start(a, token, a.first_col + c0);
             if constexpr (P == kDz) {
-                hits.start(a, token, a.first_col + c0);
-                if (there) lse = a.row_lse[r], factor = a.row_scale[r];
+                if (there) {
+                    lse = a.lse[token] * 1.4426950408889634f;
+                    factor = (share + (a.by.grad_losses ? a.by.grad_losses[token] : 0.0f)) * over;
+                }
             }
-            if (steps) ok = ok && barrier_wait(&sh.done[acc], (use >> 1) & 1);
+            if (t.steps) ok = ok && barrier_wait(&sh.done[acc], (use >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
 
             if constexpr (P == kLoss) {
                 float top = -INFINITY, sum = 0.0f, hit = 0.0f;
-                const int chunks = min(kTile, a.cols - c0 + 31) / 32;
+                const int chunks = min(a.width, a.cols - c0 + 31) / 32;
 #pragma unroll 1
-                for (int c = 0; c < chunks; c++) {
+                for (int c = side; c < chunks; c += 2) {
                     float v[32];
                     read_columns(v, from + c * 32);
-                    reads_wait();
                     const int at = c0 + c * 32;
-                    while (hits.next < at + 32) {
-                        float z = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 32; e++) z = e == hits.next - at ? v[e] : z;
-                        hit = fmaf(hits.weight(), z, hit);
-                        hits.advance();
+                    const bool some = __any_sync(0xffffffffu, hits.next < at + 32);
+                    reads_wait();
+                    if (some) {
+                        while (hits.next < at + 32) {
+                            // the other warp's chunks lie between
+                            if (hits.next >= at) hit = fmaf(hits.weight(), pick(v, hits.next - at), hit);
+                            hits.advance();
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     if (at + 32 > a.cols) {
 #pragma unroll
                         for (int e = 0; e < 32; e++) v[e] = at + e < a.cols ? v[e] : -INFINITY;
                     }
-                    float t[4] = {top, top, top, top};
+                    float m[4] = {top, top, top, top};
 #pragma unroll
-                    for (int e = 0; e < 32; e++) t[e & 3] = fmaxf(t[e & 3], v[e]);
-                    const float high = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                    for (int e = 0; e < 32; e++) m[e & 3] = fmaxf(m[e & 3], v[e]);
+                    const float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                     const float off = high * a.scale;
                     float u[4] = {sum * exp2_fast(fmaf(top, a.scale, -off)), 0.0f, 0.0f, 0.0f};
                     if (top == -INFINITY) u[0] = 0.0f;   // nothing yet
@@ -438,87 +575,98 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0 && steps) arrive_at_first(&sh.free_[acc]);
-                if (there) {
-                    const int64_t at = int64_t(col) * a.pitch + r;
+                if (lane == 0) arrive_at_first(&sh.free_[acc]);
+                // what the second warp of a quarter found, of this tile and the next (nothing else is staged)
+                float(*other)[kHalf] = reinterpret_cast<float(*)[kHalf]>(staging) + 3 * acc;
+                const int place = quarter * 32 + lane;
+                if (side) other[0][place] = top, other[1][place] = sum, other[2][place] = hit;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                if (!side && there) {
+                    const float far = other[0][place], both = fmaxf(top, far);
+                    if (far > -INFINITY || other[1][place] != 0.0f) {   // it had a chunk
+                        sum = sum * (top == both ? 1.0f : exp2_fast((top - both) * a.scale)) +
+                              other[1][place] * (far == both ? 1.0f : exp2_fast((far - both) * a.scale));
+                        top = both;
+                        hit += other[2][place];
+                    }
+                    const int64_t at = int64_t(t.col) * a.pitch + r;
                     a.part_max[at] = top;
                     a.part_sum[at] = ok ? sum : nan;
                     a.part_hit[at] = hit;
                 }
             } else {
-                T *to = nullptr;
-                if constexpr (P == kDz) to = static_cast<T *>(a.out) + int64_t(r) * a.out_pitch;
-                if constexpr (P == kGradWeight)
-                    if (there) to = static_cast<T *>(a.out) + int64_t(r) * a.out_pitch;
-                if constexpr (P == kGradHidden)
-                    if (there) to = static_cast<T *>(a.out) + int64_t(token) * a.out_pitch;
-                const int chunks = P == kDz ? kTile / 64 : min(kTile, a.cols - c0 + 63) / 64;
+                const int columns = P == kDz ? a.cols : a.depth;
+                const int chunks = (min(a.width, columns - c0) + 63) / 64;
+                float *sums = P == kGrads ? a.sums[t.kind] : nullptr;
+                uint16_t *to = nullptr;
+                if constexpr (P == kDz) to = a.dz + int64_t(r) * a.dz_pitch;   // rows past n too
+                if (P == kGrads && there) to = a.out[t.kind] + int64_t(t.kind ? r : token) * a.depth;
+                if (P == kGrads && sums) sums += int64_t(t.split) * a.depth * a.sums_pitch[t.kind] + r;
 #pragma unroll 1
-                for (int c = 0; c < chunks; c++) {
-                    float v[2][32];
-                    if (steps) {
-                        read_columns(v[0], from + c * 64);
-                        read_columns(v[1], from + c * 64 + 32);
-                        reads_wait();
-                    }
+                for (int c = side; c < chunks; c += 2) {
                     const int at = c0 + c * 64;
-                    if (!ok || !steps) {
-#pragma unroll
-                        for (int e = 0; e < 64; e++) v[e >> 5][e & 31] = ok ? 0.0f : nan;
-                    }
-                    if constexpr (P == kDz) {
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int here = at + 32 * h, column = a.first_col + here;
-#pragma unroll
-                            for (int e = 0; e < 32; e++) v[h][e] = exp2_fast(fmaf(v[h][e], a.scale, -lse));
-                            while (hits.next < column + 32) {
-                                const float q = hits.weight();
-#pragma unroll
-                                for (int e = 0; e < 32; e++) v[h][e] -= e == hits.next - column ? q : 0.0f;
-                                hits.advance();
-                            }
-                            __syncwarp();
-                            // rows past the last and columns past the vocabulary enter later sums: zeros
-                            if (!there || here + 32 > a.cols) {
-#pragma unroll
-                                for (int e = 0; e < 32; e++)
-                                    v[h][e] = there && here + e < a.cols ? v[h][e] * factor : 0.0f;
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; e++) v[h][e] *= factor;
-                            }
-                        }
-                    }
-                    if constexpr (P == kGradHidden) {
-                        if (!a.first && there) {
-#pragma unroll
-                            for (int e = 0; e < 64; e++)
-                                if (at + e < a.cols) v[e >> 5][e & 31] += a.sums[int64_t(at + e) * a.pitch + r];
-                        }
-                        if (!a.last) {
-                            if (there) {
-#pragma unroll
-                                for (int e = 0; e < 64; e++)
-                                    if (at + e < a.cols) a.sums[int64_t(at + e) * a.pitch + r] = v[e >> 5][e & 31];
-                            }
-                            __syncwarp();
-                            continue;
-                        }
-                    }
                     uint32_t packed[32];
 #pragma unroll
-                    for (int e = 0; e < 32; e++) {
-                        float low = v[e >> 4][(2 * e) & 31], high = v[e >> 4][(2 * e + 1) & 31];
-                        if constexpr (P != kDz) low *= unit, high *= unit;
-                        packed[e] = pack_two<T>(low, high);
+                    for (int h = 0; h < 2; h++) {
+                        const int here = at + 32 * h;
+                        float v[32];
+                        if (t.steps) {
+                            read_columns(v, from + c * 64 + 32 * h);
+                            reads_wait();
+                        }
+                        if (!ok || !t.steps) {
+#pragma unroll
+                            for (int e = 0; e < 32; e++) v[e] = ok ? 0.0f : nan;
+                        }
+                        if constexpr (P == kDz) {
+                            const int column = a.first_col + here;
+#pragma unroll
+                            for (int e = 0; e < 32; e++) v[e] = exp2_fast(fmaf(v[e], a.scale, -lse));
+                            if (__any_sync(0xffffffffu, hits.next < column + 32)) {
+                                while (hits.next < column + 32) {
+                                    const float q = hits.weight();
+                                    const int d = hits.next - column;   // below 0: the other warp's
+#pragma unroll
+                                    for (int e = 0; e < 32; e++) v[e] -= e == d ? q : 0.0f;
+                                    hits.advance();
+                                }
+                                __syncwarp();
+                            }
+                            // rows past the last enter later sums: zeros
+#pragma unroll
+                            for (int e = 0; e < 32; e++) v[e] = there ? v[e] * factor : 0.0f;
+                        } else {
+                            if (sums) {
+                                if (there) {
+                                    const int64_t pitch = a.sums_pitch[t.kind];
+                                    if (a.add && t.kind == 0) {
+#pragma unroll
+                                        for (int e = 0; e < 32; e++)
+                                            if (here + e < columns) v[e] += sums[int64_t(here + e) * pitch];
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 32; e++)
+                                        if (here + e < columns) sums[int64_t(here + e) * pitch] = v[e];
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e++) v[e] *= unit;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e++) packed[16 * h + e] = pack_two<T>(v[2 * e], v[2 * e + 1]);
                     }
-                    write_rows<T>(packed, mine, to ? to + at : nullptr, P == kDz ? kTile : a.cols - at, a.wide, lane);
+                    if (P == kDz || !sums)
+                        write_rows(packed, mine, to ? to + at : nullptr, min(a.width - c * 64, columns - at),
+                                   P == kDz || a.wide[t.kind], lane);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0 && steps) arrive_at_first(&sh.free_[acc]);
+                if (t.steps) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at_first(&sh.free_[acc]);
+                }
             }
+            if (t.steps) use++;
         }
     }
 
@@ -532,25 +680,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // The products' launchers, one translation unit for each type.
-int launch_gemm_bf16(Product p, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &args, int pairs,
-                     void *stream);
-int launch_gemm_f16(Product p, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &args, int pairs,
-                    void *stream);
+int launch_gemm_bf16(Product p, const Maps &maps, const GemmArgs &args, int pairs, void *stream);
+int launch_gemm_f16(Product p, const Maps &maps, const GemmArgs &args, int pairs, void *stream);
 
 template <typename T>
-int launch_gemm(Product p, const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &args, int pairs,
-                void *stream) {
+int launch_gemm(Product p, const Maps &maps, const GemmArgs &args, int pairs, void *stream) {
     auto go = [&](auto product, const char *what) {
         constexpr Product P = decltype(product)::value;
         if (const int rc = allow<gemm_kernel<P, T>>(kSharedBytes, what)) return rc;
-        return launch_kernel(gemm_kernel<P, T>, dim3(2 * pairs), dim3(kThreads), kSharedBytes, stream, 1, what, ma, mb,
+        return launch_kernel(gemm_kernel<P, T>, dim3(2 * pairs), dim3(kThreads), kSharedBytes, stream, 1, what, maps,
                              args);
     };
     switch (p) {
         case kLoss: return go(std::integral_constant<Product, kLoss>{}, "head loss launch");
         case kDz: return go(std::integral_constant<Product, kDz>{}, "head dz launch");
-        case kGradHidden: return go(std::integral_constant<Product, kGradHidden>{}, "head grad hidden launch");
-        default: return go(std::integral_constant<Product, kGradWeight>{}, "head grad weight launch");
+        default: return go(std::integral_constant<Product, kGrads>{}, "head gradients launch");
     }
 }
 

@@ -3,9 +3,8 @@
 
 namespace nest {
 namespace head {
-int launch_gemm_bf16(Product p, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &args, int pairs,
-                     void *stream) {
-    return launch_gemm<__nv_bfloat16>(p, a, b, args, pairs, stream);
+int launch_gemm_bf16(Product p, const Maps &maps, const GemmArgs &args, int pairs, void *stream) {
+    return launch_gemm<__nv_bfloat16>(p, maps, args, pairs, stream);
 }
 }  // namespace head
 }  // namespace nest

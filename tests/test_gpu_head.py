@@ -53,6 +53,9 @@ def backward(x, r, dl=None, dls=None, **kw):
 
 def near(got, want, off, what):
     bad = ~((got.double() - want).abs() <= off)
+    # beyond the largest number by half a step, rounding gives infinity: 65504 + 16 in fp16
+    big = torch.finfo(got.dtype).max * (1 + torch.finfo(got.dtype).eps / 4)
+    bad &= ~((got.double() == want.sign() * INF) & (want.abs() + off >= big))
     assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist(), got[bad][:4], want[bad][:4], off[bad][:4])
 
 
@@ -233,7 +236,7 @@ def test_scales_of_the_gradient(scale):
         x = made(150, 400, 64, dtype)
         r = forward(x)
         dl = torch.tensor(scale, device="cuda")
-        dls = torch.exp(torch.randn(150, device="cuda") * 3) * scale / 150 * 0.01
+        dls = torch.exp(torch.randn(150, device="cuda", generator=torch.Generator("cuda").manual_seed(7)) * 3) * scale / 150 * 0.01
         check(x, r, dl, dls, backward(x, r, dl, dls))
         assert not backward(x, r)[1].any()      # no gradient given: zeros
 
