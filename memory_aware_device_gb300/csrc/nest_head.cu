@@ -50,37 +50,54 @@ __device__ __forceinline__ bool is_live(const RowArgs &a, int64_t t) {
     return a.flags ? a.flags[t] != 0 : label_of(a, t) >= 0;
 }
 
-// One row by a warp.  Rows off alignment are read from the aligned addresses around them and shifted: 16
-// bytes per lane whatever the offset.  (No 16 bytes are read of which the row has none.)
-__device__ __forceinline__ void copy_row(const Rows &x, int64_t source, int64_t target, int lane) {
+constexpr int kSegment = 1024;   // numbers of a row that a warp copies at a time: four loads of 16 bytes per lane
+
+// Numbers [begin, begin + kSegment) of a row by a warp.  Rows off alignment are read from the aligned addresses
+// around them and shifted: 16 bytes per lane whatever the offset.  (No 16 bytes are read of which the row has
+// none.)
+__device__ __forceinline__ void copy_segment(const Rows &x, int64_t source, int64_t target, int begin, int lane) {
     const uint16_t *from = x.from + source * x.row_stride;
     uint16_t *to = x.to + target * x.pitch;
-    if (x.col_stride != 1 && x.width != 1) {
+    const int width = int(x.width), end = min(begin + kSegment, width);
+    if (x.col_stride != 1 && width != 1) {
 #pragma unroll 8
-        for (int64_t d = lane; d < x.width; d += 32) to[d] = from[d * x.col_stride];
+        for (int d = begin + lane; d < end; d += 32) to[d] = from[d * x.col_stride];
         return;
     }
     const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(from)) & 15;
     const uint4 *base = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(from) - shift);
-    const int64_t units = (x.width + 7) / 8, last = (int64_t(shift) + 2 * x.width - 1) >> 4;
+    const int last = (int(shift) + 2 * width - 1) >> 4;   // the last aligned address
     uint4 *out = reinterpret_cast<uint4 *>(to);
+    const int u0 = begin / 8 + lane, units = (end + 7) / 8;
+    constexpr int kPer = kSegment / 8 / 32;
     if (!shift) {
-#pragma unroll 4
-        for (int64_t u = lane; u < units; u += 32) out[u] = base[u];
+        uint4 v[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (u0 + 32 * i < units) v[i] = base[u0 + 32 * i];
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (u0 + 32 * i < units) out[u0 + 32 * i] = v[i];
         return;
     }
     const bool two = shift & 8, one = shift & 4, part = shift & 2;
-#pragma unroll 4
-    for (int64_t u = lane; u < units; u += 32) {
-        const uint4 p = base[u], q = u < last ? base[u + 1] : make_uint4(0, 0, 0, 0);
-        uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+    uint4 p[kPer], q[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        const int u = u0 + 32 * i;
+        p[i] = u < units ? base[u] : make_uint4(0, 0, 0, 0);
+        q[i] = u < units && u < last ? base[u + 1] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        uint32_t w[8] = {p[i].x, p[i].y, p[i].z, p[i].w, q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
         for (int e = 0; e < 6; e++) w[e] = two ? w[e + 2] : w[e];
 #pragma unroll
         for (int e = 0; e < 5; e++) w[e] = one ? w[e + 1] : w[e];
 #pragma unroll
         for (int e = 0; e < 4; e++) w[e] = part ? __funnelshift_r(w[e], w[e + 1], 16) : w[e];
-        out[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (u0 + 32 * i < units) out[u0 + 32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -106,7 +123,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = int(blockIdx.x);
     if (block >= a.blocks) {
         const int64_t warps = int64_t(gridDim.x - a.blocks) * kWarps;
-        for (int64_t r = int64_t(block - a.blocks) * kWarps + warp; r < a.vocab; r += warps) copy_row(a.weight, r, r, lane);
+        for (int64_t r = int64_t(block - a.blocks) * kWarps + warp; r < a.vocab; r += warps)
+            for (int c = 0; c < a.weight.width; c += kSegment) copy_segment(a.weight, r, r, c, lane);
         return;
     }
     const int64_t first = int64_t(block) * a.chunk, end = min(first + a.chunk, a.tokens);
@@ -127,13 +145,13 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         if (a.live) *a.live = all;
         if (a.ticket) *a.ticket = 0;
     }
-    // rows from the last token to the end of its stage
-    for (int64_t r = all + block * kWarps + warp; r < (all + kDepth - 1) / kDepth * kDepth; r += a.blocks * kWarps)
+    // rows from the last token to the end of its stage, which the weights' gradient reads
+    for (int64_t r = all + block * kWarps + warp; a.grad && r < (all + kDepth - 1) / kDepth * kDepth; r += a.blocks * kWarps)
         clear_row(a.hidden.to + r * a.hidden.pitch, a.hidden.pitch, true, lane);
     float top = 0.0f;
     int at = before;
     for (int64_t t0 = first; t0 < end; t0 += 32) {
-        // every warp finds the same 32 tokens' places and copies every eighth of them
+        // every warp finds the same 32 tokens' places; their rows' segments go to the warps in turn
         const int64_t t = t0 + lane;
         const bool live = t < end && is_live(a, t);
         const uint32_t set = __ballot_sync(0xffffffffu, live);
@@ -146,9 +164,14 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
                 if (g < INFINITY) top = fmaxf(top, g);
             }
         }
-        for (int i = warp; i < 32 && t0 + i < end; i += kWarps) {
-            if (set >> i & 1) copy_row(a.hidden, t0 + i, at + __popc(set & ((1u << i) - 1)), lane);
-            else if (a.grad) clear_row(a.grad + (t0 + i) * a.hidden.width, a.hidden.width, a.wide_grad, lane);
+        const int segments = (int(a.hidden.width) + kSegment - 1) / kSegment, here = int(min(int64_t(32), end - t0));
+        for (int i = warp; i < here * segments; i += kWarps) {
+            const int row = i / segments, c = (i - row * segments) * kSegment;
+            if (set >> row & 1)
+                copy_segment(a.hidden, t0 + row, at + __popc(set & ((1u << row) - 1)), c, lane);
+            else if (a.grad)
+                clear_row(a.grad + (t0 + row) * a.hidden.width + c, min(int64_t(kSegment), a.hidden.width - c), a.wide_grad,
+                          lane);
         }
         at += __popc(set);
     }
@@ -258,73 +281,85 @@ struct JoinArgs {
 
 constexpr int kJoinRows = 32, kJoinParts = 16;
 
-// Joins the tiles' maxima and sums: 32 rows a block, 16 threads to a row; the last block adds the rows'
-// losses in the blocks' order.
+// Joins the tiles' maxima and sums: 32 rows a block, 16 threads to a row, once over the maxima and once over
+// the sums, so that no step waits for the one before; the last block adds the rows' losses in the blocks' order.
 __global__ void __launch_bounds__(kJoinRows *kJoinParts) join_kernel(JoinArgs a) {
-    __shared__ float sh_max[kJoinParts][kJoinRows], sh_sum[kJoinParts][kJoinRows], sh_hit[kJoinParts][kJoinRows];
-    __shared__ double sh_all[kJoinParts];
+    __shared__ float sh_max[kJoinParts][kJoinRows + 1], sh_sum[kJoinParts][kJoinRows + 1],
+        sh_hit[kJoinParts][kJoinRows + 1];
+    __shared__ float sh_all[kJoinParts];
     __shared__ bool sh_last;
     pdl_wait();
     pdl_trigger();
     const int n = *a.count, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const int64_t r = int64_t(blockIdx.x) * kJoinRows + lane;
-    float top = -INFINITY, sum = 0.0f, hit = 0.0f;
+    const int64_t first = int64_t(blockIdx.x) * kJoinRows, r = first + lane;
+    float top = -INFINITY;
     if (r < n) {
-#pragma unroll 4
-        for (int t = part; t < a.tiles; t += kJoinParts) {
-            const int64_t at = int64_t(t) * a.pitch + r;
-            const float high = a.part_max[at], s = a.part_sum[at];
-            const float both = fmaxf(top, high);
-            // a part without a finite value has sum 0 or NaN, which stays
-            const float keep = top == both ? 1.0f : exp2_fast((top - both) * a.scale);
-            const float take = high == both ? 1.0f : exp2_fast((high - both) * a.scale);
-            sum = fmaf(s, take, sum * keep);
-            hit += a.part_hit[at];
-            top = both;
-        }
+#pragma unroll 8
+        for (int t = part; t < a.tiles; t += kJoinParts) top = fmaxf(top, a.part_max[int64_t(t) * a.pitch + r]);
     }
     sh_max[part][lane] = top;
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < kJoinParts; p++) top = fmaxf(top, sh_max[p][lane]);
+    float sum = 0.0f, hit = 0.0f;
+    if (r < n) {
+#pragma unroll 8
+        for (int t = part; t < a.tiles; t += kJoinParts) {
+            const int64_t at = int64_t(t) * a.pitch + r;
+            // a part without a finite value has a sum of NaN, which stays
+            const float high = a.part_max[at];
+            sum = fmaf(a.part_sum[at], high == top ? 1.0f : exp2_fast((high - top) * a.scale), sum);
+            hit += a.part_hit[at];
+        }
+    }
+    __syncthreads();
+    if (part == 0) sh_max[0][lane] = top;
     sh_sum[part][lane] = sum;
     sh_hit[part][lane] = hit;
     __syncthreads();
-    if (part == 0) {
-        double loss = 0.0;
-        if (r < n) {
-            for (int p = 1; p < kJoinParts; p++) {
-                const float high = sh_max[p][lane], s = sh_sum[p][lane];
-                const float both = fmaxf(top, high);
-                const float keep = top == both ? 1.0f : exp2_fast((top - both) * a.scale);
-                const float take = high == both ? 1.0f : exp2_fast((high - both) * a.scale);
-                sum = fmaf(s, take, sum * keep);
-                hit += sh_hit[p][lane];
-                top = both;
-            }
-            const int t = a.rows[r];
-            // the difference of near numbers: in 64 bits, of which there is one per row
-            const double log_all = double(top) / double(a.heat) + double(logf(sum));
-            const double apart = log_all - double(hit) / double(a.heat);
-            const float one = float(double(a.heat) * double(a.heat) * (apart + (a.entropy ? a.entropy[t] : 0.0f)));
-            a.lse[t] = float(log_all);
-            a.losses[t] = one;
-            loss = one;
-        }
+    // a warp adds the parts of two rows
+    const int row = 2 * part + (lane >> 4), p = lane & 15;
+    sum = sh_sum[p][row];
+    hit = sh_hit[p][row];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-        if (lane == 0) a.sums[blockIdx.x] = float(loss);
+    for (int o = 8; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        hit += __shfl_xor_sync(0xffffffffu, hit, o);
+    }
+    float loss = 0.0f;
+    if (p == 0 && first + row < n) {
+        const int t = a.rows[first + row];
+        // the largest logit's distance from the targets' first: the difference of near numbers is exact
+        const float high = sh_max[0][row], log_sum = logf(sum), over = 1.0f / a.heat;
+        const float apart = fmaf(high - hit, over, log_sum) + (a.entropy ? a.entropy[t] : 0.0f);
+        loss = a.heat * a.heat * apart;
+        a.lse[t] = fmaf(high, over, log_sum);
+        a.losses[t] = loss;
+    }
+    loss += __shfl_xor_sync(0xffffffffu, loss, 16);
+    if (lane == 0) sh_all[part] = loss;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kJoinParts; w++) loss += sh_all[w];
+        a.sums[blockIdx.x] = loss;
+        sh_last = gridDim.x == 1 || last_ticket(a.ticket, gridDim.x);
     }
     __syncthreads();
-    if (threadIdx.x == 0) sh_last = last_ticket(a.ticket, gridDim.x);
-    __syncthreads();
     if (!sh_last) return;
-    double all = 0.0;
-    for (int b = threadIdx.x; b < int(gridDim.x); b += kJoinRows * kJoinParts) all += __ldcg(a.sums + b);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    // a thread's sum may be of a thousand blocks: what each addition cuts off is added up beside it
+    float all = 0.0f, cut = 0.0f;
+    for (int b = threadIdx.x; b < int(gridDim.x); b += kJoinRows * kJoinParts) {
+        const float v = __ldcg(a.sums + b), next = all + v, back = next - all;
+        cut += (all - (next - back)) + (v - back);
+        all = next;
+    }
+    all = fabsf(all) < INFINITY ? all + cut : all;
+    all = warp_sum(all);
     if (lane == 0) sh_all[part] = all;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int p = 1; p < kJoinParts; p++) all += sh_all[p];
-        *a.loss = n ? float(all / n) : 0.0f;
+        for (int w = 1; w < kJoinParts; w++) all += sh_all[w];
+        *a.loss = n ? all / float(n) : 0.0f;
     }
 }
 
@@ -340,18 +375,18 @@ struct SumArgs {
     Scale by;
 };
 
-constexpr int kSumTile = 64;
+constexpr int kSumTile = 64, kSumCols = 32;
 
-// Adds the parts of results whose summed index was split, in order, and rounds them: tiles of 64 x 64, turned
+// Adds the parts of results whose summed index was split, in order, and rounds them: tiles of 64 rows x 32, turned
 // from columns to rows in shared memory.
 template <typename T>
 __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArgs a) {
-    __shared__ float tile[kSumTile][kSumTile + 1];
+    __shared__ float tile[kSumTile][kSumCols + 1];
     pdl_wait();
     pdl_trigger();
-    const int n = *a.live, kind = int(blockIdx.x) >= a.first_block, across = (a.cols + kSumTile - 1) / kSumTile;
+    const int n = *a.live, kind = int(blockIdx.x) >= a.first_block, across = (a.cols + kSumCols - 1) / kSumCols;
     const int at = int(blockIdx.x) - (kind ? a.first_block : 0), rows = kind ? a.piece_rows : n;
-    const int r0 = at / across * kSumTile, c0 = at % across * kSumTile;
+    const int r0 = at / across * kSumTile, c0 = at % across * kSumCols;
     if (r0 >= rows) return;
     const int e = scale_exponent(a.by, share_of(a.by, n));
     const float unit = ldexpf(1.0f / a.by.lift, e);
@@ -359,20 +394,25 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
     const float *from = a.sums[kind] + int64_t(c0) * a.pitch[kind] + r0 + x;
     const int64_t part = int64_t(a.cols) * a.pitch[kind];
     if (r0 + x < rows) {
-#pragma unroll 4
-        for (int c = y; c < kSumTile && c0 + c < a.cols; c += 4) {
-            float v = 0.0f;
-#pragma unroll 4
-            for (int s = 0; s < a.splits[kind]; s++) v += from[s * part + int64_t(c) * a.pitch[kind]];
-            tile[x][c] = v * unit;
+        float v[kSumCols / 4];
+#pragma unroll
+        for (int i = 0; i < kSumCols / 4; i++) v[i] = 0.0f;
+#pragma unroll 2
+        for (int s = 0; s < a.splits[kind]; s++) {
+#pragma unroll
+            for (int i = 0; i < kSumCols / 4; i++)
+                if (c0 + y + 4 * i < a.cols) v[i] += from[s * part + int64_t(y + 4 * i) * a.pitch[kind]];
         }
+#pragma unroll
+        for (int i = 0; i < kSumCols / 4; i++) tile[x][y + 4 * i] = v[i] * unit;
     }
     __syncthreads();
-    for (int r = y; r < kSumTile && r0 + r < rows; r += 4) {
-        if (c0 + x < a.cols) {
+    const int c = threadIdx.x & (kSumCols - 1);
+    for (int r = threadIdx.x / kSumCols; r < kSumTile && r0 + r < rows; r += 256 / kSumCols) {
+        if (c0 + c < a.cols) {
             const int64_t row = kind ? r0 + r : a.rows[r0 + r];
-            const T v = from_f32<T>(tile[r][x]);
-            a.out[kind][row * a.cols + c0 + x] = reinterpret_cast<const uint16_t &>(v);
+            const T v = from_f32<T>(tile[r][c]);
+            a.out[kind][row * a.cols + c0 + c] = reinterpret_cast<const uint16_t &>(v);
         }
     }
 }
@@ -450,15 +490,16 @@ int64_t piece_of(int64_t pitch, int64_t vocab) {
 
 Layout layout_of(const nest_head_desc *d, const void *weight, bool backward) {
     Layout l = {};
-    l.packed = align_up(d->hidden, 8);
+    l.packed = align_up(d->hidden, 16);   // rows of whole 32-byte sectors
     l.pitch = align_up(d->tokens > 0 ? d->tokens : 1, kTile);
     l.piece = piece_of(l.pitch, d->vocab);
     l.width = width_of(d->tokens, backward ? l.piece : d->vocab);
     l.grad_width = d->hidden > kHalf ? kTile : kHalf;
     l.tiles = int32_t(cdiv(d->vocab, l.width));
     l.join = d->tokens ? int32_t(cdiv(d->tokens, kJoinRows)) : 1;
-    l.chunk = int32_t(align_up(d->tokens ? cdiv(d->tokens, kMostRowBlocks) : 1, d->tokens > 32 * kSMs ? 32 : 8));
+    l.chunk = d->tokens > kMostRowBlocks ? int32_t(cdiv(d->tokens, kMostRowBlocks)) : 1;
     l.row_blocks = d->tokens ? int32_t(cdiv(d->tokens, l.chunk)) : 1;
+    if (backward && l.row_blocks < kDepth) l.row_blocks = kDepth;   // which clear a row each
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t here = at;
@@ -537,6 +578,7 @@ struct Call {
     void *stream;
     const void *weight;    // as TMA reads it
     int64_t weight_pitch;
+    bool copied;
 
     template <typename T> T *at(size_t offset) const { return reinterpret_cast<T *>(ws + offset); }
 
@@ -590,7 +632,8 @@ struct Call {
         weight = w;
         weight_pitch = d->weight_row;
         int64_t copiers = 0;
-        if (!in_place(d, w)) {
+        copied = !in_place(d, w);
+        if (copied) {
             weight = ws + l.weight;
             weight_pitch = l.packed;
             r.weight = Rows{static_cast<const uint16_t *>(w), d->weight_row, d->weight_col, d->hidden,
@@ -610,6 +653,13 @@ struct Call {
         g.depth = int32_t(d->hidden);
         g.width = l.width;
         g.how[0] = instruction(d->dtype, true, true, l.width);
+        // boxes of the tokens that there are: 8 rows, the swizzle's pattern, at least
+        g.a_rows = d->tokens < kHalf ? int32_t(align_up(d->tokens, 8)) : kHalf;
+        g.a_bytes = g.a_rows * kDepth * 2;
+        g.b_bytes = l.width / 2 * kDepth * 2;
+        g.stages = kStages * kStage / (g.a_bytes + g.b_bytes);
+        if (g.stages > kMostStages) g.stages = kMostStages;
+        g.early = d->tokens <= kTile && !copied;
         g.ids = at<int32_t>(l.column);
         g.shares = d->k ? at<float>(l.shares) : nullptr;
         g.k = d->k ? d->k : 1;
@@ -670,7 +720,7 @@ int nest_head_loss(const nest_head_desc *d, const void *hidden, const void *weig
     g.part_hit = g.part_sum + part;
     if (d->tokens) {
         Maps maps = {};
-        int rc = encode(&maps.a, d->dtype, c.at<void>(c.l.hidden), d->hidden, c.l.pitch, c.l.packed, kHalf);
+        int rc = encode(&maps.a, d->dtype, c.at<void>(c.l.hidden), d->hidden, c.l.pitch, c.l.packed, g.a_rows);
         if (!rc) rc = encode(&maps.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, c.l.width / 2);
         if (!rc) rc = c.multiply(kLoss, maps, g, cdiv(d->tokens, kTile) * c.l.tiles);
         if (rc) return rc;
@@ -711,16 +761,17 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
             c.start(hidden, weight, index, teacher, mask, nullptr, nullptr, nullptr, grad_hidden, grad_losses))
         return rc;
 
+    GemmArgs g = c.products();
     void *h = c.at<void>(l.hidden);
     uint16_t *dz = c.at<uint16_t>(l.dz);
     Maps logits = {}, grads = {};
-    int rc = encode(&logits.a, d->dtype, h, d->hidden, l.pitch, l.packed, kHalf);
+    int rc = NEST_OK;
+    if (d->tokens) rc = encode(&logits.a, d->dtype, h, d->hidden, l.pitch, l.packed, g.a_rows);
     if (!rc) rc = encode(&logits.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, l.width / 2);
     if (!rc) rc = encode(&grads.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, kDepth);
     if (!rc) rc = encode(&grads.d, d->dtype, h, d->hidden, l.pitch, l.packed, kDepth);
     if (rc) return rc;
 
-    GemmArgs g = c.products();
     g.lse = lse;
     g.by = Scale{grad_loss, grad_losses, c.at<float>(l.parts), l.row_blocks, d->temperature,
                  d->dtype == NEST_F16 ? 32768.0f : 1.0f};
@@ -746,6 +797,8 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
         }
         GemmArgs p = g;
         p.width = l.grad_width;
+        p.a_bytes = p.b_bytes = kOperand;
+        p.stages = kStages;
         p.how[0] = instruction(d->dtype, true, false, p.width);
         p.how[1] = instruction(d->dtype, false, false, p.width);
         p.out[0] = out[0];
@@ -759,7 +812,7 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     s.rows = g.rows;
     s.cols = g.depth;
     s.by = g.by;
-    const int64_t wide = cdiv(d->hidden, kSumTile);
+    const int64_t wide = cdiv(d->hidden, kSumCols);
     const int64_t blocks[2] = {g.sums[0] ? cdiv(d->tokens, kSumTile) * wide : 0,
                                g.sums[1] ? cdiv(d->vocab, kSumTile) * wide : 0};
     s.piece_rows = int32_t(d->vocab);

@@ -26,7 +26,8 @@ constexpr int kHalf = 128;        // rows of either operand that one block of th
 constexpr int kDepth = 64;        // of the summed index per stage: 128 bytes, the widest swizzle
 constexpr int kOperand = kHalf * kDepth * 2;   // bytes of one operand's half
 constexpr int kStage = 2 * kOperand;
-constexpr int kStages = 6;
+constexpr int kStages = 6;                     // of full size; smaller ones are more
+constexpr int kMostStages = 12;
 constexpr int kEpilogueWarps = 8;    // two for each quarter of the rows
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kStaging = 32 * 128;   // bytes: 32 rows of 64 results in 16 bits, per epilogue warp
@@ -35,7 +36,7 @@ constexpr int kNoColumn = 0x7fffffff;
 constexpr int kMostRowBlocks = 512;  // of the kernel that lists the live tokens
 
 struct Shared {   // after the stages and the staging
-    uint64_t full[kStages], empty[kStages], done[2], free_[2], drain;
+    uint64_t full[kMostStages], empty[kMostStages], done[2], free_[2], drain;
     uint32_t tmem;
 };
 constexpr size_t kSharedBytes = 1024 + size_t(kStages) * kStage + kEpilogueWarps * kStaging + sizeof(Shared);
@@ -65,6 +66,10 @@ struct GemmArgs {
     int32_t first_col;        // of the piece: where its columns start in the vocabulary
     int32_t width;            // of a tile
     uint32_t how[2];          // instruction descriptors: loss and dz or grad hidden; grad weight
+    int32_t a_bytes, b_bytes; // of a stage: where the second operand starts, and its room
+    int32_t a_rows;           // loss, dz: rows in a box of the first operand
+    int32_t stages;
+    int32_t early;            // loss, dz: one row tile, and weights that the kernel before does not write
     // targets, by token
     const int32_t *ids;       // [T][k] ascending, kNoColumn past the last
     const float *shares;      // [T][k], NULL = 1
@@ -358,6 +363,7 @@ __device__ __forceinline__ float pick(const float (&v)[32], int i) {
 
 // 64 results of each of the warp's 32 rows, through shared memory so that a row's are written together.
 // `to`: where this lane's row goes, or NULL where nothing is written; `left`: columns that exist from here on.
+// Rows off alignment are written in the 16-byte pieces that lie in them, shifted, and the rest one by one.
 __device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigned char *staging, uint16_t *to, int left,
                                            bool wide, int lane) {
     uint4 *mine = reinterpret_cast<uint4 *>(staging) + lane * 8;
@@ -367,21 +373,46 @@ __device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigne
     __syncwarp();
     const uint64_t row = reinterpret_cast<uint64_t>(to);
     const int unit = lane & 7;
+    if (left > 64) left = 64;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int r = 4 * i + (lane >> 3);
         uint16_t *p = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, row, r));
-        const uint4 v = reinterpret_cast<const uint4 *>(staging)[r * 8 + (unit ^ (r & 7))];
-        const int rest = left - 8 * unit;
-        if (p && rest > 0) {
-            p += 8 * unit;
-            if (wide && rest >= 8) {
-                *reinterpret_cast<uint4 *>(p) = v;
-            } else {
+        const uint4 *from = reinterpret_cast<const uint4 *>(staging) + r * 8;
+        const uint4 v = from[unit ^ (r & 7)];
+        if (!p) continue;
+        if (wide) {
+            const int rest = left - 8 * unit;
+            if (rest >= 8) {
+                *reinterpret_cast<uint4 *>(p + 8 * unit) = v;
+            } else if (rest > 0) {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    if (e < rest) p[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+                    if (e < rest) p[8 * unit + e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+            }
+        } else {
+            // `skip` numbers come before the row's first aligned piece
+            const int skip = int((16 - (uint32_t(reinterpret_cast<uintptr_t>(p)) & 15)) & 15) >> 1;
+            const uint4 q = unit < 7 ? from[(unit + 1) ^ (r & 7)] : make_uint4(0, 0, 0, 0);
+            if (8 * unit + skip + 8 <= left) {
+                uint32_t w[8] = {v.x, v.y, v.z, v.w, q.x, q.y, q.z, q.w};
+                const bool two = skip & 4, one = skip & 2, part = skip & 1;
+#pragma unroll
+                for (int e = 0; e < 6; e++) w[e] = two ? w[e + 2] : w[e];
+#pragma unroll
+                for (int e = 0; e < 5; e++) w[e] = one ? w[e + 1] : w[e];
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[e] = part ? __funnelshift_r(w[e], w[e + 1], 16) : w[e];
+                *reinterpret_cast<uint4 *>(p + 8 * unit + skip) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            // what no piece holds: the first `skip`, and those behind the last piece
+            const int last = left < skip ? skip : skip + (left - skip) / 8 * 8;
+            const uint16_t *one = reinterpret_cast<const uint16_t *>(from);
+#pragma unroll
+            for (int e = unit; e < 16; e += 8) {
+                const int at = e < 8 ? e : last + e - 8;
+                if (at < (e < 8 ? min(skip, left) : left)) p[at] = one[((at >> 3) ^ (r & 7)) * 8 + (at & 7)];
             }
         }
     }
@@ -399,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t half = block_in_pair();
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; i++) {
+        for (int i = 0; i < kMostStages; i++) {
             barrier_init(&sh.full[i], 1);
             barrier_init(&sh.empty[i], 1);
         }
@@ -420,12 +451,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     __syncthreads();
     pair_sync();
     fence_after();
+
+    const int col_tiles = ((P == kGrads ? a.depth : a.cols) + a.width - 1) / a.width;
+    const int stage = a.a_bytes + a.b_bytes, part = a.width / 2;   // bytes; columns that this block loads
+    // Few tokens: boxes of no more rows than there are leave room for more stages, and the second block has no
+    // rows.  Operand rows that are not loaded make result rows that are not read.
+    const bool both = P == kGrads || a.a_rows == kHalf;
+    const uint32_t bytes = P == kGrads ? 2 * (kOperand + uint32_t(part) * kDepth * 2)
+                                       : kDepth * 2 * ((both ? 2 : 1) * uint32_t(a.a_rows) + 2 * uint32_t(part));
+    int ahead = 0;   // stages whose weights are on their way before the kernel before this one has ended
+    if (P != kGrads && a.early && warp == 0 && lane == 0) {
+        // one row tile: the pair's number is its first column tile
+        const int x = int(blockIdx.x >> 1) * a.width + int(half) * part, steps = (a.depth + kDepth - 1) / kDepth;
+        for (; ahead < a.stages && ahead < steps; ahead++) {
+            if (half == 0) barrier_expect(&sh.full[ahead], bytes);
+            load_box(&maps.b, shared_address(base + ahead * stage + a.a_bytes), in_first(shared_address(&sh.full[ahead])),
+                     ahead * kDepth, a.first_col + x);
+        }
+    }
     pdl_wait();
     pdl_trigger();
 
     const uint32_t tmem = sh.tmem;
     const int n = *a.live;
-    const int row_tiles = (n + kTile - 1) / kTile, col_tiles = ((P == kGrads ? a.depth : a.cols) + a.width - 1) / a.width;
+    const int row_tiles = P == kGrads ? (n + kTile - 1) / kTile : max(1, (n + kTile - 1) / kTile);
     Work work;
     work.start(Tiles{row_tiles, col_tiles, P == kGrads ? a.splits[0] : 1,
                      ((P == kGrads ? a.cols : a.depth) + kDepth - 1) / kDepth},
@@ -436,19 +485,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const int width = a.width / 2;     // columns that this block loads
-        const uint32_t bytes = 2 * (kOperand + uint32_t(width) * kDepth * 2);
         while (ok && work.next(t)) {
-            const int y = t.row * kTile + int(half) * kHalf, x = t.col * a.width + int(half) * width;
+            const int y = t.row * kTile + int(half) * kHalf, x = t.col * a.width + int(half) * part;
             for (int kb = 0; kb < t.steps; kb++) {
                 ok = barrier_wait(&sh.empty[s], phase ^ 1);
                 if (!ok) break;
-                const uint32_t to = shared_address(base + s * kStage), bar = in_first(shared_address(&sh.full[s]));
+                const uint32_t to = shared_address(base + s * stage), bar = in_first(shared_address(&sh.full[s]));
                 const int k0 = (t.from + kb) * kDepth;
-                if (half == 0) barrier_expect(&sh.full[s], bytes);
+                const bool begun = ahead > 0;
+                if (begun) ahead--;
+                if (half == 0 && !begun) barrier_expect(&sh.full[s], bytes);
                 if constexpr (P != kGrads) {
-                    load_box(&maps.a, to, bar, k0, y);
-                    load_box(&maps.b, to + kOperand, bar, k0, a.first_col + x);
+                    if (both || half == 0) load_box(&maps.a, to, bar, k0, y);
+                    if (!begun) load_box(&maps.b, to + a.a_bytes, bar, k0, a.first_col + x);
                 } else {
                     if (t.kind == 0) {
                         load_box(&maps.a, to, bar, k0, y);
@@ -458,13 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     const CUtensorMap *map = t.kind ? &maps.d : &maps.b;
                     const int r = k0 + (t.kind ? 0 : a.first_col);
-                    for (int c = 0; c < width; c += 64) load_box(map, to + kOperand + c * kDepth * 2, bar, x + c, r);
+                    for (int c = 0; c < part; c += 64) load_box(map, to + kOperand + c * kDepth * 2, bar, x + c, r);
                 }
-                if (++s == kStages) s = 0, phase ^= 1;
+                if (++s == a.stages) s = 0, phase ^= 1;
             }
         }
         if (!ok) {   // copies under way end within microseconds: those of the stages that are still open
-            for (int i = 0; i < kStages && half == 0; i++)
+            for (int i = 0; i < a.stages && half == 0; i++)
                 barrier_wait_long(shared_address(&sh.full[i]), i < s ? phase : phase ^ 1, 1000000);
             const uint64_t start = nanoseconds();
             while (nanoseconds() - start < 10000000) __nanosleep(1000);
@@ -484,20 +533,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 ok = barrier_wait(&sh.full[s], phase);
                 if (!ok) break;
                 fence_after();
-                const uint32_t at = shared_address(base + s * kStage);
+                const uint32_t at = shared_address(base + s * stage);
                 // operands whose rows in memory run along the summed index: both; dz; none
-                auto stage = [&](auto a_along, auto b_along, uint32_t how) {
+                auto products = [&](auto a_along, auto b_along, uint32_t how) {
                     constexpr bool kA = decltype(a_along)::value, kB = decltype(b_along)::value;
-                    const uint64_t da = descriptor<kA>(at), db = descriptor<kB>(at + kOperand);
+                    const uint64_t da = descriptor<kA>(at), db = descriptor<kB>(at + a.a_bytes);
 #pragma unroll
                     for (int q = 0; q < kDepth / 16; q++)
                         multiply(tmem + acc * kTile, da + q * kStep<kA>, db + q * kStep<kB>, how, kb | q);
                 };
-                if constexpr (P != kGrads) stage(std::true_type{}, std::true_type{}, a.how[0]);
-                else if (t.kind == 0) stage(std::true_type{}, std::false_type{}, a.how[0]);
-                else stage(std::false_type{}, std::false_type{}, a.how[1]);
+                if constexpr (P != kGrads) products(std::true_type{}, std::true_type{}, a.how[0]);
+                else if (t.kind == 0) products(std::true_type{}, std::false_type{}, a.how[0]);
+                else products(std::false_type{}, std::false_type{}, a.how[1]);
                 commit(&sh.empty[s]);
-                if (++s == kStages) s = 0, phase ^= 1;
+                if (++s == a.stages) s = 0, phase ^= 1;
             }
             if (ok) commit(&sh.done[acc]);
         }
