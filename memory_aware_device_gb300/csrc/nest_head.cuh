@@ -479,38 +479,49 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     work.start(Tiles{row_tiles, col_tiles, P == kGrads ? a.splits[0] : 1,
                      ((P == kGrads ? a.cols : a.depth) + kDepth - 1) / kDepth},
                Tiles{(a.cols + kTile - 1) / kTile, col_tiles, a.splits[1], (n + kDepth - 1) / kDepth}, P == kGrads);
-    Tile t;
+    Tile t = {};
 
     if (warp == 0 && lane == 0) {
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
-        while (ok && work.next(t)) {
+        const uint32_t stage0 = shared_address(base), full0 = in_first(shared_address(&sh.full[0]));
+        const int stages = a.stages;
+        // the loop over a tile's stages, of one product each: its loads differ
+        auto loads = [&](auto product) {
+            constexpr int kKind = decltype(product)::value;   // 0, 1: grad hidden, grad weight; 2: logits
             const int y = t.row * kTile + int(half) * kHalf, x = t.col * a.width + int(half) * part;
             for (int kb = 0; kb < t.steps; kb++) {
                 ok = barrier_wait(&sh.empty[s], phase ^ 1);
                 if (!ok) break;
-                const uint32_t to = shared_address(base + s * stage), bar = in_first(shared_address(&sh.full[s]));
+                const uint32_t to = stage0 + uint32_t(s * stage), bar = full0 + s * 8;
                 const int k0 = (t.from + kb) * kDepth;
-                const bool begun = ahead > 0;
-                if (begun) ahead--;
-                if (half == 0 && !begun) barrier_expect(&sh.full[s], bytes);
-                if constexpr (P != kGrads) {
+                if constexpr (kKind == 2) {
+                    const bool begun = ahead > 0;
+                    if (begun) ahead--;
+                    if (half == 0 && !begun) barrier_expect(&sh.full[s], bytes);
                     if (both || half == 0) load_box(&maps.a, to, bar, k0, y);
                     if (!begun) load_box(&maps.b, to + a.a_bytes, bar, k0, a.first_col + x);
                 } else {
-                    if (t.kind == 0) {
+                    if (half == 0) barrier_expect(&sh.full[s], bytes);
+                    const CUtensorMap *map = kKind ? &maps.d : &maps.b;
+                    const int r = k0 + (kKind ? 0 : a.first_col);
+                    if constexpr (kKind == 0) {
                         load_box(&maps.a, to, bar, k0, y);
                     } else {
                         load_box(&maps.c, to, bar, y, k0);
                         load_box(&maps.c, to + kOperand / 2, bar, y + 64, k0);
                     }
-                    const CUtensorMap *map = t.kind ? &maps.d : &maps.b;
-                    const int r = k0 + (t.kind ? 0 : a.first_col);
-                    for (int c = 0; c < part; c += 64) load_box(map, to + kOperand + c * kDepth * 2, bar, x + c, r);
+                    load_box(map, to + kOperand, bar, x, r);
+                    if (part > 64) load_box(map, to + kOperand + kOperand / 2, bar, x + 64, r);
                 }
-                if (++s == a.stages) s = 0, phase ^= 1;
+                if (++s == stages) s = 0, phase ^= 1;
             }
+        };
+        while (ok && work.next(t)) {
+            if constexpr (P != kGrads) loads(std::integral_constant<int, 2>{});
+            else if (t.kind == 0) loads(std::integral_constant<int, 0>{});
+            else loads(std::integral_constant<int, 1>{});
         }
         if (!ok) {   // copies under way end within microseconds: those of the stages that are still open
             for (int i = 0; i < a.stages && half == 0; i++)
@@ -522,6 +533,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         int s = 0, use = 0;
         uint32_t phase = 0;
         bool ok = true;
+        const uint32_t stage0 = shared_address(base);
+        const int stages = a.stages, step = stage >> 4;   // of descriptors
+        // operands whose rows in memory run along the summed index: both; dz; none
+        auto products = [&](auto a_along, auto b_along, uint32_t how, uint32_t to) {
+            constexpr bool kA = decltype(a_along)::value, kB = decltype(b_along)::value;
+            const uint64_t a0 = descriptor<kA>(stage0), b0 = descriptor<kB>(stage0 + a.a_bytes);
+            for (int kb = 0, steps = t.steps; kb < steps; kb++) {
+                ok = barrier_wait(&sh.full[s], phase);
+                if (!ok) break;
+                fence_after();
+                const uint64_t da = a0 + uint32_t(s * step), db = b0 + uint32_t(s * step);
+#pragma unroll
+                for (int q = 0; q < kDepth / 16; q++) multiply(to, da + q * kStep<kA>, db + q * kStep<kB>, how, kb | q);
+                commit(&sh.empty[s]);
+                if (++s == stages) s = 0, phase ^= 1;
+            }
+        };
         while (ok && work.next(t)) {
             if (!t.steps) continue;
             const int acc = use & 1;
@@ -529,25 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             use++;
             if (!ok) break;
             fence_after();
-            for (int kb = 0; kb < t.steps; kb++) {
-                ok = barrier_wait(&sh.full[s], phase);
-                if (!ok) break;
-                fence_after();
-                const uint32_t at = shared_address(base + s * stage);
-                // operands whose rows in memory run along the summed index: both; dz; none
-                auto products = [&](auto a_along, auto b_along, uint32_t how) {
-                    constexpr bool kA = decltype(a_along)::value, kB = decltype(b_along)::value;
-                    const uint64_t da = descriptor<kA>(at), db = descriptor<kB>(at + a.a_bytes);
-#pragma unroll
-                    for (int q = 0; q < kDepth / 16; q++)
-                        multiply(tmem + acc * kTile, da + q * kStep<kA>, db + q * kStep<kB>, how, kb | q);
-                };
-                if constexpr (P != kGrads) products(std::true_type{}, std::true_type{}, a.how[0]);
-                else if (t.kind == 0) products(std::true_type{}, std::false_type{}, a.how[0]);
-                else products(std::false_type{}, std::false_type{}, a.how[1]);
-                commit(&sh.empty[s]);
-                if (++s == a.stages) s = 0, phase ^= 1;
-            }
+            const uint32_t to = tmem + acc * kTile;
+            if constexpr (P != kGrads) products(std::true_type{}, std::true_type{}, a.how[0], to);
+            else if (t.kind == 0) products(std::true_type{}, std::false_type{}, a.how[0], to);
+            else products(std::false_type{}, std::false_type{}, a.how[1], to);
             if (ok) commit(&sh.done[acc]);
         }
         if (!ok) {
