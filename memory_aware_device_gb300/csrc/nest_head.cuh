@@ -235,11 +235,15 @@ struct Tile {
     int kind, row, col, split, from, steps;
 };
 
+// What a tile takes, in stages: its own, or those that fit in the time of writing its results.
+constexpr int kTileCost = 12;
+
 // One product's tiles in the order in which they are taken: for each part of the summed index, groups of
 // kGroup row tiles, column by column.
 struct Tiles {
     int rows, cols, splits, steps;
     __device__ __forceinline__ int per() const { return (steps + splits - 1) / splits; }
+    __device__ __forceinline__ int cost() const { return max(per(), kTileCost); }
     __device__ __forceinline__ int count() const { return rows * cols * splits; }
     __device__ __forceinline__ void at(int i, Tile &t) const {
         t.split = i / (rows * cols);
@@ -270,7 +274,7 @@ struct Work {
         i = pair;
         const int over = long_.count() % pairs;
         idle = over ? pairs - over : 0;      // pairs with one less: the last ones
-        extra = two && idle ? (long_.per() + short_.per() / 2) / max(1, short_.per()) : 0;
+        extra = two && idle ? (long_.cost() + short_.cost() / 2) / short_.cost() : 0;
         if (!two) short_.rows = 0;
     }
     // phases of i: [0, count) the longer; then, from `count` on, idle rounds and common rounds of the shorter
