@@ -464,12 +464,12 @@ void split(int64_t tokens, int64_t cols, int64_t hidden, int width, bool pieces,
     if (pieces) splits[1] = 1;
 }
 
-// Columns of a tile of logits: the width for which the rounds of all pairs take least, counting 32 columns for
-// what a tile costs besides.
-int width_of(int64_t tokens, int64_t cols) {
+// Columns of a tile of logits: the multiple of `step` for which the rounds of all pairs take least, counting 32
+// columns for what a tile costs besides.
+int width_of(int64_t tokens, int64_t cols, int step) {
     int best = kTile;
     int64_t least = INT64_MAX;
-    for (int w = kTile; w >= 128; w -= 32) {
+    for (int w = kTile; w >= 128; w -= step) {
         const int64_t time = cdiv(cdiv(tokens, kTile) * cdiv(cols, w), kPairs) * (w + 32);
         if (time < least) least = time, best = w;
     }
@@ -514,7 +514,8 @@ Layout layout_of(const nest_head_desc *d, const void *weight, bool backward) {
     l.packed = align_up(d->hidden, 16);   // rows of whole 32-byte sectors
     l.pitch = align_up(d->tokens > 0 ? d->tokens : 1, kTile);
     l.piece = piece_of(l.pitch, d->vocab);
-    l.width = width_of(d->tokens, backward ? l.piece : d->vocab);
+    // dz is written in boxes of 64 columns
+    l.width = backward ? width_of(d->tokens, l.piece, 64) : width_of(d->tokens, d->vocab, 32);
     l.grad_width = d->hidden > kHalf ? kTile : kHalf;
     l.tiles = int32_t(cdiv(d->vocab, l.width));
     l.join = d->tokens ? int32_t(cdiv(d->tokens, kJoinRows)) : 1;
@@ -792,13 +793,13 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     if (!rc) rc = encode(&logits.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, l.width / 2);
     if (!rc) rc = encode(&grads.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, kDepth);
     if (!rc) rc = encode(&grads.d, d->dtype, h, d->hidden, l.pitch, l.packed, kDepth);
+    const bool wide_weight = d->hidden % 8 == 0 && aligned_to(grad_weight, 16);
+    if (!rc && wide_weight) rc = encode(&grads.out, d->dtype, grad_weight, d->hidden, d->vocab, d->hidden, 32);
     if (rc) return rc;
 
     g.lse = lse;
     g.by = Scale{grad_loss, grad_losses, c.at<float>(l.parts), l.row_blocks, d->temperature,
                  d->dtype == NEST_F16 ? 32768.0f : 1.0f};
-    g.dz = dz;
-    g.dz_pitch = l.piece;
     uint16_t *out[2] = {static_cast<uint16_t *>(grad_hidden), static_cast<uint16_t *>(grad_weight)};
     for (int i = 0; i < 2; i++) {
         g.wide[i] = d->hidden % 8 == 0 && aligned_to(out[i], 16);
@@ -812,6 +813,7 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
         g.first_col = int32_t(first);
         g.add = first > 0;
         if (d->tokens) {
+            if ((rc = encode(&logits.out, d->dtype, dz, g.cols, l.pitch, l.piece, 32))) return rc;
             if ((rc = c.multiply(kDz, logits, g, cdiv(d->tokens, kTile) * cdiv(g.cols, l.width)))) return rc;
             rc = encode(&grads.a, d->dtype, dz, g.cols, l.pitch, l.piece, kHalf);
             if (!rc) rc = encode(&grads.c, d->dtype, dz, g.cols, l.pitch, l.piece, kDepth);

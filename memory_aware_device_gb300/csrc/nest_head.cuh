@@ -46,6 +46,7 @@ enum Product { kLoss, kDz, kGrads };
 
 struct Maps {     // operands: loss and dz: hidden, weight; grads: dz, weight, dz again by columns, hidden
     CUtensorMap a, b, c, d;
+    CUtensorMap out;   // dz, or grad weight where it is 16-byte aligned
 };
 
 // What the gradients of the losses are scaled by.
@@ -78,9 +79,7 @@ struct GemmArgs {
     float *part_max, *part_sum, *part_hit;   // loss: [column tile][pitch]
     const float *lse;         // dz: [T]
     Scale by;                 // dz, grads
-    uint16_t *dz;             // [pitch][dz_pitch]
-    int64_t dz_pitch;
-    // grads: hidden, weight
+    // grads: hidden, weight (of the piece)
     uint16_t *out[2];
     int32_t wide[2];          // rows of out are 16-byte aligned
     int32_t splits[2];        // parts of the summed index
@@ -161,6 +160,17 @@ __device__ __forceinline__ void load_box(const CUtensorMap *map, uint32_t to, ui
         "l"(map), "r"(x), "r"(y), "r"(barrier)
         : "memory");
 }
+
+// A box of this block's shared memory to (x, y) of `map`, which cuts off what lies past its ends.
+__device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t from, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(from)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until the boxes of this thread have been read, or written.
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Shared-memory descriptors of operands in 128-byte rows with the 128-byte swizzle, whose pattern repeats
 // every 8 rows (1024 bytes).  Summed index along the rows: groups of 8 operand rows follow each other.
@@ -365,40 +375,48 @@ __device__ __forceinline__ float pick(const float (&v)[32], int i) {
     return i & 1 ? t[1] : t[0];
 }
 
-// 64 results of each of the warp's 32 rows, through shared memory so that a row's are written together.
-// `to`: where this lane's row goes, or NULL where nothing is written; `left`: columns that exist from here on.
-// Rows off alignment are written in the 16-byte pieces that lie in them, shifted, and the rest one by one.
-__device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigned char *staging, uint16_t *to, int left,
-                                           bool wide, int lane) {
+// 64 results of each of the warp's 32 rows to shared memory, 128 bytes a row with the 128-byte swizzle.
+__device__ __forceinline__ void stage_rows(const uint32_t (&packed)[32], unsigned char *staging, int lane) {
     uint4 *mine = reinterpret_cast<uint4 *>(staging) + lane * 8;
 #pragma unroll
     for (int u = 0; u < 8; u++)
         mine[u ^ (lane & 7)] = make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
-    __syncwarp();
+}
+
+// And from there to memory where the rows do not follow each other or are off alignment, a row's together.
+// `to`: where this lane's row goes, or NULL where nothing is written; `left`: columns that exist from here on.
+// Rows off alignment are written in the 16-byte pieces that lie in them, shifted, and the rest one by one.
+__device__ __forceinline__ void write_rows(const unsigned char *staging, uint16_t *to, int left, bool wide, int lane) {
     const uint64_t row = reinterpret_cast<uint64_t>(to);
     const int unit = lane & 7;
     if (left > 64) left = 64;
+    if (wide) {
+        const bool in = left - 8 * unit >= 8;   // of the columns, whose number is a multiple of 8
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            uint4 v[4];
+            uint64_t p[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = 4 * (h + i) + (lane >> 3);
+                p[i] = __shfl_sync(0xffffffffu, row, r);
+                v[i] = (reinterpret_cast<const uint4 *>(staging) + r * 8)[unit ^ (r & 7)];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (p[i] && in) *(reinterpret_cast<uint4 *>(p[i]) + unit) = v[i];
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int r = 4 * i + (lane >> 3);
         uint16_t *p = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, row, r));
         const uint4 *from = reinterpret_cast<const uint4 *>(staging) + r * 8;
-        const uint4 v = from[unit ^ (r & 7)];
-        if (!p) continue;
-        if (wide) {
-            const int rest = left - 8 * unit;
-            if (rest >= 8) {
-                *reinterpret_cast<uint4 *>(p + 8 * unit) = v;
-            } else if (rest > 0) {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    if (e < rest) p[8 * unit + e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
-            }
-        } else {
+        if (p) {
             // `skip` numbers come before the row's first aligned piece
             const int skip = int((16 - (uint32_t(reinterpret_cast<uintptr_t>(p)) & 15)) & 15) >> 1;
-            const uint4 q = unit < 7 ? from[(unit + 1) ^ (r & 7)] : make_uint4(0, 0, 0, 0);
+            const uint4 v = from[unit ^ (r & 7)], q = unit < 7 ? from[(unit + 1) ^ (r & 7)] : make_uint4(0, 0, 0, 0);
             if (8 * unit + skip + 8 <= left) {
                 uint32_t w[8] = {v.x, v.y, v.z, v.w, q.x, q.y, q.z, q.w};
                 const bool two = skip & 4, one = skip & 2, part = skip & 1;
@@ -419,8 +437,8 @@ __device__ __forceinline__ void write_rows(const uint32_t (&packed)[32], unsigne
                 if (at < (e < 8 ? min(skip, left) : left)) p[at] = one[((at >> 3) ^ (r & 7)) * 8 + (at & 7)];
             }
         }
+        __syncwarp();
     }
-    __syncwarp();
 }
 
 template <Product P, typename T>
@@ -665,7 +683,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int chunks = (min(a.width, columns - c0) + 63) / 64;
                 float *sums = P == kGrads ? a.sums[t.kind] : nullptr;
                 uint16_t *to = nullptr;
-                if constexpr (P == kDz) to = a.dz + int64_t(r) * a.dz_pitch;   // rows past n too
                 if (P == kGrads && there) to = a.out[t.kind] + int64_t(t.kind ? r : token) * a.depth;
                 if (P == kGrads && sums) sums += int64_t(t.split) * a.depth * a.sums_pitch[t.kind] + r;
 #pragma unroll 1
@@ -722,9 +739,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                         for (int e = 0; e < 16; e++) packed[16 * h + e] = pack_two<T>(v[2 * e], v[2 * e + 1]);
                     }
-                    if (P == kDz || !sums)
-                        write_rows(packed, mine, to ? to + at : nullptr, min(a.width - c * 64, columns - at),
-                                   P == kDz || a.wide[t.kind], lane);
+                    if (P == kDz || !sums) {
+                        if (lane == 0) stores_read();   // of the chunk before
+                        __syncwarp();
+                        stage_rows(packed, mine, lane);
+                        if (P == kDz || (t.kind && a.wide[1])) {
+                            // rows of dz past n too
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0 && (P == kDz || there))
+                                store_box(&maps.out, shared_address(mine), at,
+                                          (P == kGrads ? a.first_col : 0) + r);
+                        } else {
+                            __syncwarp();
+                            write_rows(mine, to ? to + at : nullptr, columns - at, a.wide[t.kind], lane);
+                        }
+                    }
                 }
                 if (t.steps) {
                     fence_before();
@@ -734,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (t.steps) use++;
         }
+        if (lane == 0) stores_done();
     }
 
     __syncwarp();
