@@ -28,7 +28,7 @@ struct RowArgs {
     const uint8_t *flags;                  // with a teacher: which tokens are live
     int32_t chunk, blocks;                 // tokens per block; the blocks after these copy weights
     int32_t *rows, *count;                 // [n], [1]
-    int32_t *column;                       // [T], with labels
+    int32_t *row_labels;                   // [n], with labels
     uint32_t *ticket;
     Rows weight;                           // to copy, or width 0
     // forward: of tokens that are not live
@@ -37,7 +37,10 @@ struct RowArgs {
     // backward
     uint16_t *grad;                        // [T][D]
     int32_t wide_grad;
+    const float *lse_in;
+    float *row_lse;                        // [n] lse log2(e)
     const float *grad_losses;
+    float *row_grad;                       // [n]
     float *parts;                          // [blocks] the largest finite |grad_losses| of live tokens
 };
 
@@ -156,12 +159,15 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         const bool live = t < end && is_live(a, t);
         const uint32_t set = __ballot_sync(0xffffffffu, live);
         if (warp == 0 && t < end) {
-            if (live) a.rows[at + __popc(set & ((1u << lane) - 1))] = int(t);
-            if (a.column) a.column[t] = label_of(a, t);
+            const int place = at + __popc(set & ((1u << lane) - 1));
+            if (live) a.rows[place] = int(t);
+            if (live && a.row_labels) a.row_labels[place] = label_of(a, t);
+            if (live && a.row_lse) a.row_lse[place] = a.lse_in[t] * kLog2e;
             if (!live && a.losses) a.losses[t] = 0.0f, a.lse[t] = 0.0f;
             if (live && a.grad_losses) {
-                const float g = fabsf(a.grad_losses[t]);
-                if (g < INFINITY) top = fmaxf(top, g);
+                const float g = a.grad_losses[t];
+                a.row_grad[place] = g;
+                if (fabsf(g) < INFINITY) top = fmaxf(top, fabsf(g));
             }
         }
         const int segments = (int(a.hidden.width) + kSegment - 1) / kSegment, here = int(min(int64_t(32), end - t0));
@@ -495,7 +501,8 @@ struct Layout {
     int32_t chunk, row_blocks;   // of the list of live tokens
     int32_t splits[2];
     int64_t sums_pitch[2];
-    size_t count, ticket, rows, column, shares, entropy, flags, hidden, weight, part, sums, parts, dz, grad_sums[2], total;
+    size_t count, ticket, rows, column, shares, entropy, flags, hidden, weight, part, sums, parts, dz, row_lse, row_grad,
+        grad_sums[2], total;
 };
 
 // Pieces of the vocabulary: dz of a piece takes up to 256 MiB, or 8192 columns where that is more (the sums
@@ -548,6 +555,8 @@ Layout layout_of(const nest_head_desc *d, const void *weight, bool backward) {
         split(d->tokens, pieces ? l.piece : d->vocab, d->hidden, l.grad_width, pieces, l.splits);
         l.sums_pitch[0] = l.pitch;
         l.sums_pitch[1] = l.piece;
+        l.row_lse = take(4 * d->tokens);
+        l.row_grad = take(4 * d->tokens);
         l.parts = take(4 * kMostRowBlocks);
         l.dz = take(2 * l.pitch * l.piece);
         for (int i = 0; i < 2; i++)
@@ -605,7 +614,7 @@ struct Call {
     template <typename T> T *at(size_t offset) const { return reinterpret_cast<T *>(ws + offset); }
 
     int start(const void *hidden, const void *w, const void *index, const void *teacher, const uint8_t *mask,
-              float *losses, float *lse, int32_t *live, void *grad, const float *grad_losses) {
+              float *losses, float *lse, int32_t *live, void *grad, const float *lse_in, const float *grad_losses) {
         if (d->k) {
             TeacherArgs t = {};
             t.index = index;
@@ -642,14 +651,17 @@ struct Call {
         r.blocks = l.row_blocks;
         r.rows = at<int32_t>(l.rows);
         r.count = at<int32_t>(l.count);
-        r.column = d->k ? nullptr : at<int32_t>(l.column);
+        r.row_labels = d->k ? nullptr : at<int32_t>(l.column);
         r.ticket = live ? at<uint32_t>(l.ticket) : nullptr;
         r.losses = losses;
         r.lse = lse;
         r.live = live;
         r.grad = static_cast<uint16_t *>(grad);
         r.wide_grad = d->hidden % 8 == 0 && aligned_to(grad, 16);
+        r.lse_in = lse_in;
+        r.row_lse = grad ? at<float>(l.row_lse) : nullptr;
         r.grad_losses = grad_losses;
+        r.row_grad = grad_losses ? at<float>(l.row_grad) : nullptr;
         r.parts = grad_losses ? at<float>(l.parts) : nullptr;
         weight = w;
         weight_pitch = d->weight_row;
@@ -682,9 +694,9 @@ struct Call {
         g.stages = kStages * kStage / (g.a_bytes + g.b_bytes);
         if (g.stages > kMostStages) g.stages = kMostStages;
         g.early = d->tokens <= kTile && !copied;
-        g.ids = at<int32_t>(l.column);
+        (d->k ? g.ids : g.labels) = at<int32_t>(l.column);
         g.shares = d->k ? at<float>(l.shares) : nullptr;
-        g.k = d->k ? d->k : 1;
+        g.k = d->k;
         g.scale = kLog2e * over_heat(d->temperature, d->hidden);
         return g;
     }
@@ -732,7 +744,7 @@ int nest_head_loss(const nest_head_desc *d, const void *hidden, const void *weig
     if (!loss || !live || (d->tokens && (!losses || !lse))) return NEST_E_INVALID;
     Call c = {d, layout_of(d, weight, false), static_cast<unsigned char *>(workspace), stream};
     if (!workspace || ws_bytes < c.l.total || !aligned_to(workspace, 256)) return NEST_E_WORKSPACE;
-    if (const int rc = c.start(hidden, weight, index, teacher, mask, losses, lse, live, nullptr, nullptr))
+    if (const int rc = c.start(hidden, weight, index, teacher, mask, losses, lse, live, nullptr, nullptr, nullptr))
         return rc;
     GemmArgs g = c.products();
     g.cols = int32_t(d->vocab);
@@ -781,7 +793,7 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     const Layout &l = c.l;
     if (!workspace || ws_bytes < l.total || !aligned_to(workspace, 256)) return NEST_E_WORKSPACE;
     if (const int rc =
-            c.start(hidden, weight, index, teacher, mask, nullptr, nullptr, nullptr, grad_hidden, grad_losses))
+            c.start(hidden, weight, index, teacher, mask, nullptr, nullptr, nullptr, grad_hidden, lse, grad_losses))
         return rc;
 
     GemmArgs g = c.products();
@@ -797,7 +809,8 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     if (!rc && wide_weight) rc = encode(&grads.out, d->dtype, grad_weight, d->hidden, d->vocab, d->hidden, 32);
     if (rc) return rc;
 
-    g.lse = lse;
+    g.row_lse = c.at<float>(l.row_lse);
+    g.row_grad = grad_losses ? c.at<float>(l.row_grad) : nullptr;
     g.by = Scale{grad_loss, grad_losses, c.at<float>(l.parts), l.row_blocks, d->temperature,
                  d->dtype == NEST_F16 ? 32768.0f : 1.0f};
     uint16_t *out[2] = {static_cast<uint16_t *>(grad_hidden), static_cast<uint16_t *>(grad_weight)};

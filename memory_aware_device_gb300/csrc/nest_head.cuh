@@ -71,13 +71,15 @@ struct GemmArgs {
     int32_t a_rows;           // loss, dz: rows in a box of the first operand
     int32_t stages;
     int32_t early;            // loss, dz: one row tile, and weights that the kernel before does not write
-    // targets, by token
+    // targets
+    const int32_t *labels;    // [n], NULL with a teacher
     const int32_t *ids;       // [T][k] ascending, kNoColumn past the last
-    const float *shares;      // [T][k], NULL = 1
+    const float *shares;      // [T][k]
     int32_t k;
     float scale;              // log2(e) / h
     float *part_max, *part_sum, *part_hit;   // loss: [column tile][pitch]
-    const float *lse;         // dz: [T]
+    const float *row_lse;     // dz: [n], lse log2(e)
+    const float *row_grad;    // dz: [n], NULL = 0: the gradient of each token's loss
     Scale by;                 // dz, grads
     // grads: hidden, weight (of the piece)
     uint16_t *out[2];
@@ -112,15 +114,17 @@ __device__ __forceinline__ void barrier_expect(uint64_t *b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(b)), "r"(bytes)
                  : "memory");
 }
+// What it lets go on are reads of tensor memory, which the fence before it orders: nothing that this thread
+// wrote to memory has to be seen by the other block (waiting for that took a seventh of the loss's time).
 __device__ __forceinline__ void arrive_at_first(uint64_t *b) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(shared_address(b)))
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(shared_address(b)))
                  : "memory");
 }
 __device__ __forceinline__ bool barrier_try(uint32_t address, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(address), "r"(parity)
@@ -230,6 +234,46 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max_of_three(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two numbers of 32 bits in one operation each.
+struct Pair {
+    uint64_t v;
+    __device__ __forceinline__ Pair() {}
+    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Pair multiply_add(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair times(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+// exp2 of v * by - off, of 32 numbers.
+__device__ __forceinline__ void exponentials(float (&v)[32], float by, float off) {
+    const Pair two_by(by, by), two_off(-off, -off);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float x, y;
+        multiply_add(Pair(v[e], v[e + 1]), two_by, two_off).get(x, y);
+        v[e] = exp2_fast(x);
+        v[e + 1] = exp2_fast(y);
+    }
+}
+
 template <typename T> __device__ __forceinline__ uint32_t pack_two(float low, float high);
 template <> __device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float low, float high) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(low, high);
@@ -246,7 +290,7 @@ struct Tile {
 };
 
 // What a tile takes, in stages: its own, or those that fit in the time of writing its results.
-constexpr int kTileCost = 12;
+constexpr int kTileCost = 10;
 
 // One product's tiles in the order in which they are taken: for each part of the summed index, groups of
 // kGroup row tiles, column by column.
@@ -339,15 +383,30 @@ __device__ __forceinline__ float share_of(const Scale &s, int n) {
     return s.grad_loss && n ? *s.grad_loss / float(n) : 0.0f;
 }
 
+// What a row of a tile needs from memory, loaded a tile ahead.
+struct Row {
+    int token;      // -1: not there
+    int label;
+    float lse, grad;
+};
+
 // A token's targets from a column on, in ascending order.
 struct Targets {
     const int32_t *id;
     const float *share;
     int j, k, next;
-    __device__ __forceinline__ void start(const GemmArgs &a, int token, int col) {
-        k = token < 0 ? 0 : a.k;
-        id = a.ids + int64_t(token < 0 ? 0 : token) * a.k;
-        share = a.shares ? a.shares + int64_t(token < 0 ? 0 : token) * a.k : nullptr;
+    __device__ __forceinline__ void start(const GemmArgs &a, const Row &row, int col) {
+        k = 0;
+        j = 0;
+        if (a.labels) {
+            next = row.token >= 0 && row.label >= col ? row.label : kNoColumn;
+            return;
+        }
+        next = kNoColumn;
+        if (row.token < 0) return;
+        k = a.k;
+        id = a.ids + int64_t(row.token) * k;
+        share = a.shares + int64_t(row.token) * k;
         int low = 0, high = k;   // the first id >= col
         while (low < high) {
             const int mid = (low + high) >> 1;
@@ -355,9 +414,9 @@ struct Targets {
             else high = mid;
         }
         j = low;
-        next = j < k ? id[j] : kNoColumn;
+        if (j < k) next = id[j];
     }
-    __device__ __forceinline__ float weight() const { return share ? share[j] : 1.0f; }
+    __device__ __forceinline__ float weight() const { return k ? share[j] : 1.0f; }
     __device__ __forceinline__ void advance() { next = ++j < k ? id[j] : kNoColumn; }
 };
 
@@ -604,21 +663,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         bool ok = true;
         int use = 0;
-        while (work.next(t)) {
+        auto row_of = [&](const Tile &x) {
+            Row row = {-1, kNoColumn, 0.0f, 0.0f};
+            const int r = x.row * kTile + local;
+            if (x.kind == 0 && r < n) {
+                row.token = a.rows[r];
+                if (P != kGrads && a.labels) row.label = a.labels[r];
+                if constexpr (P == kDz) {
+                    row.lse = a.row_lse[r];
+                    if (a.row_grad) row.grad = a.row_grad[r];
+                }
+            }
+            return row;
+        };
+        Tile after = {};
+        Row row = {}, row_after = {};
+        bool more = work.next(t);
+        if (more) row = row_of(t);
+        for (; more; t = after, row = row_after) {
+            more = work.next(after);
+            if (more) row_after = row_of(after);
             const int acc = use & 1, r = t.row * kTile + local, c0 = t.col * a.width;
             const bool there = r < (t.kind ? a.cols : n);
             const uint32_t from = tmem + acc * kTile + (uint32_t(quarter * 32) << 16);
-            int token = -1;
-            if (t.kind == 0 && there) token = a.rows[r];
+            const int token = row.token;
             Targets hits;
-            float lse = 0.0f, factor = 0.0f;
-            if constexpr (P != kGrads) hits.start(a, token, a.first_col + c0);
-            if constexpr (P == kDz) {
-                if (there) {
-                    lse = a.lse[token] * 1.4426950408889634f;
-                    factor = (share + (a.by.grad_losses ? a.by.grad_losses[token] : 0.0f)) * over;
-                }
-            }
+            if constexpr (P != kGrads) hits.start(a, row, a.first_col + c0);
+            const float lse = row.lse, factor = (share + row.grad) * over;
             if (t.steps) ok = ok && barrier_wait(&sh.done[acc], (use >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
@@ -626,14 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if constexpr (P == kLoss) {
                 float top = -INFINITY, sum = 0.0f, hit = 0.0f;
                 const int chunks = min(a.width, a.cols - c0 + 31) / 32;
-#pragma unroll 1
-                for (int c = side; c < chunks; c += 2) {
-                    float v[32];
-                    read_columns(v, from + c * 32);
-                    const int at = c0 + c * 32;
-                    const bool some = __any_sync(0xffffffffu, hits.next < at + 32);
-                    reads_wait();
-                    if (some) {
+                auto reduce = [&](float(&v)[32], int at) {
+                    if (__any_sync(0xffffffffu, hits.next < at + 32)) {
                         while (hits.next < at + 32) {
                             // the other warp's chunks lie between
                             if (hits.next >= at) hit = fmaf(hits.weight(), pick(v, hits.next - at), hit);
@@ -647,24 +712,49 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     float m[4] = {top, top, top, top};
 #pragma unroll
-                    for (int e = 0; e < 32; e++) m[e & 3] = fmaxf(m[e & 3], v[e]);
-                    const float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-                    const float off = high * a.scale;
-                    float u[4] = {sum * exp2_fast(fmaf(top, a.scale, -off)), 0.0f, 0.0f, 0.0f};
-                    if (top == -INFINITY) u[0] = 0.0f;   // nothing yet
+                    for (int e = 0; e < 32; e += 2) m[e >> 1 & 3] = max_of_three(m[e >> 1 & 3], v[e], v[e + 1]);
+                    const float high = max_of_three(fmaxf(m[0], m[1]), m[2], m[3]), off = high * a.scale;
+                    const float kept = top == -INFINITY ? 0.0f : sum * exp2_fast(fmaf(top, a.scale, -off));
+                    exponentials(v, a.scale, off);
+                    Pair u[4] = {Pair(v[0], v[1]), Pair(v[2], v[3]), Pair(v[4], v[5]), Pair(v[6], v[7])};
 #pragma unroll
-                    for (int e = 0; e < 32; e++) u[e & 3] += exp2_fast(fmaf(v[e], a.scale, -off));
-                    sum = (u[0] + u[1]) + (u[2] + u[3]);
+                    for (int e = 8; e < 32; e += 2) u[e >> 1 & 3] = add(u[e >> 1 & 3], Pair(v[e], v[e + 1]));
+                    float x, y;
+                    add(add(u[0], u[1]), add(u[2], u[3])).get(x, y);
+                    sum = kept + (x + y);
                     top = high;
+                };
+                // the next chunk is on its way while one is reduced; behind the last it is the last again
+                float v[32], w[32];
+                const int last = side + ((chunks - 1 - side) & ~1);
+                if (side < chunks) {
+                    read_columns(v, from + side * 32);
+                    reads_wait();
+#pragma unroll 1
+                    for (int c = side;; c += 4) {
+                        read_columns(w, from + min(c + 2, last) * 32);
+                        reduce(v, c0 + c * 32);
+                        reads_wait();
+                        if (c + 2 > last) break;
+                        read_columns(v, from + min(c + 4, last) * 32);
+                        reduce(w, c0 + (c + 2) * 32);
+                        reads_wait();
+                        if (c + 4 > last) break;
+                    }
                 }
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_at_first(&sh.free_[acc]);
-                // what the second warp of a quarter found, of this tile and the next (nothing else is staged)
-                float(*other)[kHalf] = reinterpret_cast<float(*)[kHalf]>(staging) + 3 * acc;
-                const int place = quarter * 32 + lane;
-                if (side) other[0][place] = top, other[1][place] = sum, other[2][place] = hit;
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                // What the second warp of a quarter found.  It does not wait for the first, which is at most two tiles
+                // behind: three places and barriers in turn.  (Nothing else is staged.)
+                const int turn = use % 3, place = quarter * 32 + lane, id = 1 + 3 * quarter + turn;
+                float(*other)[kHalf] = reinterpret_cast<float(*)[kHalf]>(staging) + 3 * turn;
+                if (side) {
+                    other[0][place] = top, other[1][place] = sum, other[2][place] = hit;
+                    asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+                } else {
+                    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+                }
                 if (!side && there) {
                     const float far = other[0][place], both = fmaxf(top, far);
                     if (far > -INFINITY || other[1][place] != 0.0f) {   // it had a chunk
@@ -689,22 +779,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int c = side; c < chunks; c += 2) {
                     const int at = c0 + c * 64;
                     uint32_t packed[32];
+                    float both[2][32];
+                    if (t.steps) {
+                        read_columns(both[0], from + c * 64);
+                        read_columns(both[1], from + c * 64 + 32);
+                        reads_wait();
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         const int here = at + 32 * h;
-                        float v[32];
-                        if (t.steps) {
-                            read_columns(v, from + c * 64 + 32 * h);
-                            reads_wait();
-                        }
+                        float(&v)[32] = both[h];
                         if (!ok || !t.steps) {
 #pragma unroll
                             for (int e = 0; e < 32; e++) v[e] = ok ? 0.0f : nan;
                         }
                         if constexpr (P == kDz) {
                             const int column = a.first_col + here;
-#pragma unroll
-                            for (int e = 0; e < 32; e++) v[e] = exp2_fast(fmaf(v[e], a.scale, -lse));
+                            exponentials(v, a.scale, lse);
                             if (__any_sync(0xffffffffu, hits.next < column + 32)) {
                                 while (hits.next < column + 32) {
                                     const float q = hits.weight();
@@ -715,9 +806,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                 }
                                 __syncwarp();
                             }
-                            // rows past the last enter later sums: zeros
 #pragma unroll
-                            for (int e = 0; e < 32; e++) v[e] = there ? v[e] * factor : 0.0f;
+                            for (int e = 0; e < 32; e += 2)
+                                times(Pair(v[e], v[e + 1]), Pair(factor, factor)).get(v[e], v[e + 1]);
                         } else {
                             if (sums) {
                                 if (there) {
@@ -738,6 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         }
 #pragma unroll
                         for (int e = 0; e < 16; e++) packed[16 * h + e] = pack_two<T>(v[2 * e], v[2 * e + 1]);
+                    }
+                    if (P == kDz && !there) {   // rows past the last enter later sums: zeros
+#pragma unroll
+                        for (int e = 0; e < 32; e++) packed[e] = 0;
                     }
                     if (P == kDz || !sums) {
                         if (lane == 0) stores_read();   // of the chunk before
