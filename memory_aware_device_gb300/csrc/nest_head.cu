@@ -392,44 +392,45 @@ struct SumArgs {
     Scale by;
 };
 
-constexpr int kSumTile = 64, kSumCols = 32;
+constexpr int kSumTile = 64, kSumCols = 16;
 
-// Adds the parts of results whose summed index was split, in order, and rounds them: tiles of 64 rows x 32, turned
-// from columns to rows in shared memory.
+// Adds the parts of results whose summed index was split, in order, and rounds them: tiles of 64 rows x 16, turned
+// from columns to rows in shared memory.  The parts are read before the number of rows is known (the buffers
+// have whole tiles of rows).
 template <typename T>
 __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArgs a) {
     __shared__ float tile[kSumTile][kSumCols + 1];
     pdl_wait();
     pdl_trigger();
-    const int n = *a.live, kind = int(blockIdx.x) >= a.first_block, across = (a.cols + kSumCols - 1) / kSumCols;
-    const int at = int(blockIdx.x) - (kind ? a.first_block : 0), rows = kind ? a.piece_rows : n;
+    const int kind = int(blockIdx.x) >= a.first_block, across = (a.cols + kSumCols - 1) / kSumCols;
+    const int at = int(blockIdx.x) - (kind ? a.first_block : 0);
     const int r0 = at / across * kSumTile, c0 = at % across * kSumCols;
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const float *from = a.sums[kind] + int64_t(c0 + y) * a.pitch[kind] + r0 + x;
+    const int64_t part = int64_t(a.cols) * a.pitch[kind];
+    constexpr int kPer = kSumCols / 4;
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; i++) v[i] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < a.splits[kind]; s++) {
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (c0 + y + 4 * i < a.cols) v[i] += from[s * part + int64_t(4 * i) * a.pitch[kind]];
+    }
+    const int n = *a.live, rows = kind ? a.piece_rows : n;
     if (r0 >= rows) return;
     const int e = scale_exponent(a.by, share_of(a.by, n));
     const float unit = ldexpf(1.0f / a.by.lift, e);
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    const float *from = a.sums[kind] + int64_t(c0) * a.pitch[kind] + r0 + x;
-    const int64_t part = int64_t(a.cols) * a.pitch[kind];
-    if (r0 + x < rows) {
-        float v[kSumCols / 4];
 #pragma unroll
-        for (int i = 0; i < kSumCols / 4; i++) v[i] = 0.0f;
-#pragma unroll 2
-        for (int s = 0; s < a.splits[kind]; s++) {
-#pragma unroll
-            for (int i = 0; i < kSumCols / 4; i++)
-                if (c0 + y + 4 * i < a.cols) v[i] += from[s * part + int64_t(y + 4 * i) * a.pitch[kind]];
-        }
-#pragma unroll
-        for (int i = 0; i < kSumCols / 4; i++) tile[x][y + 4 * i] = v[i] * unit;
-    }
+    for (int i = 0; i < kPer; i++) tile[x][y + 4 * i] = v[i] * unit;
     __syncthreads();
     const int c = threadIdx.x & (kSumCols - 1);
     for (int r = threadIdx.x / kSumCols; r < kSumTile && r0 + r < rows; r += 256 / kSumCols) {
         if (c0 + c < a.cols) {
             const int64_t row = kind ? r0 + r : a.rows[r0 + r];
-            const T v = from_f32<T>(tile[r][c]);
-            a.out[kind][row * a.cols + c0 + c] = reinterpret_cast<const uint16_t &>(v);
+            const T z = from_f32<T>(tile[r][c]);
+            a.out[kind][row * a.cols + c0 + c] = reinterpret_cast<const uint16_t &>(z);
         }
     }
 }

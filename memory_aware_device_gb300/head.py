@@ -70,53 +70,57 @@ def _described(*fields):
 
 class _Inputs:
     """The checked inputs of a call: their description and their addresses."""
+    __slots__ = ("device", "shape", "used", "ref", "pointers")
 
     def __init__(self, hidden, weight, index, teacher, mask, temperature):
         torch = train._torch or train._load_torch()
-        dtype = train._codes.get(hidden.dtype)
-        if dtype not in (BF16, F16) or weight.dtype is not hidden.dtype:
-            raise TypeError(f"hidden is {hidden.dtype} and weight {weight.dtype}: both bfloat16 or both float16 are "
-                            "supported")
-        if hidden.dim() != 2 or weight.dim() != 2 or hidden.shape[1] != weight.shape[1]:
+        if _lib is None:
+            lib()
+        kind = hidden.dtype
+        dtype = train._codes.get(kind)
+        if dtype not in (BF16, F16) or weight.dtype is not kind:
+            raise TypeError(f"hidden is {kind} and weight {weight.dtype}: both bfloat16 or both float16 are supported")
+        shape, across = self.shape = hidden.shape, weight.shape
+        if len(shape) != 2 or len(across) != 2 or shape[1] != across[1]:
             raise ValueError(f"hidden must be [tokens, width] and weight [vocabulary, width], not of shapes "
-                             f"{tuple(hidden.shape)} and {tuple(weight.shape)}")
+                             f"{tuple(shape)} and {tuple(across)}")
         dev = self.device = hidden.device
         if weight.device != dev:
             raise ValueError(f"hidden is on {dev}, weight on {weight.device}")
-        T, D = hidden.shape
-        self.shape = hidden.shape, weight.shape
-        if index.dtype is torch.int64:
+        T, D = shape
+        kind = index.dtype
+        if kind is torch.int64:
             wide = I64
-        elif index.dtype is torch.int32:
+        elif kind is torch.int32:
             wide = I32
         else:
-            raise TypeError(f"{'labels' if teacher is None else 'ids'} are {index.dtype}: int64 and int32 are supported")
-        k, kind = 0, F32
+            raise TypeError(f"{'labels' if teacher is None else 'ids'} are {kind}: int64 and int32 are supported")
+        k, listed = 0, F32
         if teacher is None:
-            _want(index, "labels", index.dtype, (T,), dev)
+            _want(index, "labels", kind, (T,), dev)
+            second = third = None
         else:
             k = index.shape[-1] if index.dim() == 2 else 0
             if not 1 <= k <= MAX_K:
                 raise ValueError(f"ids must be [tokens, k] with k from 1 to {MAX_K}, not of shape {tuple(index.shape)}")
-            kind = train._type(teacher, "teacher")
-            _want(index, "ids", index.dtype, (T, k), dev)
+            listed = train._type(teacher, "teacher")
+            _want(index, "ids", kind, (T, k), dev)
             _want(teacher, "teacher", teacher.dtype, (T, k), dev)
+            second, third = teacher.data_ptr(), None
             if mask is not None:
                 if mask.dtype not in (torch.bool, torch.uint8):
                     raise TypeError(f"mask is {mask.dtype}: bool and uint8 are supported")
-                _want(mask, "mask", mask.dtype, (T,), dev)
+                third = _want(mask, "mask", mask.dtype, (T,), dev).data_ptr()
         self.used = (hidden, weight, index, teacher, mask)
-        self.ref = _described(T, weight.shape[0], D, *hidden.stride(), *weight.stride(), dtype, wide, k, kind, temperature)
-        self.pointers = (hidden.data_ptr(), weight.data_ptr(), index.data_ptr(),
-                         None if teacher is None else teacher.data_ptr(), None if mask is None else mask.data_ptr())
-        lib()
+        self.ref = _described(T, across[0], D, *hidden.stride(), *weight.stride(), dtype, wide, k, listed, temperature)
+        self.pointers = (hidden.data_ptr(), weight.data_ptr(), index.data_ptr(), second, third)
 
     def workspace(self, size_of):
         """New memory, of the stream that the call is made on."""
         size = size_of(self.ref, self.pointers[1])
         if not size:   # the call says which limit is broken
             _check(_lib.nest_head_loss(self.ref, *self.pointers, *[None] * 5, 0, None), "nest_head_loss")
-        return train._torch.empty(size, dtype=train._torch.uint8, device=self.device)
+        return train._torch.empty(size, dtype=train._torch.uint8, device=self.device), size
 
 
 def _forward(x: _Inputs, out, stream) -> HeadLoss:
@@ -124,18 +128,20 @@ def _forward(x: _Inputs, out, stream) -> HeadLoss:
     guard = _enter(dev, stream, () if stream is None else (*x.used, *(out or ())))
     given = out is not None
     try:
+        f32 = torch.float32
         if given:
-            _want(out.loss, "out.loss", torch.float32, (), dev)
-            _want(out.losses, "out.losses", torch.float32, (T,), dev)
-            _want(out.lse, "out.lse", torch.float32, (T,), dev)
+            _want(out.loss, "out.loss", f32, (), dev)
+            _want(out.losses, "out.losses", f32, (T,), dev)
+            _want(out.lse, "out.lse", f32, (T,), dev)
             _want(out.tokens, "out.tokens", torch.int32, (1,), dev)
         else:
-            f = dict(dtype=torch.float32, device=dev)
-            out = HeadLoss(torch.empty((), **f), torch.empty(T, **f), torch.empty(T, **f),
-                           torch.empty(1, dtype=torch.int32, device=dev))
-        ws = x.workspace(_lib.nest_head_loss_workspace_size)
-        rc = _lib.nest_head_loss(x.ref, *x.pointers, out.loss.data_ptr(), out.losses.data_ptr(), out.lse.data_ptr(),
-                                 out.tokens.data_ptr(), ws.data_ptr(), ws.numel(), train._raw_stream(dev.index))
+            empty = torch.empty
+            out = HeadLoss(empty((), dtype=f32, device=dev), empty(T, dtype=f32, device=dev),
+                           empty(T, dtype=f32, device=dev), empty(1, dtype=torch.int32, device=dev))
+        loss, losses, lse, tokens = out
+        ws, size = x.workspace(_lib.nest_head_loss_workspace_size)
+        rc = _lib.nest_head_loss(x.ref, *x.pointers, loss.data_ptr(), losses.data_ptr(), lse.data_ptr(), tokens.data_ptr(),
+                                 ws.data_ptr(), size, train._raw_stream(dev.index))
     finally:
         if guard is not None:
             guard.leave()
@@ -162,11 +168,11 @@ def _backward(x: _Inputs, result, grad_loss, grad_losses, out, stream):
             out = (_want(out[0], "out[0]", kind, x.shape[0], dev), _want(out[1], "out[1]", kind, x.shape[1], dev))
         else:
             out = tuple(torch.empty(s, dtype=kind, device=dev) for s in x.shape)
-        ws = x.workspace(_lib.nest_head_backward_workspace_size)
+        ws, size = x.workspace(_lib.nest_head_backward_workspace_size)
         rc = _lib.nest_head_loss_backward(
             x.ref, *x.pointers, lse.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(),
             None if grad_losses is None else grad_losses.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
-            ws.data_ptr(), ws.numel(), train._raw_stream(dev.index))
+            ws.data_ptr(), size, train._raw_stream(dev.index))
     finally:
         if guard is not None:
             guard.leave()
