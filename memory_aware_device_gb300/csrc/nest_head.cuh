@@ -97,6 +97,14 @@ __device__ __forceinline__ uint32_t block_in_pair() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// One lane of the warp, the same every time, as a branch that the compiler knows to be one lane's: what the loops
+// around it compute stays in the registers of the whole warp, which the tensor cores' and the copies'
+// instructions take (a branch on the lane's number cost twice the time per stage).
+__device__ __forceinline__ bool one_lane() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ void pair_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     unsigned char *base = raw + ((1024 - (shared_address(raw) & 1023)) & 1023);   // the swizzle's alignment
     unsigned char *staging = base + kStages * kStage;
     Shared &sh = *reinterpret_cast<Shared *>(staging + kEpilogueWarps * kStaging);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t half = block_in_pair();
 
     if (threadIdx.x == 0) {
@@ -541,14 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t bytes = P == kGrads ? 2 * (kOperand + uint32_t(part) * kDepth * 2)
                                        : kDepth * 2 * ((both ? 2 : 1) * uint32_t(a.a_rows) + 2 * uint32_t(part));
     int ahead = 0;   // stages whose weights are on their way before the kernel before this one has ended
-    if (P != kGrads && a.early && warp == 0 && lane == 0) {
+    if (P != kGrads && a.early && warp == 0) {
         // one row tile: the pair's number is its first column tile
         const int x = int(blockIdx.x >> 1) * a.width + int(half) * part, steps = (a.depth + kDepth - 1) / kDepth;
-        for (; ahead < a.stages && ahead < steps; ahead++) {
-            if (half == 0) barrier_expect(&sh.full[ahead], bytes);
-            load_box(&maps.b, shared_address(base + ahead * stage + a.a_bytes), in_first(shared_address(&sh.full[ahead])),
-                     ahead * kDepth, a.first_col + x);
+        ahead = min(a.stages, steps);
+        if (one_lane()) {
+            for (int s = 0; s < ahead; s++) {
+                if (half == 0) barrier_expect(&sh.full[s], bytes);
+                load_box(&maps.b, shared_address(base + s * stage + a.a_bytes), in_first(shared_address(&sh.full[s])),
+                         s * kDepth, a.first_col + x);
+            }
         }
+        __syncwarp();
     }
     pdl_wait();
     pdl_trigger();
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                Tiles{(a.cols + kTile - 1) / kTile, col_tiles, a.splits[1], (n + kDepth - 1) / kDepth}, P == kGrads);
     Tile t = {};
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -573,13 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             constexpr int kKind = decltype(product)::value;   // 0, 1: grad hidden, grad weight; 2: logits
             const int y = t.row * kTile + int(half) * kHalf, x = t.col * a.width + int(half) * part;
             for (int kb = 0; kb < t.steps; kb++) {
-                ok = barrier_wait(&sh.empty[s], phase ^ 1);
+                ok = __all_sync(0xffffffffu, barrier_wait(&sh.empty[s], phase ^ 1));
                 if (!ok) break;
                 const uint32_t to = stage0 + uint32_t(s * stage), bar = full0 + s * 8;
                 const int k0 = (t.from + kb) * kDepth;
-                if constexpr (kKind == 2) {
-                    const bool begun = ahead > 0;
-                    if (begun) ahead--;
+                const bool begun = ahead > 0;
+                if (begun) ahead--;
+                if (!one_lane()) {
+                } else if constexpr (kKind == 2) {
                     if (half == 0 && !begun) barrier_expect(&sh.full[s], bytes);
                     if (both || half == 0) load_box(&maps.a, to, bar, k0, y);
                     if (!begun) load_box(&maps.b, to + a.a_bytes, bar, k0, a.first_col + x);
@@ -596,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     load_box(map, to + kOperand, bar, x, r);
                     if (part > 64) load_box(map, to + kOperand + kOperand / 2, bar, x + 64, r);
                 }
+                __syncwarp();
                 if (++s == stages) s = 0, phase ^= 1;
             }
         };
@@ -610,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint64_t start = nanoseconds();
             while (nanoseconds() - start < 10000000) __nanosleep(1000);
         }
-    } else if (warp == 1 && lane == 0 && half == 0) {
+    } else if (warp == 1 && half == 0) {
         int s = 0, use = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -621,20 +635,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             constexpr bool kA = decltype(a_along)::value, kB = decltype(b_along)::value;
             const uint64_t a0 = descriptor<kA>(stage0), b0 = descriptor<kB>(stage0 + a.a_bytes);
             for (int kb = 0, steps = t.steps; kb < steps; kb++) {
-                ok = barrier_wait(&sh.full[s], phase);
+                ok = __all_sync(0xffffffffu, barrier_wait(&sh.full[s], phase));
                 if (!ok) break;
                 fence_after();
                 const uint64_t da = a0 + uint32_t(s * step), db = b0 + uint32_t(s * step);
+                if (one_lane()) {
 #pragma unroll
-                for (int q = 0; q < kDepth / 16; q++) multiply(to, da + q * kStep<kA>, db + q * kStep<kB>, how, kb | q);
-                commit(&sh.empty[s]);
+                    for (int q = 0; q < kDepth / 16; q++) multiply(to, da + q * kStep<kA>, db + q * kStep<kB>, how, kb | q);
+                    commit(&sh.empty[s]);
+                }
+                __syncwarp();
                 if (++s == stages) s = 0, phase ^= 1;
             }
         };
         while (ok && work.next(t)) {
             if (!t.steps) continue;
             const int acc = use & 1;
-            ok = barrier_wait(&sh.free_[acc], ((use >> 1) & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, barrier_wait(&sh.free_[acc], ((use >> 1) & 1) ^ 1));
             use++;
             if (!ok) break;
             fence_after();
@@ -642,10 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if constexpr (P != kGrads) products(std::true_type{}, std::true_type{}, a.how[0], to);
             else if (t.kind == 0) products(std::true_type{}, std::false_type{}, a.how[0], to);
             else products(std::false_type{}, std::false_type{}, a.how[1], to);
-            if (ok) commit(&sh.done[acc]);
+            if (ok && one_lane()) commit(&sh.done[acc]);
+            __syncwarp();
         }
         if (!ok) {
-            commit(&sh.drain);
+            if (one_lane()) commit(&sh.drain);
+            __syncwarp();
             barrier_wait(&sh.drain, 0);
         }
     } else if (warp >= 2) {
