@@ -79,10 +79,10 @@ int nest_head_loss(const nest_head_desc *desc, const void *hidden, const void *w
  *   dz[t][v]          = g[t] h (p[t][v] - sum over j with index[t][j] = v of q[t][j])
  *   grad_hidden[t][d] = sum over v of dz[t][v] weight[v][d]
  *   grad_weight[v][d] = sum over live t of dz[t][v] hidden[t][d]
- * dz is rounded once to the inputs' type, relative to the power of two above the largest
- * finite |g[t] h| (and lifted by 2^15 in NEST_F16, which would lose small p otherwise), the
- * sums are in 32 bits and rounded once to the inputs' type.  Tokens that are not live have
- * gradient 0.
+ * dz is rounded once to the inputs' type - without grad_losses p - q, before the factor that
+ * all rows share, else relative to a power of two above every finite |g[t] h| - and lifted by
+ * 2^15 in NEST_F16, which would lose small p otherwise; the sums are in 32 bits and rounded
+ * once to the inputs' type.  Tokens that are not live have gradient 0.
  *   grad_hidden   DEVICE [T][D], grad_weight DEVICE [V][D], contiguous                   */
 int nest_head_loss_backward(const nest_head_desc *desc, const void *hidden, const void *weight, const void *index,
                             const void *teacher, const uint8_t *mask, const float *lse, const float *grad_loss,

@@ -420,8 +420,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
     }
     const int n = *a.live, rows = kind ? a.piece_rows : n;
     if (r0 >= rows) return;
-    const int e = scale_exponent(a.by, share_of(a.by, n));
-    const float unit = ldexpf(1.0f / a.by.lift, e);
+    const float unit = scaling_of(a.by, n).unit;
 #pragma unroll
     for (int i = 0; i < kPer; i++) tile[x][y + 4 * i] = v[i] * unit;
     __syncthreads();

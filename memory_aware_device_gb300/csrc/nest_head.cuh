@@ -372,23 +372,26 @@ struct Work {
     }
 };
 
-// Exponent e of the power of two that gradients are taken relative to: 2^e is above the size of every finite
-// factor, so that dz is below 1 (2^15 where it is lifted) and both scalings are exact.  By all lanes of a warp.
-__device__ __forceinline__ int scale_exponent(const Scale &s, float share) {
+// How dz is scaled: a row's factor is (base + its loss's gradient) * over, and the products are multiplied by unit.
+// Without gradients of single losses every row has the same factor, which is left to unit: p - q itself is
+// rounded, whose -1 at most labels is exact, and no rounding of the factor is common to all rows.  With them the
+// largest finite factor lies below 1 (2^15 where dz is lifted) by a power of two.  By all lanes of a warp.
+struct Scaling {
+    float base, over, unit;
+};
+__device__ __forceinline__ Scaling scaling_of(const Scale &s, int n) {
+    const float share = s.grad_loss && n ? *s.grad_loss / float(n) : 0.0f;
+    if (!s.grad_losses) return Scaling{1.0f, s.lift, share * s.heat / s.lift};
     float top = 0.0f;
-    if (s.grad_losses) {
-        for (int b = threadIdx.x & 31; b < s.blocks; b += 32) top = fmaxf(top, s.parts[b]);
+    for (int b = threadIdx.x & 31; b < s.blocks; b += 32) top = fmaxf(top, s.parts[b]);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (fabsf(share) < INFINITY) top += fabsf(share);
     top = fminf(top * s.heat, 8e37f);
     int e = 0;
     if (top > 0.0f) frexpf(top, &e);
-    return max(-100, e);
-}
-__device__ __forceinline__ float share_of(const Scale &s, int n) {
-    return s.grad_loss && n ? *s.grad_loss / float(n) : 0.0f;
+    e = max(-100, e);
+    return Scaling{share, ldexpf(s.lift, -e) * s.heat, ldexpf(1.0f / s.lift, e)};
 }
 
 // What a row of a tile needs from memory, loaded a tile ahead.
@@ -673,13 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         unsigned char *mine = staging + (warp - 2) * kStaging;
         const int local = int(half) * kHalf + quarter * 32 + lane;
         const float nan = __int_as_float(0x7fc00000);
-        float share = 0.0f, over = 1.0f, unit = 1.0f;
-        if constexpr (P != kLoss) {
-            share = share_of(a.by, n);
-            const int e = scale_exponent(a.by, share);
-            over = ldexpf(a.by.lift, -e) * a.by.heat;
-            unit = ldexpf(1.0f / a.by.lift, e);
-        }
+        Scaling by = {};
+        if constexpr (P != kLoss) by = scaling_of(a.by, n);
+        const float unit = by.unit;
         bool ok = true;
         int use = 0;
         auto row_of = [&](const Tile &x) {
@@ -708,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int token = row.token;
             Targets hits;
             if constexpr (P != kGrads) hits.start(a, row, a.first_col + c0);
-            const float lse = row.lse, factor = (share + row.grad) * over;
+            const float lse = row.lse, factor = (by.base + row.grad) * by.over;
             if (t.steps) ok = ok && barrier_wait(&sh.done[acc], (use >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();

@@ -231,6 +231,7 @@ def _functions():
             r = _forward(_Inputs(hidden, weight, index, teacher, mask, temperature), None, None)
             ctx.save_for_backward(hidden, weight, index, teacher, mask, *r)
             ctx.temperature = temperature
+            ctx.set_materialize_grads(False)   # of the two losses mostly one has a gradient
             ctx.mark_non_differentiable(r.lse, r.tokens)
             return tuple(r)
 
