@@ -46,7 +46,7 @@ extern "C" {
 #define NEST_I64 1
 
 typedef struct {
-    int64_t tokens;                      /* 0 <= T <= 2^24 */
+    int64_t tokens;                      /* 0 <= T <= 2^24, with ceil(T / 256) ceil(V / 128) <= 2^30 */
     int64_t vocab;                       /* 1 <= V <= 2^24 */
     int64_t hidden;                      /* 1 <= D <= 2^16 */
     int64_t hidden_row, hidden_col;      /* strides in elements, >= 0 */
@@ -83,7 +83,8 @@ int nest_head_loss(const nest_head_desc *desc, const void *hidden, const void *w
  * all rows share, else relative to a power of two above every finite |g[t] h| - and lifted by
  * 2^15 in NEST_F16, which would lose small p otherwise; the sums are in 32 bits and rounded
  * once to the inputs' type.  Tokens that are not live have gradient 0.
- *   grad_hidden   DEVICE [T][D], grad_weight DEVICE [V][D], contiguous                   */
+ *   grad_hidden   DEVICE [T][D], grad_weight DEVICE [V][D], contiguous; one of them may be
+ *                 NULL, which leaves out its product                                     */
 int nest_head_loss_backward(const nest_head_desc *desc, const void *hidden, const void *weight, const void *index,
                             const void *teacher, const uint8_t *mask, const float *lse, const float *grad_loss,
                             const float *grad_losses, void *grad_hidden, void *grad_weight, void *workspace,

@@ -35,7 +35,8 @@ struct RowArgs {
     float *losses, *lse;
     int32_t *live;
     // backward
-    uint16_t *grad;                        // [T][D]
+    int32_t clear;                         // the rows behind the last
+    uint16_t *grad;                        // [T][D], or NULL
     int32_t wide_grad;
     const float *lse_in;
     float *row_lse;                        // [n] lse log2(e)
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         if (a.ticket) *a.ticket = 0;
     }
     // rows from the last token to the end of its stage, which the weights' gradient reads
-    for (int64_t r = all + block * kWarps + warp; a.grad && r < (all + kDepth - 1) / kDepth * kDepth; r += a.blocks * kWarps)
+    for (int64_t r = all + block * kWarps + warp; a.clear && r < (all + kDepth - 1) / kDepth * kDepth; r += a.blocks * kWarps)
         clear_row(a.hidden.to + r * a.hidden.pitch, a.hidden.pitch, true, lane);
     float top = 0.0f;
     int at = before;
@@ -442,14 +443,17 @@ int check(const nest_head_desc *d) {
     if (d->k ? !valid_type(d->teacher_type) || !(d->temperature >= 0.0009765625f && d->temperature <= 1024.0f)
              : d->temperature != 1.0f)
         return NEST_E_INVALID;
-    if (d->tokens > 1 << 24 || d->vocab > 1 << 24 || d->hidden > 1 << 16 || d->k > kTeacherMost) return NEST_E_LIMITS;
+    // the last: tiles of logits are counted in 32 bits
+    if (d->tokens > 1 << 24 || d->vocab > 1 << 24 || d->hidden > 1 << 16 || d->k > kTeacherMost ||
+        cdiv(d->tokens, kTile) * cdiv(d->vocab, kHalf) > 1 << 30)
+        return NEST_E_LIMITS;
     return NEST_OK;
 }
 
 // Whether TMA reads the weights where they are.
 bool in_place(const nest_head_desc *d, const void *weight) {
     return (d->weight_col == 1 || d->hidden == 1) && d->weight_row % 8 == 0 && d->weight_row >= d->hidden &&
-           aligned_to(weight, 16);
+           d->weight_row < int64_t(1) << 38 && aligned_to(weight, 16);
 }
 
 constexpr int kPairs = kSMs / 2;
@@ -658,10 +662,11 @@ struct Call {
         r.losses = losses;
         r.lse = lse;
         r.live = live;
+        r.clear = lse_in != nullptr;
         r.grad = static_cast<uint16_t *>(grad);
         r.wide_grad = d->hidden % 8 == 0 && aligned_to(grad, 16);
         r.lse_in = lse_in;
-        r.row_lse = grad ? at<float>(l.row_lse) : nullptr;
+        r.row_lse = lse_in ? at<float>(l.row_lse) : nullptr;
         r.grad_losses = grad_losses;
         r.row_grad = grad_losses ? at<float>(l.row_grad) : nullptr;
         r.parts = grad_losses ? at<float>(l.parts) : nullptr;
@@ -788,8 +793,8 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
                             size_t ws_bytes, void *stream) {
     if (const int rc = check(d)) return rc;
     if (const int rc = check_inputs(d, hidden, weight, index, teacher, mask)) return rc;
-    if (!grad_weight || !aligned_to(grad_weight, 2) ||
-        (d->tokens && (!lse || !grad_hidden || !aligned_to(grad_hidden, 2))))
+    if ((!grad_weight && (!grad_hidden && d->tokens)) || (d->tokens && !lse) || !aligned_to(grad_weight, 2) ||
+        !aligned_to(grad_hidden, 2))
         return NEST_E_INVALID;
     Call c = {d, layout_of(d, weight, true), static_cast<unsigned char *>(workspace), stream};
     const Layout &l = c.l;
@@ -807,7 +812,7 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     if (!rc) rc = encode(&logits.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, l.width / 2);
     if (!rc) rc = encode(&grads.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, kDepth);
     if (!rc) rc = encode(&grads.d, d->dtype, h, d->hidden, l.pitch, l.packed, kDepth);
-    const bool wide_weight = d->hidden % 8 == 0 && aligned_to(grad_weight, 16);
+    const bool wide_weight = grad_weight && d->hidden % 8 == 0 && aligned_to(grad_weight, 16);
     if (!rc && wide_weight) rc = encode(&grads.out, d->dtype, grad_weight, d->hidden, d->vocab, d->hidden, 32);
     if (rc) return rc;
 
@@ -841,7 +846,7 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
         p.how[0] = instruction(d->dtype, true, false, p.width);
         p.how[1] = instruction(d->dtype, false, false, p.width);
         p.out[0] = out[0];
-        p.out[1] = out[1] + first * d->hidden;
+        p.out[1] = out[1] ? out[1] + first * d->hidden : nullptr;
         const int64_t tiles = (cdiv(d->tokens, kTile) * p.splits[0] + cdiv(p.cols, kTile) * p.splits[1]) * across;
         if ((rc = c.multiply(kGrads, grads, p, tiles))) return rc;
     }
@@ -852,8 +857,9 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     s.cols = g.depth;
     s.by = g.by;
     const int64_t wide = cdiv(d->hidden, kSumCols);
-    const int64_t blocks[2] = {g.sums[0] ? cdiv(d->tokens, kSumTile) * wide : 0,
-                               g.sums[1] ? cdiv(d->vocab, kSumTile) * wide : 0};
+    const int64_t blocks[2] = {g.sums[0] && out[0] ? cdiv(d->tokens, kSumTile) * wide : 0,
+                               g.sums[1] && out[1] ? cdiv(d->vocab, kSumTile) * wide : 0};
+    if (!blocks[0] && !blocks[1]) return NEST_OK;
     s.piece_rows = int32_t(d->vocab);
     s.first_block = int32_t(blocks[0]);
     for (int i = 0; i < 2; i++) {

@@ -81,7 +81,7 @@ struct GemmArgs {
     const float *row_lse;     // dz: [n], lse log2(e)
     const float *row_grad;    // dz: [n], NULL = 0: the gradient of each token's loss
     Scale by;                 // dz, grads
-    // grads: hidden, weight (of the piece)
+    // grads: hidden, weight (of the piece); NULL: not wanted
     uint16_t *out[2];
     int32_t wide[2];          // rows of out are 16-byte aligned
     int32_t splits[2];        // parts of the summed index
@@ -570,11 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
     const uint32_t tmem = sh.tmem;
     const int n = *a.live;
-    const int row_tiles = P == kGrads ? (n + kTile - 1) / kTile : max(1, (n + kTile - 1) / kTile);
+    const int row_tiles = P != kGrads ? max(1, (n + kTile - 1) / kTile) : a.out[0] ? (n + kTile - 1) / kTile : 0;
     Work work;
     work.start(Tiles{row_tiles, col_tiles, P == kGrads ? a.splits[0] : 1,
                      ((P == kGrads ? a.cols : a.depth) + kDepth - 1) / kDepth},
-               Tiles{(a.cols + kTile - 1) / kTile, col_tiles, a.splits[1], (n + kDepth - 1) / kDepth}, P == kGrads);
+               Tiles{a.out[1] ? (a.cols + kTile - 1) / kTile : 0, col_tiles, a.splits[1], (n + kDepth - 1) / kDepth}, P == kGrads);
     Tile t = {};
 
     if (warp == 0) {

@@ -151,8 +151,10 @@ def _forward(x: _Inputs, out, stream) -> HeadLoss:
     return out
 
 
-def _backward(x: _Inputs, result, grad_loss, grad_losses, out, stream):
+def _backward(x: _Inputs, result, grad_loss, grad_losses, out, stream, needs=(True, True)):
     torch, dev, (T, D) = train._torch, x.device, x.shape[0]
+    if not any(needs):
+        raise ValueError("neither gradient is needed")
     lse = _want(result.lse, "result.lse", torch.float32, (T,), dev)
     if grad_loss is not None:
         _want(grad_loss, "grad_loss", torch.float32, grad_loss.shape, dev)
@@ -165,20 +167,21 @@ def _backward(x: _Inputs, result, grad_loss, grad_losses, out, stream):
     given = out is not None
     try:
         if given:
-            out = (_want(out[0], "out[0]", kind, x.shape[0], dev), _want(out[1], "out[1]", kind, x.shape[1], dev))
+            out = tuple(_want(t, f"out[{i}]", kind, s, dev) if n else None
+                        for i, (t, s, n) in enumerate(zip(out, x.shape, needs)))
         else:
-            out = tuple(torch.empty(s, dtype=kind, device=dev) for s in x.shape)
+            out = tuple(torch.empty(s, dtype=kind, device=dev) if n else None for s, n in zip(x.shape, needs))
         ws, size = x.workspace(_lib.nest_head_backward_workspace_size)
         rc = _lib.nest_head_loss_backward(
             x.ref, *x.pointers, lse.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(),
-            None if grad_losses is None else grad_losses.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
-            ws.data_ptr(), size, train._raw_stream(dev.index))
+            None if grad_losses is None else grad_losses.data_ptr(),
+            *(None if t is None else t.data_ptr() for t in out), ws.data_ptr(), size, train._raw_stream(dev.index))
     finally:
         if guard is not None:
             guard.leave()
     _check(rc, "nest_head_loss_backward")
     if given:
-        train._written(out)
+        train._written(tuple(t for t in out if t is not None))
     return out
 
 
@@ -194,11 +197,12 @@ def cross_entropy(hidden, weight, labels, out: HeadLoss | None = None, stream=No
 
 
 def cross_entropy_backward(hidden, weight, labels, result: HeadLoss, grad_loss=None, grad_losses=None, out=None,
-                           stream=None):
+                           stream=None, needs=(True, True)):
     """nest_head_loss_backward with labels: (grad_hidden [T, D], grad_weight [V, D]), in the inputs'
     type, from the gradients of the loss (float32 scalar tensor) and of the losses (float32 [T]);
-    None counts as zero.  out: two contiguous tensors to write instead of new ones."""
-    return _backward(_Inputs(hidden, weight, labels, None, None, 1.0), result, grad_loss, grad_losses, out, stream)
+    None counts as zero.  out: two contiguous tensors to write instead of new ones.  needs: which of the
+    two gradients are computed (a frozen head's weights need none); None takes the other's place."""
+    return _backward(_Inputs(hidden, weight, labels, None, None, 1.0), result, grad_loss, grad_losses, out, stream, needs)
 
 
 def distill(hidden, weight, ids, teacher, temperature: float = 1.0, mask=None, out: HeadLoss | None = None,
@@ -215,11 +219,11 @@ def distill(hidden, weight, ids, teacher, temperature: float = 1.0, mask=None, o
 
 
 def distill_backward(hidden, weight, ids, teacher, result: HeadLoss, grad_loss=None, grad_losses=None,
-                     temperature: float = 1.0, mask=None, out=None, stream=None):
+                     temperature: float = 1.0, mask=None, out=None, stream=None, needs=(True, True)):
     """nest_head_loss_backward with a teacher (which gets no gradient), as `cross_entropy_backward`;
     temperature and mask as in the forward call."""
     return _backward(_Inputs(hidden, weight, ids, teacher, mask, temperature), result, grad_loss, grad_losses, out,
-                     stream)
+                     stream, needs)
 
 
 def _functions():
@@ -241,8 +245,8 @@ def _functions():
             hidden, weight, index, teacher, mask, *r = ctx.saved_tensors
             x = _Inputs(hidden, weight, index, teacher, mask, ctx.temperature)
             return (*_backward(x, HeadLoss(*r), None if grad_loss is None else grad_loss.contiguous(),
-                               None if grad_losses is None else grad_losses.contiguous(), None, None),
-                    None, None, None, None)
+                               None if grad_losses is None else grad_losses.contiguous(), None, None,
+                               ctx.needs_input_grad[:2]), None, None, None, None)
 
     return Loss
 

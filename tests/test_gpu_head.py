@@ -81,7 +81,10 @@ def both(x, seed=0, parts="both"):
 
 SIZES = [(1, 1, 1), (1, 2, 8), (2, 31, 3), (3, 255, 7), (16, 256, 64), (31, 513, 200), (127, 257, 65), (128, 256, 64),
          (129, 512, 63), (255, 1000, 128), (256, 1, 64), (257, 300, 72), (300, 5000, 192), (513, 769, 321), (1, 40000, 96),
-         (700, 33, 40), (64, 1024, 2048)]
+         (700, 33, 40), (64, 1024, 2048),
+         # tiles of 224, 160 and 192 columns; rounds of several tiles for few tokens; split sums of either gradient
+         (1, 17000, 4096), (40, 33000, 130), (300, 32000, 520), (9, 24000, 2048), (513, 20000, 1000), (8192, 1000, 64),
+         (5000, 700, 41)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
@@ -275,6 +278,52 @@ def test_pieces_of_the_vocabulary(k):
 def test_many_tiles_for_each_pair():
     both(made(2500, 9000, 640, "bf16"))
     both(made(1100, 3000, 2304, "fp16", k=50, temperature=2.0))
+
+
+def test_one_gradient_alone():
+    for k, (T, V, D) in itertools.product((0, 12), ((200, 900, 72), (3, 9000, 256), (3000, 600, 33), (16384, 9000, 64))):
+        x = made(T, V, D, "bf16", k=k, dead=0.2)
+        r, dl = forward(x), torch.ones((), device="cuda")
+        dh, dw = backward(x, r, dl)
+        one, none = backward(x, r, dl, needs=(True, False))
+        assert none is None and (one.double() - dh.double()).abs().max() <= 2.0 ** -7 * dh.abs().max().double()
+        none, one = backward(x, r, dl, needs=(False, True))
+        assert none is None and torch.equal(one, dw)
+        out = torch.empty_like(dw)
+        assert backward(x, r, dl, out=(None, out), needs=(False, True))[1] is out and torch.equal(out, dw)
+    h, w = x["hidden"].clone().requires_grad_(), x["weight"]
+    h.data[~x["mask"]] = 0
+    head.teacher_loss(h, w, x["ids"], x["teacher"], mask=x["mask"]).loss.backward()
+    assert torch.equal(h.grad, backward(x, r, dl, needs=(True, False))[0]) and w.grad is None
+    with pytest.raises(ValueError, match="neither"):
+        backward(x, r, dl, needs=(False, False))
+
+
+def test_weights_written_just_before():
+    """The kernel that reads the weights may start before the one ahead of it ends: not before the weights are
+    written, by an optimizer step whose kernels let the next start early too."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    for T, V, D in ((1, 30000, 512), (200, 20000, 256), (700, 8000, 128)):
+        x = made(T, V, D, "bf16")
+        w = [torch.nn.Parameter(x["weight"].clone()) for _ in range(2)]
+        grads = [torch.randn(V, D, generator=g, device="cuda") for _ in range(3)]
+        opts = [train.AdamW([t.detach()], [torch.empty_like(grads[0])]) for t in w]
+        got, want = [], []
+        for opt, t, losses, wait in ((opts[0], w[0], want, True), (opts[1], w[1], got, False)):
+            y = x | {"weight": t.detach()}
+            for n in range(6):
+                opt.grads[0].copy_(grads[n % 3])
+                opt.step(0.1)
+                if wait:
+                    torch.cuda.synchronize()
+                r = forward(y)
+                losses.append((r, backward(y, r, torch.ones((), device="cuda"))))
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        for (r, p), (s, q) in zip(want, got):
+            assert torch.equal(r.losses, s.losses) and torch.equal(p[0], q[0]) and torch.equal(p[1], q[1])
+        assert not torch.equal(want[0][0].losses, want[-1][0].losses)
 
 
 def test_offsets_beyond_32_bits():

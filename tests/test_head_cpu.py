@@ -56,7 +56,8 @@ def test_invalid_descriptions(kw):
     assert head.lib().nest_head_loss_workspace_size(C.byref(desc(**kw)), FAKE) == 0
 
 
-@pytest.mark.parametrize("kw", [dict(tokens=2 ** 24 + 1), dict(vocab=2 ** 24 + 1), dict(hidden=2 ** 16 + 1), dict(k=257)])
+@pytest.mark.parametrize("kw", [dict(tokens=2 ** 24 + 1), dict(vocab=2 ** 24 + 1), dict(hidden=2 ** 16 + 1), dict(k=257),
+                                dict(tokens=2 ** 24, vocab=2 ** 24)])
 def test_limits(kw):
     assert calls(desc(**kw)) == (nest.NEST_E_LIMITS,) * 2
     assert head.lib().nest_head_backward_workspace_size(C.byref(desc(**kw)), FAKE) == 0
@@ -72,6 +73,11 @@ def test_missing_and_misaligned_buffers():
     for kw in (dict(ws=None), dict(ws=FAKE + 16), dict(more=-1)):
         assert calls(desc(), **kw) == (nest.NEST_E_WORKSPACE,) * 2, kw
     assert head.lib().nest_head_loss(None, *[None] * 10, 0, None) == nest.NEST_E_INVALID
+    L, d = head.lib(), desc()
+    size = L.nest_head_backward_workspace_size(C.byref(d), FAKE)
+    for lse, dh, dw in ((None, FAKE, FAKE), (FAKE, None, None), (FAKE, FAKE + 1, FAKE), (FAKE, None, FAKE + 1)):
+        assert L.nest_head_loss_backward(C.byref(d), FAKE, FAKE, FAKE, None, None, lse, None, None, dh, dw, FAKE, size,
+                                         None) == nest.NEST_E_INVALID
 
 
 def test_workspace_sizes():
