@@ -273,92 +273,19 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(TeacherArgs
     }
 }
 
-struct JoinArgs {
-    const int32_t *count, *rows;
-    const float *part_max, *part_sum, *part_hit;
-    int64_t pitch;
-    int32_t tiles;
-    float scale;          // log2(e) / h
-    float heat, over;     // h, 1 / h
-    const float *entropy; // NULL with labels
-    float *losses, *lse, *loss;
-    float *sums;          // [blocks]
-    uint32_t *ticket;
-};
+constexpr int kJoinParts = 16;
 
-constexpr int kJoinRows = 32, kJoinParts = 16;
-
-// Joins the tiles' maxima and sums: 32 rows a block, 16 threads to a row, eight tiles at a time so that no load
-// waits for another; the last block adds the rows' losses in the blocks' order.
-__global__ void __launch_bounds__(kJoinRows *kJoinParts) join_kernel(JoinArgs a) {
-    constexpr int kAtOnce = 8;
-    __shared__ float sh_max[kJoinParts][kJoinRows + 1], sh_sum[kJoinParts][kJoinRows + 1],
-        sh_hit[kJoinParts][kJoinRows + 1];
-    __shared__ float sh_all[kJoinParts];
+// The join where one block has too many tokens for it: 32 rows a block, 16 threads to a row; the last block adds the
+// rows' losses in the blocks' order.
+__global__ void __launch_bounds__(kJoinRows *kJoinParts) join_kernel(const __grid_constant__ JoinArgs a) {
+    __shared__ JoinShared<kJoinParts> sh;
     __shared__ bool sh_last;
     pdl_wait();
     pdl_trigger();
     const int n = *a.count, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const int64_t first = int64_t(blockIdx.x) * kJoinRows, r = first + lane;
-    float top = -INFINITY, sum = 0.0f, hit = 0.0f;
-    if (r < n) {
-        for (int t0 = part; t0 < a.tiles; t0 += kJoinParts * kAtOnce) {
-            float high[kAtOnce], s[kAtOnce], h[kAtOnce], most = top;
-#pragma unroll
-            for (int i = 0; i < kAtOnce; i++) {
-                const int t = t0 + i * kJoinParts;
-                const int64_t at = int64_t(t) * a.pitch + r;
-                const bool in = t < a.tiles;
-                high[i] = in ? a.part_max[at] : -INFINITY;
-                s[i] = in ? a.part_sum[at] : 0.0f;
-                h[i] = in ? a.part_hit[at] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < kAtOnce; i++) most = fmaxf(most, high[i]);
-            sum *= top == most ? 1.0f : exp2_fast((top - most) * a.scale);
-            top = most;
-            // a tile without a finite value has a sum of NaN, which stays
-#pragma unroll
-            for (int i = 0; i < kAtOnce; i++) {
-                sum = fmaf(s[i], high[i] == top ? 1.0f : exp2_fast((high[i] - top) * a.scale), sum);
-                hit += h[i];
-            }
-        }
-    }
-    sh_max[part][lane] = top;
-    __syncthreads();
-    float high = -INFINITY;
-#pragma unroll
-    for (int p = 0; p < kJoinParts; p++) high = fmaxf(high, sh_max[p][lane]);
-    sh_sum[part][lane] = sum * (top == high ? 1.0f : exp2_fast((top - high) * a.scale));
-    sh_hit[part][lane] = hit;
-    __syncthreads();
-    if (part == 0) sh_max[0][lane] = high;
-    __syncthreads();
-    // a warp adds the parts of two rows
-    const int row = 2 * part + (lane >> 4), p = lane & 15;
-    sum = sh_sum[p][row];
-    hit = sh_hit[p][row];
-#pragma unroll
-    for (int o = 8; o; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        hit += __shfl_xor_sync(0xffffffffu, hit, o);
-    }
-    float loss = 0.0f;
-    if (p == 0 && first + row < n) {
-        const int t = a.rows[first + row];
-        // the largest logit's distance from the targets' first: the difference of near numbers is exact
-        const float most = sh_max[0][row], log_sum = logf(sum);
-        const float apart = fmaf(most - hit, a.over, log_sum) + (a.entropy ? a.entropy[t] : 0.0f);
-        loss = a.heat * a.heat * apart;
-        a.lse[t] = fmaf(most, a.over, log_sum);
-        a.losses[t] = loss;
-    }
-    loss += __shfl_xor_sync(0xffffffffu, loss, 16);
-    if (lane == 0) sh_all[part] = loss;
-    __syncthreads();
+    const float loss = join_rows<kJoinParts>(a, int64_t(blockIdx.x) * kJoinRows, n, part, lane, sh,
+                                             [] { __syncthreads(); });
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kJoinParts; w++) loss += sh_all[w];
         a.sums[blockIdx.x] = loss;
         sh_last = gridDim.x == 1 || last_ticket(a.ticket, gridDim.x);
     }
@@ -373,10 +300,10 @@ __global__ void __launch_bounds__(kJoinRows *kJoinParts) join_kernel(JoinArgs a)
     }
     all = fabsf(all) < INFINITY ? all + cut : all;
     all = warp_sum(all);
-    if (lane == 0) sh_all[part] = all;
+    if (lane == 0) sh.all[part] = all;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kJoinParts; w++) all += sh_all[w];
+        for (int w = 1; w < kJoinParts; w++) all += sh.all[w];
         *a.loss = n ? all / float(n) : 0.0f;
     }
 }
@@ -759,13 +686,6 @@ int nest_head_loss(const nest_head_desc *d, const void *hidden, const void *weig
     g.part_max = c.at<float>(c.l.part);
     g.part_sum = g.part_max + part;
     g.part_hit = g.part_sum + part;
-    if (d->tokens) {
-        Maps maps = {};
-        int rc = encode(&maps.a, d->dtype, c.at<void>(c.l.hidden), d->hidden, c.l.pitch, c.l.packed, g.a_rows);
-        if (!rc) rc = encode(&maps.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, c.l.width / 2);
-        if (!rc) rc = c.multiply(kLoss, maps, g, cdiv(d->tokens, kTile) * c.l.tiles);
-        if (rc) return rc;
-    }
     JoinArgs j = {};
     j.count = g.live;
     j.rows = g.rows;
@@ -783,6 +703,15 @@ int nest_head_loss(const nest_head_desc *d, const void *hidden, const void *weig
     j.loss = loss;
     j.sums = c.at<float>(c.l.sums);
     j.ticket = c.at<uint32_t>(c.l.ticket);
+    g.join = j;
+    g.join_here = d->tokens <= kJoinRows;
+    if (d->tokens) {
+        Maps maps = {};
+        int rc = encode(&maps.a, d->dtype, c.at<void>(c.l.hidden), d->hidden, c.l.pitch, c.l.packed, g.a_rows);
+        if (!rc) rc = encode(&maps.b, d->dtype, c.weight, d->hidden, d->vocab, c.weight_pitch, c.l.width / 2);
+        if (!rc) rc = c.multiply(kLoss, maps, g, cdiv(d->tokens, kTile) * c.l.tiles);
+        if (rc || g.join_here) return rc;
+    }
     return launch_kernel(join_kernel, dim3(unsigned(c.l.join)), dim3(kJoinRows * kJoinParts), 0, stream, 1,
                          "head join launch", j);
 }

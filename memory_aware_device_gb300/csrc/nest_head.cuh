@@ -59,6 +59,20 @@ struct Scale {
     float lift;                 // 2^15 in half precision
 };
 
+// What the tiles' maxima and sums are joined into.
+struct JoinArgs {
+    const int32_t *count, *rows;
+    const float *part_max, *part_sum, *part_hit;
+    int64_t pitch;
+    int32_t tiles;
+    float scale;          // log2(e) / h
+    float heat, over;     // h, 1 / h
+    const float *entropy; // NULL with labels
+    float *losses, *lse, *loss;
+    float *sums;          // [blocks]
+    uint32_t *ticket;
+};
+
 struct GemmArgs {
     const int32_t *live;      // n
     const int32_t *rows;      // [n] the live tokens
@@ -78,6 +92,8 @@ struct GemmArgs {
     int32_t k;
     float scale;              // log2(e) / h
     float *part_max, *part_sum, *part_hit;   // loss: [column tile][pitch]
+    int32_t join_here;        // loss: the last block joins the tiles of up to kJoinRows tokens
+    JoinArgs join;
     const float *row_lse;     // dz: [n], lse log2(e)
     const float *row_grad;    // dz: [n], NULL = 0: the gradient of each token's loss
     Scale by;                 // dz, grads
@@ -443,6 +459,83 @@ __device__ __forceinline__ float pick(const float (&v)[32], int i) {
 #pragma unroll
     for (int e = 0; e < 2; e++) t[e] = i & 2 ? t[e + 2] : t[e];
     return i & 1 ? t[1] : t[0];
+}
+
+constexpr int kJoinRows = 32;
+
+template <int PARTS>
+struct JoinShared {
+    float max[PARTS][kJoinRows + 1], sum[PARTS][kJoinRows + 1], hit[PARTS][kJoinRows + 1], all[PARTS];
+};
+
+// Joins the tiles' maxima and sums of 32 rows, PARTS warps with a lane to a row, eight tiles at a time so that no
+// load waits for another.  Returns the sum of the rows' losses to thread 0 of warp 0.  `sync`: a barrier of
+// these warps.
+template <int PARTS, typename Sync>
+__device__ __forceinline__ float join_rows(const JoinArgs &a, int64_t first, int n, int part, int lane,
+                                           JoinShared<PARTS> &sh, Sync sync) {
+    constexpr int kAtOnce = 8;
+    const int64_t r = first + lane;
+    float top = -INFINITY, sum = 0.0f, hit = 0.0f;
+    if (r < n) {
+        for (int t0 = part; t0 < a.tiles; t0 += PARTS * kAtOnce) {
+            float high[kAtOnce], s[kAtOnce], h[kAtOnce], most = top;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) {
+                const int t = t0 + i * PARTS;
+                const int64_t at = int64_t(t) * a.pitch + r;
+                const bool in = t < a.tiles;
+                high[i] = in ? __ldcg(a.part_max + at) : -INFINITY;
+                s[i] = in ? __ldcg(a.part_sum + at) : 0.0f;
+                h[i] = in ? __ldcg(a.part_hit + at) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) most = fmaxf(most, high[i]);
+            sum *= top == most ? 1.0f : exp2_fast((top - most) * a.scale);
+            top = most;
+            // a tile without a finite value has a sum of NaN, which stays
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) {
+                sum = fmaf(s[i], high[i] == top ? 1.0f : exp2_fast((high[i] - top) * a.scale), sum);
+                hit += h[i];
+            }
+        }
+    }
+    sh.max[part][lane] = top;
+    sync();
+    float high = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < PARTS; p++) high = fmaxf(high, sh.max[p][lane]);
+    sh.sum[part][lane] = sum * (top == high ? 1.0f : exp2_fast((top - high) * a.scale));
+    sh.hit[part][lane] = hit;
+    sync();
+    if (part == 0) sh.max[0][lane] = high;
+    sync();
+    // a warp adds the parts of 32 / PARTS rows
+    const int row = (kJoinRows / PARTS) * part + lane / PARTS, p = lane % PARTS;
+    sum = sh.sum[p][row];
+    hit = sh.hit[p][row];
+#pragma unroll
+    for (int o = PARTS / 2; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        hit += __shfl_xor_sync(0xffffffffu, hit, o);
+    }
+    float loss = 0.0f;
+    if (p == 0 && first + row < n) {
+        const int t = a.rows[first + row];
+        // the largest logit's distance from the targets' first: the difference of near numbers is exact
+        const float most = sh.max[0][row], log_sum = logf(sum);
+        const float apart = fmaf(most - hit, a.over, log_sum) + (a.entropy ? a.entropy[t] : 0.0f);
+        loss = a.heat * a.heat * apart;
+        a.lse[t] = fmaf(most, a.over, log_sum);
+        a.losses[t] = loss;
+    }
+    loss = warp_sum(loss);
+    if (lane == 0) sh.all[part] = loss;
+    sync();
+    if (part == 0 && lane == 0)
+        for (int w = 1; w < PARTS; w++) loss += sh.all[w];
+    return loss;
 }
 
 // 64 results of each of the warp's 32 rows to shared memory, 128 bytes a row with the 128-byte swizzle.
@@ -884,6 +977,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (t.steps) use++;
         }
         if (lane == 0) stores_done();
+        if (P == kLoss && a.join_here) {
+            // Few tokens: the last block joins what all blocks left, which saves a launch (32 tokens x 32000
+            // columns: 55 KB; for more, one block reads longer than a launch takes).
+            auto sync = [] { asm volatile("bar.sync 13, %0;" ::"n"(32 * kEpilogueWarps) : "memory"); };
+            auto &last = *reinterpret_cast<int *>(staging);
+            auto &room = *reinterpret_cast<JoinShared<kEpilogueWarps> *>(staging + 16);
+            sync();
+            if (warp == 2 && lane == 0) last = last_ticket(a.join.ticket, gridDim.x);
+            sync();
+            if (last) {
+                const float sum = join_rows<kEpilogueWarps>(a.join, 0, n, warp - 2, lane, room, sync);
+                if (warp == 2 && lane == 0) *a.join.loss = n ? sum / float(n) : 0.0f;
+            }
+        }
     }
 
     __syncwarp();

@@ -166,16 +166,20 @@ def _backward(x: _Inputs, result, grad_loss, grad_losses, out, stream, needs=(Tr
     guard = _enter(dev, stream, () if stream is None else (*x.used, lse, grad_loss, grad_losses, *(out or ())))
     given = out is not None
     try:
+        for_hidden, for_weight = needs
+        across, down = x.shape
         if given:
-            out = tuple(_want(t, f"out[{i}]", kind, s, dev) if n else None
-                        for i, (t, s, n) in enumerate(zip(out, x.shape, needs)))
+            first = _want(out[0], "out[0]", kind, across, dev) if for_hidden else None
+            second = _want(out[1], "out[1]", kind, down, dev) if for_weight else None
         else:
-            out = tuple(torch.empty(s, dtype=kind, device=dev) if n else None for s, n in zip(x.shape, needs))
+            first = torch.empty(across, dtype=kind, device=dev) if for_hidden else None
+            second = torch.empty(down, dtype=kind, device=dev) if for_weight else None
+        out = first, second
         ws, size = x.workspace(_lib.nest_head_backward_workspace_size)
         rc = _lib.nest_head_loss_backward(
             x.ref, *x.pointers, lse.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(),
-            None if grad_losses is None else grad_losses.data_ptr(),
-            *(None if t is None else t.data_ptr() for t in out), ws.data_ptr(), size, train._raw_stream(dev.index))
+            None if grad_losses is None else grad_losses.data_ptr(), None if first is None else first.data_ptr(),
+            None if second is None else second.data_ptr(), ws.data_ptr(), size, train._raw_stream(dev.index))
     finally:
         if guard is not None:
             guard.leave()
