@@ -171,6 +171,9 @@ def _backward(x: _Inputs, result, grad_loss, grad_losses, out, stream, needs=(Tr
         if given:
             first = _want(out[0], "out[0]", kind, across, dev) if for_hidden else None
             second = _want(out[1], "out[1]", kind, down, dev) if for_weight else None
+            read = x.pointers[:2]
+            if any(t is not None and t.numel() and t.data_ptr() in read for t in (first, second)):
+                raise ValueError("out holds an input: the gradients are written while the inputs are read")
         else:
             first = torch.empty(across, dtype=kind, device=dev) if for_hidden else None
             second = torch.empty(down, dtype=kind, device=dev) if for_weight else None
@@ -204,7 +207,8 @@ def cross_entropy_backward(hidden, weight, labels, result: HeadLoss, grad_loss=N
                            stream=None, needs=(True, True)):
     """nest_head_loss_backward with labels: (grad_hidden [T, D], grad_weight [V, D]), in the inputs'
     type, from the gradients of the loss (float32 scalar tensor) and of the losses (float32 [T]);
-    None counts as zero.  out: two contiguous tensors to write instead of new ones.  needs: which of the
+    None counts as zero.  out: two contiguous tensors to write instead of new ones, which share no memory
+    with the inputs.  needs: which of the
     two gradients are computed (a frozen head's weights need none); None takes the other's place."""
     return _backward(_Inputs(hidden, weight, labels, None, None, 1.0), result, grad_loss, grad_losses, out, stream, needs)
 

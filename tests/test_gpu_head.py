@@ -572,6 +572,8 @@ def test_refusals():
                  lambda: head.cross_entropy_backward(h, w, y, r, None, torch.ones(7, device="cuda")),
                  lambda: head.cross_entropy_backward(h, w, y, r, one, out=(h.clone().half(), w.clone())),
                  lambda: head.cross_entropy_backward(h, w, y, r, one, out=(h.clone(), w.T.contiguous().T)),
+                 lambda: head.cross_entropy_backward(h, w, y, r, one, out=(torch.empty_like(h), w)),
+                 lambda: head.cross_entropy_backward(h, w, y, r, one, out=(h, torch.empty_like(w))),
                  lambda: head.cross_entropy(h, w, y, out=r._replace(tokens=r.loss))]:
         with pytest.raises(ValueError):
             call()
