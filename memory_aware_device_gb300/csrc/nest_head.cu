@@ -385,17 +385,22 @@ bool in_place(const nest_head_desc *d, const void *weight) {
 
 constexpr int kPairs = kSMs / 2;
 
+// Stages in whose time a tile of gradients is written: with 4, 5, 7 and 10 those of 64 x 100000 x 1024 take 79, 86, 96
+// and 105 us, of 1 x 32000 x 4096 97, 95, 108 and 117 (with 3: 89 and 111).  Rows off alignment take longer: of 64 x 100000 x 1023 161 us with 10 and 144 with 16.
+int least_of(int64_t hidden) { return hidden % 8 == 0 ? 4 : 16; }
+
 // Parts of the summed index of the two gradients: one, unless there are fewer tiles than pairs of blocks or one
-// product's tiles are longer than an even share of all work.  A part is at least 16 stages (as long as
-// writing and reading its 256 KB of sums takes).
+// product's tiles are longer than an even share of all work.  A part is at least 24 stages: writing and reading
+// its 256 KB of sums takes as long (1000 x 5000 x 300: 21.0 us with both kernels, 23.0 with 16).
 void split(int64_t tokens, int64_t cols, int64_t hidden, int width, bool pieces, int32_t (&splits)[2]) {
+    constexpr int64_t kPart = 24;
     const int64_t across = cdiv(hidden, width), row_tiles[2] = {cdiv(tokens, kTile), cdiv(cols, kTile)};
-    const int64_t steps[2] = {cdiv(cols, kDepth), cdiv(tokens, kDepth)};
+    const int64_t steps[2] = {cdiv(cols, kDepth), cdiv(tokens, kDepth)}, least = least_of(hidden);
     int64_t share = 0;
-    for (int i = 0; i < 2; i++) share += row_tiles[i] * across * (steps[i] > kTileCost ? steps[i] : kTileCost);
+    for (int i = 0; i < 2; i++) share += row_tiles[i] * across * (steps[i] > least ? steps[i] : least);
     share = cdiv(share, kPairs);
     for (int i = 0; i < 2; i++) {
-        const int64_t most = cdiv(steps[i], share > 16 ? share : 16);
+        const int64_t most = cdiv(steps[i], share > kPart ? share : kPart);
         splits[i] = int32_t(most < 1 ? 1 : most);
     }
     if (pieces) splits[1] = 1;
@@ -754,6 +759,7 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
     for (int i = 0; i < 2; i++) {
         g.wide[i] = d->hidden % 8 == 0 && aligned_to(out[i], 16);
         g.splits[i] = l.splits[i];
+        g.least = least_of(d->hidden);
         g.sums[i] = l.grad_sums[i] ? c.at<float>(l.grad_sums[i]) : nullptr;
         g.sums_pitch[i] = l.sums_pitch[i];
     }

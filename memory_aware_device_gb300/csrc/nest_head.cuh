@@ -101,6 +101,7 @@ struct GemmArgs {
     uint16_t *out[2];
     int32_t wide[2];          // rows of out are 16-byte aligned
     int32_t splits[2];        // parts of the summed index
+    int32_t least;            // what a tile takes at least, in stages
     float *sums[2];           // [split][column][row], where results are not final; else NULL
     int64_t sums_pitch[2];
     int32_t add;              // a later piece: sums of grad hidden go on
@@ -313,15 +314,13 @@ struct Tile {
     int kind, row, col, split, from, steps;
 };
 
-// What a tile takes, in stages: its own, or those that fit in the time of writing its results.
-constexpr int kTileCost = 10;
-
 // One product's tiles in the order in which they are taken: for each part of the summed index, groups of
 // kGroup row tiles, column by column.
 struct Tiles {
     int rows, cols, splits, steps;
+    int least;   // stages in whose time a tile's results are written
     __device__ __forceinline__ int per() const { return (steps + splits - 1) / splits; }
-    __device__ __forceinline__ int cost() const { return max(per(), kTileCost); }
+    __device__ __forceinline__ int cost() const { return max(per(), least); }
     __device__ __forceinline__ int count() const { return rows * cols * splits; }
     __device__ __forceinline__ void at(int i, Tile &t) const {
         t.split = i / (rows * cols);
@@ -672,8 +671,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int row_tiles = P != kGrads ? max(1, (n + kTile - 1) / kTile) : a.out[0] ? (n + kTile - 1) / kTile : 0;
     Work work;
     work.start(Tiles{row_tiles, col_tiles, P == kGrads ? a.splits[0] : 1,
-                     ((P == kGrads ? a.cols : a.depth) + kDepth - 1) / kDepth},
-               Tiles{a.out[1] ? (a.cols + kTile - 1) / kTile : 0, col_tiles, a.splits[1], (n + kDepth - 1) / kDepth}, P == kGrads);
+                     ((P == kGrads ? a.cols : a.depth) + kDepth - 1) / kDepth, a.least},
+               Tiles{a.out[1] ? (a.cols + kTile - 1) / kTile : 0, col_tiles, a.splits[1], (n + kDepth - 1) / kDepth, a.least},
+               P == kGrads);
     Tile t = {};
 
     if (warp == 0) {
