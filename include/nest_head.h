@@ -41,7 +41,10 @@ extern "C" {
  *
  * Both: loss = the mean of losses over the n live tokens, 0 when n = 0; live = n.  Tokens
  * that are not live have losses and lse 0, and whatever their hidden states hold (NaN
- * included) reaches no result.  NaN in a live token's row gives it a NaN loss.          */
+ * included) reaches no result.  NaN in a live token's row gives it a NaN loss.  A logit of
+ * minus infinity adds nothing to lse; as a target's it makes the loss infinite, and a row that
+ * is nothing else has lse minus infinity and a NaN loss.  (Logits whose z log2(e) / h is
+ * beyond 32 bits give results that are not finite.)                                      */
 #define NEST_I32 0
 #define NEST_I64 1
 

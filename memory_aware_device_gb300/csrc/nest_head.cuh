@@ -492,7 +492,7 @@ __device__ __forceinline__ float join_rows(const JoinArgs &a, int64_t first, int
             for (int i = 0; i < kAtOnce; i++) most = fmaxf(most, high[i]);
             sum *= top == most ? 1.0f : exp2_fast((top - most) * a.scale);
             top = most;
-            // a tile without a finite value has a sum of NaN, which stays
+            // (a tile of minus infinity alone has a sum of 0, one with NaN a sum of NaN, which stays)
 #pragma unroll
             for (int i = 0; i < kAtOnce; i++) {
                 sum = fmaf(s[i], high[i] == top ? 1.0f : exp2_fast((high[i] - top) * a.scale), sum);
@@ -830,7 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     float m[4] = {top, top, top, top};
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) m[e >> 1 & 3] = max_of_three(m[e >> 1 & 3], v[e], v[e + 1]);
-                    const float high = max_of_three(fmaxf(m[0], m[1]), m[2], m[3]), off = high * a.scale;
+                    // no finite logit yet: 0 is subtracted, so that minus infinity gives exponentials of 0 (and NaN NaN)
+                    const float high = max_of_three(fmaxf(m[0], m[1]), m[2], m[3]);
+                    const float off = high == -INFINITY ? 0.0f : high * a.scale;
                     const float kept = top == -INFINITY ? 0.0f : sum * exp2_fast(fmaf(top, a.scale, -off));
                     exponentials(v, a.scale, off);
                     Pair u[4] = {Pair(v[0], v[1]), Pair(v[2], v[3]), Pair(v[4], v[5]), Pair(v[6], v[7])};
@@ -873,13 +875,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
                 }
                 if (!side && there) {
+                    // without a chunk: minus infinity, 0 and 0
                     const float far = other[0][place], both = fmaxf(top, far);
-                    if (far > -INFINITY || other[1][place] != 0.0f) {   // it had a chunk
-                        sum = sum * (top == both ? 1.0f : exp2_fast((top - both) * a.scale)) +
-                              other[1][place] * (far == both ? 1.0f : exp2_fast((far - both) * a.scale));
-                        top = both;
-                        hit += other[2][place];
-                    }
+                    sum = sum * (top == both ? 1.0f : exp2_fast((top - both) * a.scale)) +
+                          other[1][place] * (far == both ? 1.0f : exp2_fast((far - both) * a.scale));
+                    top = both;
+                    hit += other[2][place];
                     const int64_t at = int64_t(t.col) * a.pitch + r;
                     a.part_max[at] = top;
                     a.part_sum[at] = ok ? sum : nan;

@@ -1,0 +1,79 @@
+"""The output head's losses where the formulas meet infinities, extremes and long sums.  Bounds as in head_ref."""
+import itertools
+
+import pytest
+import torch
+
+import head_ref as ref
+from memory_aware_device_gb300 import build as nbuild
+from memory_aware_device_gb300 import head
+from test_gpu_head import INF, backward, forward, made, near
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    nbuild.build()
+
+
+def closed(T, V, D, dtype, closed_columns, k=0, dead=0.0, seed=0):
+    """(inputs whose logits of these columns are minus infinity, by a bias column; the same without those columns;
+    the open columns)"""
+    x = made(T, V, D, dtype, k=k, dead=dead, seed=seed)
+    x["hidden"][:, D - 1] = torch.where(torch.isnan(x["hidden"][:, D - 1]), x["hidden"][:, D - 1], 1.0)
+    keep = torch.ones(V, dtype=torch.bool, device="cuda")
+    for a, b in closed_columns:
+        keep[a:b] = False
+    columns = keep.nonzero()[:, 0]
+    name = "ids" if k else "labels"
+    at = x[name] % len(columns)
+    live = torch.ones_like(at, dtype=torch.bool) if k else x[name] >= 0
+    y = x | {"weight": x["weight"][columns], name: torch.where(live, at, -100)}
+    x[name] = torch.where(live, columns[at], -100)
+    x["weight"][~keep, D - 1] = -INF
+    return x, y, columns
+
+
+@pytest.mark.parametrize("dtype,k", [("bf16", 0), ("bf16", 7), ("fp16", 0), ("fp16", 40)])
+@pytest.mark.parametrize("T,V,ranges", [
+    (5, 300, [(0, 32)]), (5, 300, [(32, 64)]), (90, 300, [(0, 32)]), (90, 300, [(32, 64)]), (90, 300, [(0, 64)]),
+    (90, 300, [(64, 300)]), (90, 700, [(0, 256)]), (300, 2000, [(256, 1024)]), (300, 2000, [(0, 1999)]),
+    (300, 2000, [(1, 2000)]), (12, 2000, [(0, 777), (778, 2000)]), (257, 2000, [(0, 777), (778, 2000)]),
+    (40, 1000, [(i, i + 32) for i in range(0, 1000, 64)]), (40, 1000, [(i + 32, i + 64) for i in range(0, 960, 64)])])
+def test_columns_of_minus_infinity_add_nothing(T, V, ranges, dtype, k):
+    """As if they were not there: a part of the vocabulary that is closed by a bias.  (Of the bias itself the gradient
+    of the hidden states is 0 * -inf.)"""
+    D = 64
+    x, y, columns = closed(T, V, D, dtype, ranges, k=k, dead=0.2)
+    dl, r = torch.ones((), device="cuda"), forward(x)
+    want = ref.loss(y, dl)
+    assert int(r.tokens[0]) == want["tokens"]
+    for name in ("losses", "lse", "loss"):
+        near(getattr(r, name), want[name], want[name + "_off"], name)
+    dh, dw = backward(x, r, dl)
+    near(dh[:, :-1], want["dh"][:, :-1], want["dh_off"][:, :-1], "grad_hidden")
+    near(dw[columns], want["dw"], want["dw_off"], "grad_weight")
+    dw[columns] = 0
+    assert not dw.any()
+
+
+@pytest.mark.parametrize("T", [3, 80])
+def test_labels_in_closed_columns_and_rows_that_are_closed(T):
+    """A target that cannot be has an infinite loss; where nothing can be there is no loss."""
+    for ranges, k in itertools.product(([(0, 32)], [(32, 64)], [(0, 256)], [(256, 300)]), (0, 4)):
+        x, y, _ = closed(T, 300, 64, "bf16", ranges, k=k)
+        want = ref.loss(y)
+        name = "ids" if k else "labels"
+        x[name] = x[name].clone()
+        x[name][1] = ranges[0][0]
+        r = forward(x)
+        assert float(r.losses[1]) == INF and float(r.loss) == INF
+        others = torch.arange(T, device="cuda") != 1
+        near(r.losses[others], want["losses"][others], want["losses_off"][others], "losses")
+        near(r.lse, want["lse"], want["lse_off"], "lse")
+        x["weight"][:, 63] = -INF
+        r = forward(x)
+        assert torch.isnan(r.losses).all() and torch.isnan(r.loss) and (r.lse == -INF).all()
+        dh, dw = backward(x, r, torch.ones((), device="cuda"))
+        assert torch.isnan(dh).all() and torch.isnan(dw).all()
