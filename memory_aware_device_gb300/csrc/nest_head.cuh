@@ -833,7 +833,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     // no finite logit yet: 0 is subtracted, so that minus infinity gives exponentials of 0 (and NaN NaN)
                     const float high = max_of_three(fmaxf(m[0], m[1]), m[2], m[3]);
                     const float off = high == -INFINITY ? 0.0f : high * a.scale;
-                    const float kept = top == -INFINITY ? 0.0f : sum * exp2_fast(fmaf(top, a.scale, -off));
+                    // (a product with 0 too: the sum so far may be NaN, of logits that the maximum passes over)
+                    const float kept = top == high ? sum : sum * exp2_fast(fmaf(top, a.scale, -off));
                     exponentials(v, a.scale, off);
                     Pair u[4] = {Pair(v[0], v[1]), Pair(v[2], v[3]), Pair(v[4], v[5]), Pair(v[6], v[7])};
 #pragma unroll

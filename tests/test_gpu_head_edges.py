@@ -17,6 +17,23 @@ def built():
     nbuild.build()
 
 
+@pytest.mark.parametrize("T,V,D,first,count", [
+    (*size, *columns) for size, columns in itertools.product(
+        [(5, 600, 64), (70, 600, 64), (300, 1500, 72), (33, 40, 8)],
+        [(0, 32), (32, 32), (64, 32), (0, 1), (31, 2), (256, 32), (0, 256), (512, 64)]) if sum(columns) < size[1]])
+def test_nan_in_weights_reaches_every_loss(T, V, D, first, count):
+    """Wherever the columns lie in a tile, and whatever the columns beside them hold."""
+    for k in (0, 6):
+        x = made(T, V, D, "bf16", k=k)
+        x["labels" if not k else "ids"].fill_(V - 1)
+        x["weight"][first:first + count] = float("nan")
+        r = forward(x)
+        assert torch.isnan(r.losses).all() and torch.isnan(r.lse).all() and torch.isnan(r.loss)
+        assert int(r.tokens[0]) == T
+        dh, dw = backward(x, r, torch.ones((), device="cuda"))
+        assert torch.isnan(dh).all() and torch.isnan(dw[first:first + count]).all()
+
+
 def closed(T, V, D, dtype, closed_columns, k=0, dead=0.0, seed=0):
     """(inputs whose logits of these columns are minus infinity, by a bias column; the same without those columns;
     the open columns)"""
