@@ -111,6 +111,7 @@ class _Inputs:
                 if mask.dtype not in (torch.bool, torch.uint8):
                     raise TypeError(f"mask is {mask.dtype}: bool and uint8 are supported")
                 third = _want(mask, "mask", mask.dtype, (T,), dev).data_ptr()
+            temperature = float(temperature)   # as it is now: descriptions are kept by value
         self.used = (hidden, weight, index, teacher, mask)
         self.ref = _described(T, across[0], D, *hidden.stride(), *weight.stride(), dtype, wide, k, listed, temperature)
         self.pointers = (hidden.data_ptr(), weight.data_ptr(), index.data_ptr(), second, third)
@@ -222,7 +223,8 @@ def distill(hidden, weight, ids, teacher, temperature: float = 1.0, mask=None, o
     hidden, weight and out as for `cross_entropy`; ids [T, k] (int64 or int32, in any order, k up to
     256) and teacher [T, k] (float32, bfloat16 or float16): columns and the teacher's logits of them.
     A slot whose id is not in [0, V) or whose logit is minus infinity does not count; a token counts when
-    one of its slots does and mask [T] (bool or uint8) is None or True.  temperature: from 2^-10 to 2^10."""
+    one of its slots does and mask [T] (bool or uint8) is None or True.  temperature: a number from 2^-10 to
+    2^10 (of a tensor its value at the call, which waits for the GPU where the tensor is there)."""
     return _forward(_Inputs(hidden, weight, ids, teacher, mask, temperature), out, stream)
 
 
@@ -282,5 +284,6 @@ def label_loss(hidden, weight, labels) -> HeadLoss:
 
 
 def teacher_loss(hidden, weight, ids, teacher, temperature: float = 1.0, mask=None) -> HeadLoss:
-    """`distill` with gradients, as `label_loss`; the teacher's logits get none."""
-    return _differentiable(hidden, weight, ids, teacher, mask, temperature)
+    """`distill` with gradients, as `label_loss`; the teacher's logits and the temperature get none, and the
+    backward pass is at the temperature of this call."""
+    return _differentiable(hidden, weight, ids, teacher, mask, float(temperature))

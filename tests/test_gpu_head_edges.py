@@ -94,3 +94,20 @@ def test_labels_in_closed_columns_and_rows_that_are_closed(T):
         assert torch.isnan(r.losses).all() and torch.isnan(r.loss) and (r.lse == -INF).all()
         dh, dw = backward(x, r, torch.ones((), device="cuda"))
         assert torch.isnan(dh).all() and torch.isnan(dw).all()
+
+
+def test_temperatures_that_are_tensors():
+    """A temperature that is changed in place counts as it is at each call, and at the forward call for its gradient."""
+    x = made(50, 300, 64, "bf16", k=6)
+    dl, heat = torch.ones((), device="cuda"), torch.tensor(2.0)
+    for value in (2.0, 4.0, 0.5):
+        heat.fill_(value)
+        r, want = forward(x | {"temperature": heat}), forward(x | {"temperature": value})
+        assert torch.equal(r.losses, want.losses) and torch.equal(r.lse, want.lse)
+        grads = backward(x | {"temperature": value}, want, dl), backward(x | {"temperature": heat}, want, dl)
+        assert all(torch.equal(p, q) for p, q in zip(*grads))
+        h = x["hidden"].clone().requires_grad_()
+        s = head.teacher_loss(h, x["weight"], x["ids"], x["teacher"], temperature=heat)
+        heat.fill_(3.0)
+        s.loss.backward()
+        assert torch.equal(s.losses, want.losses) and torch.equal(h.grad, grads[0][0])

@@ -131,3 +131,13 @@ def test_the_64_bit_form_against_autograd(k):
     (dl.double() * loss + (dls.double() * losses).sum()).backward()
     for p, q in ((got["losses"], losses), (got["loss"], loss), (got["dh"], a.grad), (got["dw"], b.grad)):
         assert torch.allclose(p, q, rtol=1e-10, atol=1e-12)
+
+
+def test_a_temperature_is_taken_by_value():
+    """Of a tensor too, which may be changed in place between two calls."""
+    h, w = torch.zeros(3, 8, dtype=torch.bfloat16), torch.zeros(5, 8, dtype=torch.bfloat16)
+    ids, teacher, heat = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2), torch.tensor(2.0)
+    for value in (2.0, 4.0, 0.5):
+        heat.fill_(value)
+        x = head._Inputs(h, w, ids, teacher, None, heat)
+        assert C.cast(x.ref, C.POINTER(head.HeadDesc))[0].temperature == value
