@@ -243,7 +243,7 @@ def _functions():
         @staticmethod
         def forward(ctx, hidden, weight, index, teacher, mask, temperature):
             r = _forward(_Inputs(hidden, weight, index, teacher, mask, temperature), None, None)
-            ctx.save_for_backward(hidden, weight, index, teacher, mask, *r)
+            ctx.save_for_backward(hidden, weight, index, teacher, mask, r.lse)   # the losses may be changed in place
             ctx.temperature = temperature
             ctx.set_materialize_grads(False)   # of the two losses mostly one has a gradient
             ctx.mark_non_differentiable(r.lse, r.tokens)
@@ -252,9 +252,9 @@ def _functions():
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, grad_loss, grad_losses, _lse, _tokens):
-            hidden, weight, index, teacher, mask, *r = ctx.saved_tensors
+            hidden, weight, index, teacher, mask, lse = ctx.saved_tensors
             x = _Inputs(hidden, weight, index, teacher, mask, ctx.temperature)
-            return (*_backward(x, HeadLoss(*r), None if grad_loss is None else grad_loss.contiguous(),
+            return (*_backward(x, HeadLoss(None, None, lse, None), None if grad_loss is None else grad_loss.contiguous(),
                                None if grad_losses is None else grad_losses.contiguous(), None, None,
                                ctx.needs_input_grad[:2]), None, None, None, None)
 

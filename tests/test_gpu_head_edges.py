@@ -111,3 +111,32 @@ def test_temperatures_that_are_tensors():
         heat.fill_(3.0)
         s.loss.backward()
         assert torch.equal(s.losses, want.losses) and torch.equal(h.grad, grads[0][0])
+
+
+@pytest.mark.parametrize("k", [0, 5])
+def test_losses_changed_in_place_before_the_backward_pass(k):
+    """The backward pass reads lse alone: weighting the losses where they lie is no error, changing lse is."""
+    x = made(40, 200, 64, "bf16", k=k)
+    w = torch.rand(40, device="cuda")
+
+    def losses():
+        h = x["hidden"].clone().requires_grad_()
+        if k:
+            return h, head.teacher_loss(h, x["weight"], x["ids"], x["teacher"])
+        return h, head.label_loss(h, x["weight"], x["labels"])
+    h, r = losses()
+    (r.losses * w).sum().backward()
+    g, s = losses()
+    s.losses.mul_(w)
+    s.losses.sum().backward()
+    assert torch.equal(g.grad, h.grad)
+    h, r = losses()
+    (r.loss * 0.5).backward()
+    g, s = losses()
+    s.loss.mul_(0.5)
+    s.loss.backward()
+    assert torch.equal(g.grad, h.grad)
+    g, s = losses()
+    s.lse.add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        s.loss.backward()
