@@ -11,7 +11,8 @@
  *
  * Conventions are those of nest_train.h: the caller allocates every buffer, a call only
  * checks its arguments and enqueues kernels on the caller's stream, and the same inputs
- * give the same bits.
+ * give the same bits.  Results and workspace share no memory with the inputs or with each other:
+ * the kernels read the ones while they write the others (calls do not check it).
  */
 #ifndef NEST_HEAD_H
 #define NEST_HEAD_H

@@ -124,6 +124,42 @@ class _Inputs:
         return train._torch.empty(size, dtype=train._torch.uint8, device=self.device), size
 
 
+def _span(t):
+    """(first, behind the last) address of a tensor's numbers."""
+    at = t.data_ptr()
+    if t.is_contiguous():
+        return at, at + t.nbytes
+    return at, at + (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size()
+
+
+def _touches(low, high, t):
+    """Whether a row of t, a matrix of any strides, has numbers in these addresses (its rows are the steps of its
+    larger stride, and all between a row's first and last number counts as its own)."""
+    (inner, across), (outer, down) = sorted(zip(t.stride(), t.shape))
+    at, size = t.data_ptr(), t.element_size()
+    length, step = ((across - 1) * inner + 1) * size, outer * size
+    if not step:
+        return low < at + length and at < high
+    return max(0, (low - at - length) // step + 1) <= min(down - 1, (high - 1 - at) // step)
+
+
+def _apart(results, names, inputs):
+    """An error where a result shares memory with an input or with another result: the kernels read the
+    inputs while they write the results."""
+    spans = [(*_span(t), t) for t in inputs if t is not None]
+    for t, name in zip(results, names):
+        if t is None:
+            continue
+        low, high = _span(t)
+        if low == high:
+            continue
+        for first, end, other in spans:
+            if first < high and low < end and first != end and \
+                    (other.is_contiguous() or other.dim() != 2 or _touches(low, high, other)):
+                raise ValueError(f"{name} shares memory with an input or with another result")
+        spans.append((low, high, t))
+
+
 def _forward(x: _Inputs, out, stream) -> HeadLoss:
     torch, dev, T = train._torch, x.device, x.shape[0][0]
     guard = _enter(dev, stream, () if stream is None else (*x.used, *(out or ())))
@@ -135,6 +171,7 @@ def _forward(x: _Inputs, out, stream) -> HeadLoss:
             _want(out.losses, "out.losses", f32, (T,), dev)
             _want(out.lse, "out.lse", f32, (T,), dev)
             _want(out.tokens, "out.tokens", torch.int32, (1,), dev)
+            _apart(out, ("out.loss", "out.losses", "out.lse", "out.tokens"), x.used)
         else:
             empty = torch.empty
             out = HeadLoss(empty((), dtype=f32, device=dev), empty(T, dtype=f32, device=dev),
@@ -172,9 +209,7 @@ def _backward(x: _Inputs, result, grad_loss, grad_losses, out, stream, needs=(Tr
         if given:
             first = _want(out[0], "out[0]", kind, across, dev) if for_hidden else None
             second = _want(out[1], "out[1]", kind, down, dev) if for_weight else None
-            read = x.pointers[:2]
-            if any(t is not None and t.numel() and t.data_ptr() in read for t in (first, second)):
-                raise ValueError("out holds an input: the gradients are written while the inputs are read")
+            _apart((first, second), ("out[0]", "out[1]"), (*x.used, lse, grad_loss, grad_losses))
         else:
             first = torch.empty(across, dtype=kind, device=dev) if for_hidden else None
             second = torch.empty(down, dtype=kind, device=dev) if for_weight else None
@@ -200,7 +235,8 @@ def cross_entropy(hidden, weight, labels, out: HeadLoss | None = None, stream=No
     hidden [T, D] and weight [V, D] (any strides; both bfloat16 or both float16); labels [T] (int64 or
     int32): a token whose label is not in [0, V) does not count (-100, padding), whatever it holds.
     Weights whose rows are contiguous and 16-byte aligned are read in place, others are copied by
-    every call.  out: buffers to write instead of new ones."""
+    every call.  out: buffers to write instead of new ones, which share no memory with the inputs or each
+    other."""
     return _forward(_Inputs(hidden, weight, labels, None, None, 1.0), out, stream)
 
 
@@ -209,7 +245,7 @@ def cross_entropy_backward(hidden, weight, labels, result: HeadLoss, grad_loss=N
     """nest_head_loss_backward with labels: (grad_hidden [T, D], grad_weight [V, D]), in the inputs'
     type, from the gradients of the loss (float32 scalar tensor) and of the losses (float32 [T]);
     None counts as zero.  out: two contiguous tensors to write instead of new ones, which share no memory
-    with the inputs.  needs: which of the
+    with the inputs or each other.  needs: which of the
     two gradients are computed (a frozen head's weights need none); None takes the other's place."""
     return _backward(_Inputs(hidden, weight, labels, None, None, 1.0), result, grad_loss, grad_losses, out, stream, needs)
 

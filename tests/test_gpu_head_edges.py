@@ -140,3 +140,49 @@ def test_losses_changed_in_place_before_the_backward_pass(k):
     s.lse.add_(1)
     with pytest.raises(RuntimeError, match="inplace"):
         s.loss.backward()
+
+
+@pytest.mark.parametrize("k", [0, 4])
+def test_results_over_inputs_are_refused(k):
+    """Wherever in an input's memory they begin; a result between the rows of an input is not over it."""
+    T, V, D = 24, 80, 16
+    x = made(T, V, D, "bf16", k=k)
+    room = torch.zeros(T + V, 2 * D, dtype=torch.bfloat16, device="cuda")
+    hidden, weight = room[:T, :D], room[T:, :D]
+    hidden.copy_(x["hidden"])
+    weight.copy_(x["weight"])
+    x |= {"hidden": hidden, "weight": weight, "mask": torch.ones(T, dtype=torch.bool, device="cuda")}
+    name = "ids" if k else "labels"
+    r, dl, dls = forward(x), torch.ones((), device="cuda"), torch.ones(T, device="cuda")
+    dh, dw = torch.empty(T, D, dtype=torch.bfloat16, device="cuda"), torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    want = [t.clone() for t in (*r, *backward(x, r, dl, dls))]
+    flat, long = room.view(-1), torch.zeros(4000, dtype=torch.bfloat16, device="cuda")
+    index = long[400:].view(x[name].dtype)[:x[name].numel()].view(x[name].shape).copy_(x[name])
+    lse, rows, one = long.view(torch.float32)[100:100 + T], long.view(torch.float32)[200:200 + T], long.view(torch.float32)[300]
+    for y, result, first, second in [
+            (x, r, flat[D:D + T * D], dw), (x, r, dh, flat[3 * D:3 * D + V * D]), (x, r, dh, flat[(2 * T - 1) * D:][:V * D]),
+            (x | {name: index}, r, long[300:300 + T * D], dw), (x, r, dw.view(-1)[8:8 + T * D], dw),
+            (x | {"hidden": dw[-T:]}, r, dh, dw), (x, r._replace(lse=lse), long[190:190 + T * D], dw)]:
+        with pytest.raises(ValueError, match="shares memory"):
+            backward(y, result, dl, dls, out=(first.view(T, D), second.view(V, D)))
+    for at in (dict(dl=dl, dls=rows), dict(dl=one, dls=dls), dict(dl=one)):
+        with pytest.raises(ValueError, match="shares memory"):
+            backward(x, r, out=(long[230:230 + T * D].view(T, D), dw), **at)
+    good = head.HeadLoss(*(torch.empty_like(t) for t in r))
+    places = [good._replace(lse=good.losses), good._replace(loss=good.losses[3]),
+              good._replace(losses=flat.view(torch.float32)[2:2 + T]), good._replace(tokens=good.lse.view(torch.int32)[5:6])]
+    if k:
+        places += [good._replace(lse=x["teacher"].view(-1)[1:1 + T]), good._replace(losses=x["ids"].view(-1).view(torch.float32)[:T]),
+                   good._replace(tokens=x["mask"].view(torch.int32)[3:4])]
+    else:
+        places.append(good._replace(losses=x["labels"].view(torch.float32)[T:]))
+    for out in places:
+        with pytest.raises(ValueError, match="shares memory"):
+            forward(x, out=out)
+    # one token: its gradient may lie beside it in its row
+    y = {"hidden": hidden[:1], "weight": x["weight"], "labels": torch.zeros(1, dtype=torch.int64, device="cuda")}
+    s = forward(y)
+    plain = backward(y, s, dl)
+    assert all(torch.equal(p, q) for p, q in zip(plain, backward(y, s, dl, out=(room[:1, D:], dw))))
+    got = (*forward(x, out=good), *backward(x, good, dl, dls, out=(dh, dw)))
+    assert all(torch.equal(p, q) for p, q in zip(want, got))

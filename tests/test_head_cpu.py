@@ -1,6 +1,7 @@
 """Host-side checks of the output head's losses that need no GPU: the ABI, refusals, workspace sizes, and the
 64-bit form that the GPU tests compare against."""
 import ctypes as C
+import itertools
 import os
 import re
 
@@ -141,3 +142,28 @@ def test_a_temperature_is_taken_by_value():
         heat.fill_(value)
         x = head._Inputs(h, w, ids, teacher, None, heat)
         assert C.cast(x.ref, C.POINTER(head.HeadDesc))[0].temperature == value
+
+
+@pytest.mark.parametrize("strides", [(8, 1), (11, 1), (1, 5), (1, 9), (20, 2), (0, 1), (3, 1), (40, 0)])
+def test_results_that_touch_an_input(strides):
+    """Against the numbers of the input's rows one by one: what lies between two rows is free."""
+    rows, cols = 5, 8
+    room = torch.zeros(400, dtype=torch.bfloat16)
+    t = room.as_strided((rows, cols), strides, 100)
+    inner = min(strides)
+    taken = set()
+    for i in range(rows if strides[0] >= strides[1] else cols):
+        n = cols if strides[0] >= strides[1] else rows
+        taken |= set(range(100 + i * max(strides), 100 + i * max(strides) + (n - 1) * inner + 1))
+    for at, n in itertools.product(range(60, 340), (1, 2, 7, 30)):
+        try:
+            head._apart((None, room[at:at + n]), ("first", "second"), (None, t))
+            refused = False
+        except ValueError as e:
+            refused = "second shares memory" in str(e)
+        assert refused == bool(taken & set(range(at, at + n))), (at, n)
+    head._apart((room[120:120],), ("empty",), (t,))     # nothing is written, nothing read
+    head._apart((room[120:130],), ("result",), (t[:0], t[:, :0]))
+    with pytest.raises(ValueError, match="b shares memory"):
+        head._apart((room[:10], room[9:12]), ("a", "b"), ())
+    head._apart((room[:10], room[10:12]), ("a", "b"), ())
