@@ -205,6 +205,7 @@ constexpr int kTeacherMost = 256, kTeacherWarps = 8;
 
 // A warp per token: the softmax over the slots that count, and the slots in the order of their columns
 // (each slot's place is the number of slots before it), so that a tile of logits finds its own by bisection.
+// The temperature divides differences from the largest logit: the logits' own quotients may be beyond 32 bits.
 template <typename T>
 __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(TeacherArgs a) {
     __shared__ int32_t sh_id[kTeacherWarps][kTeacherMost];
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(TeacherArgs
             if (open && j < a.k) {
                 const int64_t c = a.wide_index ? static_cast<const int64_t *>(a.index)[t * a.k + j]
                                                : static_cast<const int32_t *>(a.index)[t * a.k + j];
-                const float v = to_f32(static_cast<const T *>(a.teacher)[t * a.k + j]) * a.over;
+                const float v = to_f32(static_cast<const T *>(a.teacher)[t * a.k + j]);
                 if (c >= 0 && c < a.vocab && v != -INFINITY) {
                     id[e] = int32_t(c);
                     x[e] = v;
@@ -242,7 +243,8 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(TeacherArgs
         float sum = 0.0f, p[kPer];
 #pragma unroll
         for (int e = 0; e < kPer; e++) {
-            p[e] = id[e] != kNoColumn ? expf(x[e] - top) : 0.0f;
+            x[e] = (x[e] - top) * a.over;
+            p[e] = id[e] != kNoColumn ? expf(x[e]) : 0.0f;
             sum += p[e];
         }
         sum = warp_sum(sum);
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(TeacherArgs
             if (j < a.k) {
                 const bool in = id[e] != kNoColumn;
                 const float q = in ? p[e] * over : 0.0f;
-                if (in) entropy += q * (x[e] - top - log_sum);
+                if (in && q != 0.0f) entropy += q * (x[e] - log_sum);   // q log q is 0 in the limit
                 int place = 0;
                 for (int i = 0; i < a.k; i++) {
                     const int32_t other = sh_id[warp][i];

@@ -186,3 +186,30 @@ def test_results_over_inputs_are_refused(k):
     assert all(torch.equal(p, q) for p, q in zip(plain, backward(y, s, dl, out=(room[:1, D:], dw))))
     got = (*forward(x, out=good), *backward(x, good, dl, dls, out=(dh, dw)))
     assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
+@pytest.mark.parametrize("temperature", [2.0 ** -10, 0.5, 0.7, 1.0, 3.0])
+@pytest.mark.parametrize("teacher", [torch.float32, torch.bfloat16])
+def test_extreme_teacher_logits_at_any_temperature(teacher, temperature):
+    """Whether a slot counts goes by its logit, not by what dividing it gives; the largest logits share the mass."""
+    low, high = torch.finfo(teacher).min, torch.finfo(teacher).max
+    x = made(60, 300, 64, "bf16", k=6, teacher=teacher, temperature=temperature)
+    dl = torch.ones((), device="cuda")
+
+    def same(rows, slots):
+        """The rows are as if their slots were those, of equal logits, and the others closed."""
+        r, y = forward(x), x | {"teacher": x["teacher"].clone()}
+        y["teacher"][rows] = -INF
+        y["teacher"][rows, slots] = 0
+        s = forward(y)
+        assert int(r.tokens[0]) == 60 and torch.equal(r.losses, s.losses) and torch.equal(r.loss, s.loss)
+        assert all(torch.equal(p, q) for p, q in zip(backward(x, r, dl), backward(y, s, dl)))
+    x["teacher"][:20] = low                      # nothing but the lowest: all slots alike
+    same(slice(0, 20), slice(0, 6))
+    x["teacher"][20:30] = low
+    x["teacher"][20:30, 2:4] = high              # two of the largest
+    same(slice(20, 30), slice(2, 4))
+    x["teacher"][30:40, 1] = high                # one, by more than any quotient holds
+    same(slice(30, 40), slice(1, 2))
+    x["teacher"][40] = -INF                      # closed at any temperature
+    assert int(forward(x).tokens[0]) == 59
