@@ -38,7 +38,7 @@ extern "C" {
  *   lse[t]    = log(sum over v of exp(z[t][v] / h))
  *   losses[t] = h^2 sum over j of q[t][j] (log q[t][j] - z[t][index[t][j]] / h + lse[t])
  * A column that is listed twice has the sum of both shares in the gradients (each slot has
- * its own log q in the loss).
+ * its own log q in the loss); one whose share is 0 in 32 bits adds nothing.
  *
  * Both: loss = the mean of losses over the n live tokens, 0 when n = 0; live = n.  Tokens
  * that are not live have losses and lse 0, and whatever their hidden states hold (NaN

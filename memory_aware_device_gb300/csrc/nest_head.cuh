@@ -817,8 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 auto reduce = [&](float(&v)[32], int at) {
                     if (__any_sync(0xffffffffu, hits.next < at + 32)) {
                         while (hits.next < at + 32) {
-                            // the other warp's chunks lie between
-                            if (hits.next >= at) hit = fmaf(hits.weight(), pick(v, hits.next - at), hit);
+                            // the other warp's chunks lie between; a share of 0 takes nothing of minus infinity
+                            if (const float q = hits.weight(); hits.next >= at && q != 0.0f)
+                                hit = fmaf(q, pick(v, hits.next - at), hit);
                             hits.advance();
                         }
                         __syncwarp();

@@ -213,3 +213,18 @@ def test_extreme_teacher_logits_at_any_temperature(teacher, temperature):
     same(slice(30, 40), slice(1, 2))
     x["teacher"][40] = -INF                      # closed at any temperature
     assert int(forward(x).tokens[0]) == 59
+
+
+@pytest.mark.parametrize("T", [10, 90])
+def test_listed_columns_of_share_zero_add_nothing(T):
+    """Where the model's logit is minus infinity too: as if they were not listed."""
+    x, _, columns = closed(T, 300, 64, "bf16", [(0, 40), (100, 290)], k=6)
+    y = x | {"teacher": x["teacher"].clone()}
+    x["ids"][:, 2], x["ids"][::2, 4] = 17, 288
+    x["teacher"][:, 2], x["teacher"][::2, 4] = -1e9, -2000.0
+    y["teacher"][:, 2], y["teacher"][::2, 4] = -INF, -INF
+    r, s, dl = forward(x), forward(y), torch.ones((), device="cuda")
+    assert torch.isfinite(r.losses).all()
+    assert torch.equal(r.losses, s.losses) and torch.equal(r.loss, s.loss) and torch.equal(r.lse, s.lse)
+    p, q = backward(x, r, dl), backward(y, s, dl)
+    assert torch.equal(p[0][:, :-1], q[0][:, :-1]) and torch.equal(p[1], q[1])
