@@ -393,19 +393,22 @@ int least_of(int64_t hidden) { return hidden % 8 == 0 ? 4 : 16; }
 
 // Parts of the summed index of the two gradients: one, unless there are fewer tiles than pairs of blocks or one
 // product's tiles are longer than an even share of all work.  A part is at least 24 stages: writing and reading
-// its 256 KB of sums takes as long (1000 x 5000 x 300: 21.0 us with both kernels, 23.0 with 16).
+// its 256 KB of sums takes as long (1000 x 5000 x 300: 21.0 us with both kernels, 23.0 with 16).  And at most 2048
+// (131072 tokens or columns): what the tensor cores' additions cut off, 0.26 to 0.30 * 2^-24 of the sum per 16 products
+// in the mean (over_heat), is then up to 1.5e-4 of it, below the half step of 2^-11 or 2^-8 to which it is rounded.
 void split(int64_t tokens, int64_t cols, int64_t hidden, int width, bool pieces, int32_t (&splits)[2]) {
-    constexpr int64_t kPart = 24;
+    constexpr int64_t kPart = 24, kLongest = 2048;
     const int64_t across = cdiv(hidden, width), row_tiles[2] = {cdiv(tokens, kTile), cdiv(cols, kTile)};
     const int64_t steps[2] = {cdiv(cols, kDepth), cdiv(tokens, kDepth)}, least = least_of(hidden);
     int64_t share = 0;
     for (int i = 0; i < 2; i++) share += row_tiles[i] * across * (steps[i] > least ? steps[i] : least);
     share = cdiv(share, kPairs);
+    if (share < kPart) share = kPart;
     for (int i = 0; i < 2; i++) {
-        const int64_t most = cdiv(steps[i], share > kPart ? share : kPart);
+        // with pieces the weights' sums are added up once per piece: no more parts than their length asks for
+        const int64_t part = share < kLongest && !(pieces && i == 1) ? share : kLongest, most = cdiv(steps[i], part);
         splits[i] = int32_t(most < 1 ? 1 : most);
     }
-    if (pieces) splits[1] = 1;
 }
 
 // Columns of a tile of logits: the multiple of `step` for which the rounds of all pairs take least, counting 900
@@ -765,6 +768,32 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
         g.sums[i] = l.grad_sums[i] ? c.at<float>(l.grad_sums[i]) : nullptr;
         g.sums_pitch[i] = l.sums_pitch[i];
     }
+    const bool pieces = l.piece < d->vocab;
+    // adds the parts of the wanted results: the hidden states' gradient, and that of `rows` rows of the weights
+    auto sums = [&](bool for_hidden, bool for_weight, int64_t rows, uint16_t *to) {
+        if (!for_hidden && !for_weight) return int(NEST_OK);
+        SumArgs s = {};
+        s.live = g.live;
+        s.rows = g.rows;
+        s.cols = g.depth;
+        s.by = g.by;
+        const int64_t wide = cdiv(d->hidden, kSumCols);
+        const int64_t blocks[2] = {for_hidden ? cdiv(d->tokens, kSumTile) * wide : 0,
+                                   for_weight ? cdiv(rows, kSumTile) * wide : 0};
+        if (!blocks[0] && !blocks[1]) return int(NEST_OK);
+        s.piece_rows = int32_t(rows);
+        s.first_block = int32_t(blocks[0]);
+        for (int i = 0; i < 2; i++) {
+            s.splits[i] = g.splits[i];
+            s.sums[i] = g.sums[i];
+            s.pitch[i] = g.sums_pitch[i];
+            s.out[i] = i ? to : out[0];
+        }
+        const dim3 grid(unsigned(blocks[0] + blocks[1]));
+        return d->dtype == NEST_BF16
+                   ? launch_kernel(sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, 1, "head sums launch", s)
+                   : launch_kernel(sum_kernel<__half>, grid, dim3(256), 0, stream, 1, "head sums launch", s);
+    };
     const int64_t across = cdiv(d->hidden, l.grad_width);
     for (int64_t first = 0; first < d->vocab; first += l.piece) {
         g.cols = int32_t(d->vocab - first < l.piece ? d->vocab - first : l.piece);
@@ -787,29 +816,10 @@ int nest_head_loss_backward(const nest_head_desc *d, const void *hidden, const v
         p.out[1] = out[1] ? out[1] + first * d->hidden : nullptr;
         const int64_t tiles = (cdiv(d->tokens, kTile) * p.splits[0] + cdiv(p.cols, kTile) * p.splits[1]) * across;
         if ((rc = c.multiply(kGrads, grads, p, tiles))) return rc;
+        // before the next piece's take their place
+        if ((rc = sums(false, pieces && g.sums[1] && out[1], g.cols, p.out[1]))) return rc;
     }
-    if (!g.sums[0] && !g.sums[1]) return NEST_OK;
-    SumArgs s = {};
-    s.live = g.live;
-    s.rows = g.rows;
-    s.cols = g.depth;
-    s.by = g.by;
-    const int64_t wide = cdiv(d->hidden, kSumCols);
-    const int64_t blocks[2] = {g.sums[0] && out[0] ? cdiv(d->tokens, kSumTile) * wide : 0,
-                               g.sums[1] && out[1] ? cdiv(d->vocab, kSumTile) * wide : 0};
-    if (!blocks[0] && !blocks[1]) return NEST_OK;
-    s.piece_rows = int32_t(d->vocab);
-    s.first_block = int32_t(blocks[0]);
-    for (int i = 0; i < 2; i++) {
-        s.splits[i] = g.splits[i];
-        s.sums[i] = g.sums[i];
-        s.pitch[i] = g.sums_pitch[i];
-        s.out[i] = out[i];
-    }
-    const dim3 grid(unsigned(blocks[0] + blocks[1]));
-    return d->dtype == NEST_BF16
-               ? launch_kernel(sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, 1, "head sums launch", s)
-               : launch_kernel(sum_kernel<__half>, grid, dim3(256), 0, stream, 1, "head sums launch", s);
+    return sums(g.sums[0] && out[0], g.sums[1] && out[1] && !pieces, d->vocab, out[1]);
 }
 
 }  // extern "C"

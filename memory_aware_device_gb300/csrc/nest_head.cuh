@@ -161,7 +161,7 @@ __device__ __forceinline__ uint64_t nanoseconds() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-constexpr uint64_t kPatience = 2000000000;   // a tile takes well under a millisecond
+constexpr uint64_t kPatience = 2000000000;   // a tile, of 2048 stages at most, takes under a millisecond
 
 // Waits for the barrier's phase; false when it did not come in `patience` nanoseconds.  A role whose wait gave
 // up waits for nothing more, and the results that it did not see are NaN.

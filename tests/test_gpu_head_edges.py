@@ -228,3 +228,27 @@ def test_listed_columns_of_share_zero_add_nothing(T):
     assert torch.equal(r.losses, s.losses) and torch.equal(r.loss, s.loss) and torch.equal(r.lse, s.lse)
     p, q = backward(x, r, dl), backward(y, s, dl)
     assert torch.equal(p[0][:, :-1], q[0][:, :-1]) and torch.equal(p[1], q[1])
+
+
+@pytest.mark.parametrize("T,V,D", [(2 ** 21, 8300, 8), (2 ** 18 + 77, 24, 64)])
+def test_long_sums_over_tokens(T, V, D):
+    """All terms of the weights' gradient have one sign in columns that are no label, so that what each addition
+    cuts off adds up.  Bound: half a step of 2^-10 for dz and for the result, and of a sum that grows evenly in
+    parts of at most 2^17 tokens a step of 2^-23 of half the part for every 16 tokens."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    hidden = (1 + torch.rand(T, D, generator=g, device="cuda")).half()
+    weight = (torch.rand(V, D, generator=g, device="cuda") * 0.01).half()
+    labels = torch.randint(1, V - 1, (T,), generator=g, device="cuda")
+    r = head.cross_entropy(hidden, weight, labels)
+    dl = torch.tensor(1000.0, device="cuda")
+    dw = head.cross_entropy_backward(hidden, weight, labels, r, dl, needs=(False, True))[1]
+    assert torch.equal(dw, head.cross_entropy_backward(hidden, weight, labels, r, dl)[1])
+    want, w = torch.zeros(2, D, dtype=torch.float64, device="cuda"), weight.double()
+    for a in range(0, T, 2 ** 16):
+        h = hidden[a:a + 2 ** 16].double()
+        z = h @ w.T
+        want += torch.exp(z[:, [0, V - 1]] - torch.logsumexp(z, 1)[:, None]).T @ h
+    want *= 1000 / T
+    bound = 2 * 2.0 ** -11 + min(T, 2 ** 17) / 16 * 2.0 ** -24 + 2.0 ** -16
+    got = ((dw[[0, V - 1]].double() - want).abs() / want).max()
+    assert got <= bound, (float(got), bound)
