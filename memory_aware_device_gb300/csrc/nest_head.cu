@@ -394,8 +394,8 @@ int least_of(int64_t hidden) { return hidden % 8 == 0 ? 4 : 16; }
 // Parts of the summed index of the two gradients: one, unless there are fewer tiles than pairs of blocks or one
 // product's tiles are longer than an even share of all work.  A part is at least 24 stages: writing and reading
 // its 256 KB of sums takes as long (1000 x 5000 x 300: 21.0 us with both kernels, 23.0 with 16).  And at most 2048
-// (131072 tokens or columns): what the tensor cores' additions cut off, 0.26 to 0.30 * 2^-24 of the sum per 16 products
-// in the mean (over_heat), is then up to 1.5e-4 of it, below the half step of 2^-11 or 2^-8 to which it is rounded.
+// (131072 tokens or columns): what the tensor cores' additions cut off, 0.26 to 0.46 * 2^-24 of the sum per 16 products
+// in the mean (over_heat), is then up to 2.3e-4 of it, below the half step of 2^-11 or 2^-8 to which it is rounded.
 void split(int64_t tokens, int64_t cols, int64_t hidden, int width, bool pieces, int32_t (&splits)[2]) {
     constexpr int64_t kPart = 24, kLongest = 2048;
     const int64_t across = cdiv(hidden, width), row_tiles[2] = {cdiv(tokens, kTile), cdiv(cols, kTile)};
@@ -424,10 +424,12 @@ int width_of(int64_t tokens, int64_t cols, int64_t hidden, int step) {
     return best;
 }
 
-// 1 / h for logits as the tensor cores sum them.  Each step of 16 products cuts a sum in 32 bits off towards zero;
-// with partial sums that grow evenly that takes 0.26 * 2^-24 of the sum per step in the mean, in half precision
-// 0.30 (measured for 64 to 16384 terms, sums that grow straight and at random), which is given back: the root
-// of the mean square of the error falls from 3.0e-5 to 5.6e-6 for logits of 7 over 4096 terms in bfloat16.
+// 1 / h for logits as the tensor cores sum them.  Each step of 16 products cuts a sum in 32 bits off towards zero, which
+// takes 0.26 * 2^-24 of a sum like a model's logits (products of either sign, 64 to 16384 terms) per step in the
+// mean, in half precision 0.30 (measured), and is given back: the root of the mean square of the error falls from 3.0e-5
+// to 5.6e-6 for logits of 7 over 4096 terms in bfloat16, that of the losses of 2048 x 32000 x 4096 from 1.2e-6
+// to 1.3e-7 of them (32-bit products: 1.2e-7).  Products of one sign lose more (0.46 over 1024 terms), and a sum that
+// loses nothing is off by the factor, 4e-6 of itself over 4096 terms: as far as the others are without it.
 float over_heat(const nest_head_desc *d) {
     const double per = d->dtype == NEST_F16 ? 0.30 : 0.26;
     return float((1.0 + per * double(cdiv(d->hidden, 16)) / 16777216.0) / double(d->temperature));

@@ -252,3 +252,47 @@ def test_long_sums_over_tokens(T, V, D):
     bound = 2 * 2.0 ** -11 + min(T, 2 ** 17) / 16 * 2.0 ** -24 + 2.0 ** -16
     got = ((dw[[0, V - 1]].double() - want).abs() / want).max()
     assert got <= bound, (float(got), bound)
+
+
+@pytest.mark.parametrize("dtype,per", [("bf16", 0.26), ("fp16", 0.30)])
+@pytest.mark.parametrize("D", [64, 4096, 16384])
+def test_logits_whose_sums_lose_nothing(D, dtype, per):
+    """Rows of one number, and short rows padded with zeros: their logits are exact on the tensor cores, and get the
+    factor of all logits, per * D / 16 steps of 2^-24."""
+    T, V = 64, 40
+    g = torch.Generator(device="cuda").manual_seed(D)
+    kind = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    for width in (1, 8):
+        hidden, weight = torch.zeros(T, D, device="cuda"), torch.zeros(V, D, device="cuda")
+        at = torch.randint(0, D // 8, (1,), generator=g, device="cuda").item() * 8
+        hidden[:, at:at + width] = torch.randint(-8, 9, (T, width), generator=g, device="cuda").float()
+        weight[:, at:at + width] = torch.randint(-4, 5, (V, width), generator=g, device="cuda").float()
+        x = {"hidden": hidden.to(kind), "weight": weight.to(kind),
+             "labels": torch.randint(0, V, (T,), generator=g, device="cuda")}
+        r, z = forward(x), hidden.double() @ weight.double().T
+        lse, size = torch.logsumexp(z, 1), z.abs().amax(1)
+        given = per * (D // 16) * 2.0 ** -24
+        picked = z.gather(1, x["labels"][:, None])[:, 0]
+        # the exponentials and the logarithm within 2^-19, the last operations within 2^-22 of their terms
+        off = 2.0 ** -19 + 2.0 ** -22 * size
+        near(r.lse, lse, size * given * 1.01 + off, "lse")
+        near(r.losses, lse - picked, 2 * size * given * 1.01 + off, "losses")
+
+
+@pytest.mark.parametrize("dtype,per", [("bf16", 0.26), ("fp16", 0.30)])
+@pytest.mark.parametrize("D", [1024, 4096])
+@pytest.mark.parametrize("signs", ["one", "both"])
+def test_the_factor_of_logits_brings_dense_sums_nearer(D, dtype, per, signs):
+    """One column, whose logit lse is: nearer to the sum, by the root of the mean square, than without the factor."""
+    g = torch.Generator(device="cuda").manual_seed(D + 1)
+    kind = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    if signs == "one":
+        hidden, weight = (torch.rand(n, D, generator=g, device="cuda") for n in (2000, 1))
+    else:   # rows that lean towards the column, as those of a model which has learnt its labels
+        weight = torch.randn(1, D, generator=g, device="cuda") * 2 * D ** -0.5
+        hidden = torch.randn(2000, D, generator=g, device="cuda") + 2 * weight * torch.rand(2000, 1, generator=g, device="cuda")
+    x = {"hidden": hidden.to(kind), "weight": weight.to(kind), "labels": torch.zeros(2000, dtype=torch.int64, device="cuda")}
+    z = (x["hidden"].double() @ x["weight"].double().T)[:, 0]
+    got = forward(x).lse.double()
+    with_, without = got - z, got / (1 + per * (D // 16) * 2.0 ** -24) - z
+    assert float(with_.square().mean()) < float(without.square().mean())
