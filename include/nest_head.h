@@ -99,6 +99,12 @@ int nest_head_loss_backward(const nest_head_desc *desc, const void *hidden, cons
                             const float *grad_losses, void *grad_hidden, void *grad_weight, void *workspace,
                             size_t ws_bytes, void *stream);
 
+/* Warps of these calls' kernels on the current device whose wait for a copy or a product gave
+ * up after 2 s, since the library was loaded: 0 unless the GPU failed or stood still.  What they did not see is
+ * NaN in the results, which NaN in the inputs would give too; the count tells the two apart.
+ * Unlike the calls above it waits for the work that is on the stream, and cannot be captured. */
+int nest_head_waits_given_up(int64_t *count, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

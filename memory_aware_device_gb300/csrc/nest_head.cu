@@ -683,6 +683,15 @@ size_t nest_head_backward_workspace_size(const nest_head_desc *d, const void *we
     return check(d) ? 0 : layout_of(d, weight, true).total;
 }
 
+int nest_head_waits_given_up(int64_t *count, void *stream) {
+    if (!count) return NEST_E_INVALID;
+    int64_t n[2] = {};
+    int rc = gave_up_bf16(&n[0], stream);
+    if (!rc) rc = gave_up_f16(&n[1], stream);
+    if (!rc) *count = n[0] + n[1];
+    return rc;
+}
+
 int nest_head_loss(const nest_head_desc *d, const void *hidden, const void *weight, const void *index,
                    const void *teacher, const uint8_t *mask, float *loss, float *losses, float *lse, int32_t *live,
                    void *workspace, size_t ws_bytes, void *stream) {

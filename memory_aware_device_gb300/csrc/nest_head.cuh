@@ -163,8 +163,11 @@ __device__ __forceinline__ uint64_t nanoseconds() {
 }
 constexpr uint64_t kPatience = 2000000000;   // a tile, of 2048 stages at most, takes under a millisecond
 
+// Warps whose wait gave up, since the library was loaded, in the kernels of this type.
+template <typename T> __device__ unsigned long long gave_up = 0;
+
 // Waits for the barrier's phase; false when it did not come in `patience` nanoseconds.  A role whose wait gave
-// up waits for nothing more, and the results that it did not see are NaN.
+// up waits for nothing more, and the results that it did not see are NaN; it is counted in gave_up.
 inline __device__ __noinline__ bool barrier_wait_long(uint32_t address, uint32_t parity, uint64_t patience) {
     const uint64_t start = nanoseconds();
     for (;;) {
@@ -720,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             else if (t.kind == 0) loads(std::integral_constant<int, 0>{});
             else loads(std::integral_constant<int, 1>{});
         }
+        if (!ok && lane == 0) atomicAdd(&gave_up<T>, 1ull);
         if (!ok) {   // copies under way end within microseconds: those of the stages that are still open
             for (int i = 0; i < a.stages && half == 0; i++)
                 barrier_wait_long(shared_address(&sh.full[i]), i < s ? phase : phase ^ 1, 1000000);
@@ -765,6 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
         }
         if (!ok) {
+            if (lane == 0) atomicAdd(&gave_up<T>, 1ull);
             if (one_lane()) commit(&sh.drain);
             __syncwarp();
             barrier_wait(&sh.drain, 0);
@@ -980,6 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (t.steps) use++;
         }
         if (lane == 0) stores_done();
+        if (!ok && lane == 0) atomicAdd(&gave_up<T>, 1ull);
         if (P == kLoss && a.join_here) {
             // Few tokens: the last block joins what all blocks left, which saves a launch (32 tokens x 32000
             // columns: 55 KB; for more, one block reads longer than a launch takes).
@@ -1008,6 +1014,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 // The products' launchers, one translation unit for each type.
 int launch_gemm_bf16(Product p, const Maps &maps, const GemmArgs &args, int pairs, void *stream);
 int launch_gemm_f16(Product p, const Maps &maps, const GemmArgs &args, int pairs, void *stream);
+// gave_up of this type on the current device, behind the work of the stream, which is waited for.
+int gave_up_bf16(int64_t *count, void *stream);
+int gave_up_f16(int64_t *count, void *stream);
+
+template <typename T> int read_gave_up(int64_t *count, void *stream) {
+    unsigned long long n = 0;
+    const auto s = static_cast<cudaStream_t>(stream);
+    int rc = cuda_status(cudaMemcpyFromSymbolAsync(&n, gave_up<T>, sizeof(n), 0, cudaMemcpyDeviceToHost, s), "waits given up");
+    if (!rc) rc = cuda_status(cudaStreamSynchronize(s), "waits given up");
+    *count = int64_t(n);
+    return rc;
+}
 
 template <typename T>
 int launch_gemm(Product p, const Maps &maps, const GemmArgs &args, int pairs, void *stream) {

@@ -28,7 +28,7 @@ MAX_K = 256
 
 # Every function declared in include/nest_head.h.
 EXPORTS = ("nest_head_loss_workspace_size", "nest_head_backward_workspace_size", "nest_head_loss",
-           "nest_head_loss_backward")
+           "nest_head_loss_backward", "nest_head_waits_given_up")
 
 
 class HeadDesc(C.Structure):
@@ -50,6 +50,7 @@ def lib():
             f.argtypes, f.restype = [P(HeadDesc), V], C.c_size_t
         L.nest_head_loss.argtypes = [P(HeadDesc)] + [V] * 10 + [C.c_size_t, V]
         L.nest_head_loss_backward.argtypes = [P(HeadDesc)] + [V] * 11 + [C.c_size_t, V]
+        L.nest_head_waits_given_up.argtypes = [P(C.c_int64), V]
         _lib = L
     return _lib
 
@@ -270,6 +271,24 @@ def distill_backward(hidden, weight, ids, teacher, result: HeadLoss, grad_loss=N
     temperature and mask as in the forward call."""
     return _backward(_Inputs(hidden, weight, ids, teacher, mask, temperature), result, grad_loss, grad_losses, out,
                      stream, needs)
+
+
+def waits_given_up(device="cuda", stream=None) -> int:
+    """nest_head_waits_given_up: how many warps of these calls on the device gave up waiting (and left NaN) since the
+    library was loaded, 0 unless the GPU failed or stood still.  Waits for the work of the stream; not under capture."""
+    torch = train._torch or train._load_torch()
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    guard, count = _enter(device, stream), C.c_int64()
+    try:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the count is read on the host: not under capture")
+        _check(lib().nest_head_waits_given_up(C.byref(count), train._raw_stream(device.index)), "nest_head_waits_given_up")
+    finally:
+        if guard is not None:
+            guard.leave()
+    return count.value
 
 
 def _functions():

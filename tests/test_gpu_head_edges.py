@@ -296,3 +296,21 @@ def test_the_factor_of_logits_brings_dense_sums_nearer(D, dtype, per, signs):
     got = forward(x).lse.double()
     with_, without = got - z, got / (1 + per * (D // 16) * 2.0 ** -24) - z
     assert float(with_.square().mean()) < float(without.square().mean())
+
+
+def test_no_wait_gives_up():
+    """NaN of the inputs is told from that of a wait that gave up."""
+    x, dl = made(600, 3000, 128, "bf16"), torch.ones((), device="cuda")
+    x["hidden"][5] = float("nan")
+    for dtype in ("bf16", "fp16"):
+        y = x | {n: x[n].to({"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]) for n in ("hidden", "weight")}
+        r = forward(y)
+        assert torch.isnan(r.loss) and torch.isnan(backward(y, r, dl)[1]).any()
+    assert head.waits_given_up() == 0 and head.waits_given_up(x["hidden"].device, torch.cuda.Stream()) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = forward(x)
+        with pytest.raises(RuntimeError, match="capture"):
+            head.waits_given_up()
+    graph.replay()
+    assert head.waits_given_up() == 0 and torch.isnan(r.loss)

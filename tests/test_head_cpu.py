@@ -167,3 +167,9 @@ def test_results_that_touch_an_input(strides):
     with pytest.raises(ValueError, match="b shares memory"):
         head._apart((room[:10], room[9:12]), ("a", "b"), ())
     head._apart((room[:10], room[10:12]), ("a", "b"), ())
+
+
+def test_the_count_of_waits_refuses():
+    assert head.lib().nest_head_waits_given_up(None, None) == nest.NEST_E_INVALID
+    with pytest.raises(ValueError, match="CUDA"):
+        head.waits_given_up("cpu")
