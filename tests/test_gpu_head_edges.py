@@ -314,3 +314,29 @@ def test_no_wait_gives_up():
             head.waits_given_up()
     graph.replay()
     assert head.waits_given_up() == 0 and torch.isnan(r.loss)
+
+
+def test_the_gradient_of_a_broadcast_row_against_64_bits():
+    """One hidden state for all tokens: autograd adds the rows' gradients in 32 bits and rounds once."""
+    x = made(60, 200, 64, "bf16", k=6, temperature=2.0)
+    x["ids"][:] = x["ids"][:1]                   # the rows' gradients point one way
+    one = x["hidden"][:1].clone().requires_grad_()
+    head.teacher_loss(one.expand(60, 64), x["weight"], x["ids"], x["teacher"], temperature=2.0).loss.backward()
+    want = ref.loss(x | {"hidden": x["hidden"][:1].expand(60, 64)}, torch.ones((), device="cuda"))
+    rows, sums = want["dh"], want["dh"].sum(0)
+    off = want["dh_off"].sum(0) + 60 * 2.0 ** -23 * rows.abs().sum(0)
+    off = off + 2.0 ** -9 * (sums.abs() + off)
+    assert float(sums.abs().max()) > 8 * float(off.max())
+    near(one.grad[0], sums, off, "gradient of the broadcast row")
+
+
+@pytest.mark.parametrize("T,V,D,k", [(2 ** 24, 2, 1, 0), (2 ** 22, 5, 3, 2), (3, 2 ** 24, 8, 0), (2, 2 ** 24 - 1, 3, 4),
+                                     (5, 40, 2 ** 16, 0), (300, 7, 2 ** 16 - 1, 5)])
+def test_the_largest_sizes(T, V, D, k):
+    x, dl = made(T, V, D, "bf16", k=k, dead=0.1), torch.ones((), device="cuda")
+    r = forward(x)
+    dh, dw = backward(x, r, dl)
+    want = ref.loss(x, dl)
+    assert int(r.tokens[0]) == want["tokens"]
+    for name, got in (("losses", r.losses), ("lse", r.lse), ("loss", r.loss), ("dh", dh), ("dw", dw)):
+        near(got, want[name], want[name + "_off"], name)
