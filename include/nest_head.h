@@ -7,7 +7,8 @@
  * tokens * vocabulary numbers, against tokens * hidden of a layer's output.  These entry
  * points compute two losses of those logits, and the gradients of hidden states and
  * weights, without keeping them: the logits are made in tiles and reduced where they are
- * made, and made again, a piece of the vocabulary at a time, for the gradients.
+ * made, and made again for the gradients, whose workspace holds the losses' derivatives in 16
+ * bits of a piece of the vocabulary (up to 256 MiB, or 8192 columns; tokens rounded up to 256).
  *
  * Conventions are those of nest_train.h: the caller allocates every buffer, a call only
  * checks its arguments and enqueues kernels on the caller's stream, and the same inputs

@@ -610,7 +610,7 @@ __device__ __forceinline__ void write_rows(const unsigned char *staging, uint16_
 // Bound by the tensor cores at large hidden sizes: 2048 x 32000 x 4096 in bf16 takes 267 us for the loss (2.0
 // PFLOP/s), 278 for dz and 533 for both gradients, with the tensor pipe 97, 93 and 97 % active.  Tiles of 256 x
 // 256 need 64 KB of operands a stage, 16 TB/s over all pairs, which L2 gives; with six stages on their way the
-// products do not wait.  At hidden size 64 the epilogue bounds: 4096 x 128000 takes 190 us, 1.8 us a tile.  For few
+// products do not wait.  At hidden size 64 the epilogue bounds: 4096 x 128000 takes 187 us, 1.8 us a tile.  For few
 // tokens memory does: 1 x 32000 x 4096 reads 262 MB in 45 us.
 template <Product P, typename T>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)

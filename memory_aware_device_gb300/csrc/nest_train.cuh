@@ -1,4 +1,4 @@
-// Shared by the training-step operators (nest_route.cu, nest_optim.cu).
+// Shared by the training-step operators (nest_route.cu, nest_optim.cu) and the output head's losses (nest_head.cu).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -173,3 +173,14 @@ def test_the_count_of_waits_refuses():
     assert head.lib().nest_head_waits_given_up(None, None) == nest.NEST_E_INVALID
     with pytest.raises(ValueError, match="CUDA"):
         head.waits_given_up("cpu")
+
+
+@pytest.mark.parametrize("T,V,D,k,loss,backward", [(1, 32000, 4096, 0, 2.5, 31.1), (64, 128000, 1024, 0, 2.1, 76.5),
+                                                   (1777, 50021, 1000, 0, 8.4, 197.8), (2048, 32000, 4096, 0, 20.9, 147.9),
+                                                   (2048, 32000, 4096, 64, 21.9, 148.9), (4096, 128000, 4096, 0, 58.2, 362.9),
+                                                   (16384, 128000, 512, 0, 115.2, 319.0)])
+def test_workspace_of_a_planner(T, V, D, k, loss, backward):
+    """What a step at the head needs beside its inputs and results, in MB as it is documented."""
+    L, d = head.lib(), desc(tokens=T, vocab=V, hidden=D, hidden_row=D, weight_row=D, k=k)
+    assert round(L.nest_head_loss_workspace_size(C.byref(d), FAKE) / 1e6, 1) == loss
+    assert round(L.nest_head_backward_workspace_size(C.byref(d), FAKE) / 1e6, 1) == backward
