@@ -50,8 +50,8 @@ extern "C" {
  * that are not live have losses and lse 0, and whatever their hidden states hold (NaN
  * included) reaches no result.  NaN in a live token's row gives it a NaN loss.  A logit of
  * minus infinity adds nothing to lse; as a target's it makes the loss infinite, and a row that
- * is nothing else has lse minus infinity and a NaN loss.  (Logits whose z log2(e) / h is
- * beyond 32 bits give results that are not finite.)                                      */
+ * is nothing else has lse minus infinity and a NaN loss.  (Where z log2(e) / h of a row's
+ * largest logit is beyond 32 bits, its results are not finite.)                          */
 #define NEST_I32 0
 #define NEST_I64 1
 
@@ -101,9 +101,10 @@ int nest_head_loss_backward(const nest_head_desc *desc, const void *hidden, cons
                             size_t ws_bytes, void *stream);
 
 /* Warps of these calls' kernels on the current device whose wait for a copy or a product gave
- * up after 2 s, since the library was loaded: 0 unless the GPU failed or stood still.  What they did not see is
- * NaN in the results, which NaN in the inputs would give too; the count tells the two apart.
- * Unlike the calls above it waits for the work that is on the stream, and cannot be captured. */
+ * up after 2 s, since the library was loaded: 0 unless the GPU failed or stood still.  What
+ * they did not see is NaN in the results, which NaN in the inputs would give too; the count
+ * tells the two apart.  Unlike the calls above it waits for the work that is on the stream,
+ * and cannot be captured. */
 int nest_head_waits_given_up(int64_t *count, void *stream);
 
 #ifdef __cplusplus
